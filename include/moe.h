@@ -59,6 +59,8 @@ enum { MOE_BF16 = 0, MOE_F32 = 1, MOE_FP8_E4M3 = 2 };
 enum { MOE_EPI_NONE = 0, MOE_EPI_SWIGLU = 1 };
 /* Scale formats of FP8 tensors: float32 scales, or E8M0 codes (uint8, value 2^(code-127)). */
 enum { MOE_SCALE_F32 = 0, MOE_SCALE_E8M0 = 1 };
+/* Norms of the layer's input rows: with the mean subtracted, or by the root mean square alone. */
+enum { MOE_NORM_LAYER = 0, MOE_NORM_RMS = 1 };
 
 /* Human-readable name of a status code (static string). */
 const char* moe_status_str(moe_status s);
@@ -418,6 +420,136 @@ moe_status moe_segment_transpose_fp8(const uint16_t* src, int64_t ld_src, const 
 moe_status moe_router_wgrad(const uint16_t* x, const int32_t* sorted_token,
                             const int32_t* expert_offsets, const float* du_row, int n_experts,
                             int d, float* dw_router, hipStream_t stream);
+
+/* ====================================================================================
+ * Norm of the rows that enter the layer, and activation checkpoints in 8 bits.
+ *
+ * Checkpoint format ("DeepSeek-V3 Technical Report", "FP8 混合精度訓練", 低精度ストレージ・通信:
+ * activations kept for the backward pass in low precision): E4M3 codes u8 [rows, cols] and one
+ * E8M0 scale code per 1x128 tile, u8 [rows, ceil(cols / 128)] (the last tile of a row may be
+ * short), scale = 2^(code - 127) the least 2^k with max |v| <= 448 * 2^k, k in [-127, 127], 0 for
+ * a tile of zeros: the rule of fp8_quant_1x128_e8m0.  The value of a code is E4M3(code) * scale,
+ * exact in bf16 (2^128, to which f32 values from 248 * 2^120 on round, is infinite there and in
+ * f32).  In a tile with infinities they saturate (a code of 448 at the largest scale an
+ * f32 needs, whose value is again infinite) and NaN keeps a NaN code; NaN does not enter the scale.
+ *
+ * In this section rows may have any width and start at any element (pointers and leading
+ * dimensions need only the alignment of one element) unless a call says otherwise; outputs must
+ * not overlap inputs.
+ * ==================================================================================== */
+
+/* moe_norm -- y = xhat * weight + bias, xhat = (x - mean) * rstd, per row, in fp32:
+ *   mean = sum(x) / d (MOE_NORM_LAYER) or 0 (MOE_NORM_RMS),
+ *   rstd = 1 / sqrt(sum((x - mean)^2) / d + eps).
+ *   x       device bf16 or f32 [rows, d], leading dimension ldx
+ *   weight, bias  device [d], both bf16 or f32 per w_dtype; NULL: all ones / all zeros
+ *   y       device bf16 (RNE) or f32 [rows, d] out, leading dimension ldy
+ *   mean, rstd  device f32 [rows] out, each optional (NULL)
+ *   ck_q, ck_scale  NULL, or the 8-bit checkpoint of xhat out: u8 [rows, d], u8 [rows, ceil(d/128)]
+ * Limits: rows >= 0; 1 <= d <= 16384; 0 <= eps, finite; ldx, ldy >= d. */
+moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const void* weight, const void* bias,
+                    int w_dtype, int rows, int d, float eps, int kind, void* y, int y_dtype,
+                    int64_t ldy, float* mean, float* rstd, uint8_t* ck_q, uint8_t* ck_scale,
+                    hipStream_t stream);
+
+/* moe_norm_backward -- with g = dy * weight:
+ *   dx = rstd * (g - sum(g)/d [layer norm only] - xhat * sum(g * xhat)/d),
+ *   dweight = sum over rows of dy * xhat,  dbias = sum over rows of dy   (fp32, fixed order)
+ * xhat comes from x, mean and rstd, or (x = NULL) from the checkpoint that moe_norm wrote.
+ *   dy      device bf16 or f32 [rows, d], leading dimension lddy
+ *   x       device bf16 or f32 [rows, d], leading dimension ldx, or NULL
+ *   ck_q, ck_scale  the checkpoint (contiguous), or NULL
+ *   mean    device f32 [rows] (needed for the layer norm from x), rstd device f32 [rows]
+ *   weight  device [d] per w_dtype, or NULL (ones)
+ *   dx      device bf16 or f32 [rows, d] out, leading dimension lddx
+ *   dweight, dbias  device f32 [d] out (overwritten; zeros when rows == 0), each optional
+ *   ws      device workspace of moe_norm_backward_workspace_size(rows, d) bytes, 16-byte aligned
+ *           (needed for dweight or dbias); need not be initialised
+ * Limits: those of moe_norm. */
+size_t moe_norm_backward_workspace_size(int rows, int d);
+moe_status moe_norm_backward(const void* dy, int dy_dtype, int64_t lddy, const void* x, int x_dtype,
+                             int64_t ldx, const uint8_t* ck_q, const uint8_t* ck_scale,
+                             const float* mean, const float* rstd, const void* weight, int w_dtype,
+                             int rows, int d, int kind, void* dx, int dx_dtype, int64_t lddx,
+                             float* dweight, float* dbias, void* ws, size_t ws_bytes,
+                             hipStream_t stream);
+
+/* fp8_ckpt_pack -- x (device bf16 or f32 [rows, cols], leading dimension ldx) -> its checkpoint.
+ * Limits: rows >= 0; 1 <= cols <= 2^24; ldx >= cols. */
+moe_status fp8_ckpt_pack(const void* x, int x_dtype, int64_t rows, int cols, int64_t ldx,
+                         uint8_t* q, uint8_t* scale, hipStream_t stream);
+
+/* fp8_ckpt_unpack -- a checkpoint's values v, or v * weight + bias (device [cols] per w_dtype, each
+ * optional: the norm's output from the checkpoint of its xhat), as bf16 (RNE) or f32 [rows, cols],
+ * leading dimension ldo. */
+moe_status fp8_ckpt_unpack(const uint8_t* q, const uint8_t* scale, int64_t rows, int cols,
+                           const void* weight, const void* bias, int w_dtype, void* out,
+                           int out_dtype, int64_t ldo, hipStream_t stream);
+
+/* moe_swiglu_backward_ckpt -- moe_swiglu_backward with a | c from a checkpoint of [rows, 2*inter],
+ * which also recomputes the product itself:
+ *   h       device bf16 [rows, inter] out = RNE(silu(a) c), or NULL
+ * Other arguments and limits as moe_swiglu_backward; pointers 16-byte aligned. */
+moe_status moe_swiglu_backward_ckpt(const uint8_t* ac_q, const uint8_t* ac_scale, const float* dh,
+                                    int64_t rows, int inter, uint16_t* dac, uint8_t* dac_q,
+                                    float* dac_scale, uint16_t* h, hipStream_t stream);
+
+/* moe_combine_backward_ckpt -- moe_combine_backward with the routed expert outputs from a
+ * checkpoint of [T*top_k, d].  Other arguments and limits as there. */
+moe_status moe_combine_backward_ckpt(const uint16_t* d_out, const uint8_t* y_q, const uint8_t* y_scale,
+                                     const int32_t* topk_idx, const float* topk_gate,
+                                     const float* scores, const int32_t* pair_pos, int T, int top_k,
+                                     int d, int n_experts, uint16_t* dy, float* du, float* du_row,
+                                     uint8_t* dy_q, float* dy_scale, hipStream_t stream);
+
+/* ====================================================================================
+ * Experts with 4-bit weights, for batches of few tokens (decode), where the bytes of the active
+ * experts' weights set the time.
+ *
+ * Format: E2M1 codes, two to a byte (column 2j in the low nibble of byte j), u8 [n_mats, n, k/2],
+ * and one E8M0 scale code per 32 consecutive columns of a row, u8 [n_mats, n, k/32]:
+ * weight = E2M1(code) * 2^(scale - 127) (a scale code of 255 is NaN).  E2M1: a sign bit and
+ * 0, 0.5, 1, 1.5, 2, 3, 4, 6.
+ * ==================================================================================== */
+
+/* w4_quant -- one-time weight preparation: scale = the least 2^k with max |w| <= 6 * 2^k of the 32
+ * weights (k in [-127, 126]; 0 for a group of zeros), codes = RNE(w / 2^k) (exact product, ties to
+ * the even code).  A group that holds an infinity or NaN gets the scale code 255 (and codes 0).
+ *   w  device bf16 [n_mats, n, k];  q device u8 [n_mats, n, k/2] out;  scale device u8
+ *   [n_mats, n, k/32] out.  Limits: n_mats >= 0; n >= 1; k a positive multiple of 32. */
+moe_status w4_quant(const uint16_t* w, int n_mats, int n, int k, uint8_t* q, uint8_t* scale,
+                    hipStream_t stream);
+
+/* moe_w4_gemm -- for every sorted row r of group g (groups and rows as in moe_grouped_gemm):
+ *   out[r - off[first_group]] = epilogue(A[a_rows[r] or r] . W[g]^T)
+ * with A bf16, W 4-bit, exact bf16 x weight products and fp32 sums (K split over four waves, added
+ * in a fixed order).  SWIGLU: W[g] holds N/2 gate rows, then N/2 up rows; out = silu(a) c.  Any
+ * number of rows per group is right; it is made for the few of a decode batch (moe_grouped_gemm's
+ * bf16 or E4M3 weights suit the many rows of a training batch). */
+typedef struct {
+  const void* a;                /* device bf16 rows, leading dimension lda (elements) */
+  const int32_t* a_rows;        /* device i32: row of A of each sorted row, or NULL: A row r */
+  int64_t lda;
+  const uint8_t* w_q;           /* device codes [G, N, K/2] */
+  const uint8_t* w_scale;       /* device scale codes [G, N, K/32] */
+  const int32_t* group_offsets; /* device i32, at least first_group + n_groups + 1 entries, non-decreasing */
+  int first_group;
+  int n_groups;                 /* 1..1024 */
+  int64_t m_total;              /* rows covered by the groups, an upper bound */
+  int N;                        /* weight rows of each group (2*I for SWIGLU) */
+  int K;                        /* inputs, a positive multiple of 32 */
+  int epilogue;                 /* MOE_EPI_NONE or MOE_EPI_SWIGLU (N even) */
+  void* out;                    /* device output, leading dimension ldo (elements, >= output columns) */
+  int out_dtype;                /* MOE_BF16 (RNE) or MOE_F32 */
+  int64_t ldo;
+  int tail_groups;              /* the last tail_groups groups write f32 rows to out_tail instead, */
+  void* out_tail;               /* row r to r - off[first_group + n_groups - tail_groups]; 0: none */
+  int64_t ldo_tail;
+} moe_w4_desc;
+/* Limits: m_total in [0, 2^31); lda >= K and a multiple of 8; a and w_q 16-byte aligned; outputs
+ * aligned to their elements and not overlapping inputs; one W[g] < 2 GiB.  Rows of out past the groups' last row are
+ * left as they were. */
+moe_status moe_w4_gemm(const moe_w4_desc* desc, hipStream_t stream);
 
 #ifdef __cplusplus
 }

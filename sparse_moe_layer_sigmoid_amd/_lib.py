@@ -17,6 +17,7 @@ MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_WORKS
 MOE_BF16, MOE_F32, MOE_FP8_E4M3 = 0, 1, 2
 MOE_EPI_NONE, MOE_EPI_SWIGLU = 0, 1
 MOE_SCALE_F32, MOE_SCALE_E8M0 = 0, 1
+MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
 
 EXPORTS = (
     "moe_status_str", "moe_last_error", "moe_abi_version",
@@ -26,6 +27,9 @@ EXPORTS = (
     "moe_grouped_gemm_workspace_size", "moe_grouped_gemm", "moe_combine", "moe_bias_update",
     "moe_combine_backward", "moe_swiglu_backward", "moe_segment_transpose", "moe_segment_transpose_fp8",
     "moe_router_wgrad",
+    "moe_norm", "moe_norm_backward_workspace_size", "moe_norm_backward",
+    "fp8_ckpt_pack", "fp8_ckpt_unpack", "moe_swiglu_backward_ckpt", "moe_combine_backward_ckpt",
+    "w4_quant", "moe_w4_gemm",
 )
 
 _p = ctypes.c_void_p
@@ -43,6 +47,14 @@ class MoeGemmDesc(ctypes.Structure):
         ("out", _p), ("out_dtype", _i), ("ldo", _i64), ("out_scale", _p),
         ("tail_groups", _i), ("out_tail", _p), ("ldo_tail", _i64), ("scale_fmt", _i), ("ldw", _i64),
         ("ws", _p), ("ws_bytes", _sz), ("k_offsets", _p), ("out_preact", _p), ("ldo_preact", _i64),
+    ]
+
+
+class MoeW4Desc(ctypes.Structure):
+    _fields_ = [
+        ("a", _p), ("a_rows", _p), ("lda", _i64), ("w_q", _p), ("w_scale", _p), ("group_offsets", _p),
+        ("first_group", _i), ("n_groups", _i), ("m_total", _i64), ("N", _i), ("K", _i), ("epilogue", _i),
+        ("out", _p), ("out_dtype", _i), ("ldo", _i64), ("tail_groups", _i), ("out_tail", _p), ("ldo_tail", _i64),
     ]
 
 
@@ -107,6 +119,25 @@ def lib() -> ctypes.CDLL:
         L.moe_segment_transpose_fp8.argtypes = [_p, _i64, _p, _p, _i, _i, _i, _i, _p, _p, _p]
         L.moe_router_wgrad.restype = _i
         L.moe_router_wgrad.argtypes = [_p, _p, _p, _p, _i, _i, _p, _p]
+        L.moe_norm.restype = _i
+        L.moe_norm.argtypes = [_p, _i, _i64, _p, _p, _i, _i, _i, _f, _i, _p, _i, _i64, _p, _p, _p, _p, _p]
+        L.moe_norm_backward_workspace_size.restype = _sz
+        L.moe_norm_backward_workspace_size.argtypes = [_i, _i]
+        L.moe_norm_backward.restype = _i
+        L.moe_norm_backward.argtypes = [_p, _i, _i64, _p, _i, _i64, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _i, _i64,
+                                        _p, _p, _p, _sz, _p]
+        L.fp8_ckpt_pack.restype = _i
+        L.fp8_ckpt_pack.argtypes = [_p, _i, _i64, _i, _i64, _p, _p, _p]
+        L.fp8_ckpt_unpack.restype = _i
+        L.fp8_ckpt_unpack.argtypes = [_p, _p, _i64, _i, _p, _p, _i, _p, _i, _i64, _p]
+        L.moe_swiglu_backward_ckpt.restype = _i
+        L.moe_swiglu_backward_ckpt.argtypes = [_p, _p, _p, _i64, _i, _p, _p, _p, _p, _p]
+        L.moe_combine_backward_ckpt.restype = _i
+        L.moe_combine_backward_ckpt.argtypes = [_p, _p, _p, _p, _p, _p, _p, _i, _i, _i, _i, _p, _p, _p, _p, _p, _p]
+        L.w4_quant.restype = _i
+        L.w4_quant.argtypes = [_p, _i, _i, _i, _p, _p, _p]
+        L.moe_w4_gemm.restype = _i
+        L.moe_w4_gemm.argtypes = [ctypes.POINTER(MoeW4Desc), _p]
         _LIB = L
     return _LIB
 
@@ -455,4 +486,278 @@ def moe_router_wgrad(x, sorted_token, expert_offsets, du_row, n_experts: int, ou
     st = lib().moe_router_wgrad(_ptr(x), _ptr(sorted_token), _ptr(expert_offsets), _ptr(du_row), n_experts, d,
                                 _ptr(out), _stream(x))
     _check("moe_router_wgrad", st)
+    return out
+
+
+# ----------------------------------------------------------------------------- norm, 8-bit checkpoints, 4-bit weights
+
+
+def _same_device(dev, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on {dev}, got {t.device}")
+
+
+def _shape(t, shape, name):
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    return t
+
+
+def _launch(dev, fn: str, *args):
+    """Call `fn` with the current stream of `dev` as its last argument, on that device."""
+    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    if torch.cuda.current_device() == dev.index:
+        st = getattr(lib(), fn)(*args, stream)
+    else:
+        with torch.cuda.device(dev):
+            st = getattr(lib(), fn)(*args, stream)
+    _check(fn, st)
+
+
+_ROW_DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
+
+
+def _rows(t, name: str):
+    """A 2-D bf16 or f32 GPU tensor with contiguous rows (the row stride may exceed the width)."""
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if t.dtype not in _ROW_DT:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float32, got {t.dtype}")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be two-dimensional")
+    if t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} rows must be contiguous")
+    return t
+
+
+def _vectors(d: int, weight, bias):
+    """dtype code of the [d] weight and bias (either may be None); they share a dtype."""
+    dt = None
+    for t, name in ((weight, "weight"), (bias, "bias")):
+        if t is None:
+            continue
+        if not isinstance(t, torch.Tensor) or not t.is_cuda:
+            raise TypeError(f"{name} must be a GPU tensor")
+        if t.dtype not in _ROW_DT or (dt is not None and t.dtype != dt):
+            raise TypeError("weight and bias must both be torch.bfloat16 or both torch.float32")
+        if tuple(t.shape) != (d,) or not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous with shape ({d},)")
+        dt = t.dtype
+    return _ROW_DT[dt] if dt is not None else MOE_F32
+
+
+def _checkpoint(q, scale, name: str):
+    """The two contiguous uint8 tensors of an 8-bit checkpoint -> (rows, cols)."""
+    _dev(q, torch.uint8, f"{name} codes")
+    _dev(scale, torch.uint8, f"{name} scales")
+    if q.dim() != 2:
+        raise ValueError(f"{name} codes must be two-dimensional")
+    rows, cols = q.shape
+    _shape(scale, (rows, (cols + 127) // 128), f"{name} scales")
+    return rows, cols
+
+
+def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, rms: bool = False, out_dtype=None, want_stats: bool = False,
+             checkpoint: bool = False):
+    """Layer norm (rms=True: root mean square norm) of the rows of x [T, d] (bf16 or f32):
+    (y [T, d], mean [T]|None, rstd [T]|None, checkpoint|None).  weight / bias [d], bf16 or f32,
+    optional.  want_stats gives what moe_norm_backward takes (mean only for the layer norm);
+    checkpoint=True also packs the normalised rows in 8 bits, (codes u8 [T, d], scale codes u8
+    [T, ceil(d/128)]), from which the backward runs without x (it implies rstd)."""
+    _rows(x, "x")
+    T, d = x.shape
+    dev = x.device
+    wdt = _vectors(d, weight, bias)
+    _same_device(dev, weight=weight, bias=bias)
+    odt = x.dtype if out_dtype is None else out_dtype
+    if odt not in _ROW_DT:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {odt}")
+    y = torch.empty((T, d), dtype=odt, device=dev)
+    mean = torch.empty(T, dtype=torch.float32, device=dev) if want_stats and not rms else None
+    rstd = torch.empty(T, dtype=torch.float32, device=dev) if want_stats or checkpoint else None
+    q = torch.empty((T, d), dtype=torch.uint8, device=dev) if checkpoint else None
+    s = torch.empty((T, (d + 127) // 128), dtype=torch.uint8, device=dev) if checkpoint else None
+    _launch(dev, "moe_norm", _ptr(x), _ROW_DT[x.dtype], x.stride(0), _ptr(weight), _ptr(bias), wdt, T, d, float(eps),
+            MOE_NORM_RMS if rms else MOE_NORM_LAYER, _ptr(y), _ROW_DT[odt], d, _ptr(mean), _ptr(rstd), _ptr(q), _ptr(s))
+    return y, mean, rstd, ((q, s) if checkpoint else None)
+
+
+def moe_norm_backward(dy, x, mean, rstd, weight=None, rms: bool = False, checkpoint=None, want_dweight: bool = True,
+                      want_dbias: bool = False, out_dtype=None):
+    """Gradients of moe_norm: (dx [T, d], dweight f32 [d]|None, dbias f32 [d]|None).  dy [T, d] bf16
+    or f32; x as in the forward with its mean and rstd (mean None for rms), or x=None and the
+    forward's checkpoint with rstd.  dx has out_dtype (default: dy's dtype)."""
+    _rows(dy, "dy")
+    T, d = dy.shape
+    dev = dy.device
+    wdt = _vectors(d, weight, None)
+    _dev(rstd, torch.float32, "rstd")
+    _shape(rstd, (T,), "rstd")
+    if (x is None) == (checkpoint is None):
+        raise ValueError("give either x or the checkpoint")
+    q = s = None
+    if checkpoint is not None:
+        q, s = checkpoint
+        _checkpoint(q, s, "checkpoint")
+        _shape(q, (T, d), "checkpoint codes")
+        mean = None
+    else:
+        _shape(_rows(x, "x"), (T, d), "x")
+        if rms:
+            mean = None
+        else:
+            if mean is None:
+                raise ValueError("the layer norm's backward from x needs mean")
+            _dev(mean, torch.float32, "mean")
+            _shape(mean, (T,), "mean")
+    _same_device(dev, x=x, mean=mean, rstd=rstd, weight=weight, codes=q, scales=s)
+    odt = dy.dtype if out_dtype is None else out_dtype
+    if odt not in _ROW_DT:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {odt}")
+    dx = torch.empty((T, d), dtype=odt, device=dev)
+    dw = torch.empty(d, dtype=torch.float32, device=dev) if want_dweight else None
+    db = torch.empty(d, dtype=torch.float32, device=dev) if want_dbias else None
+    wsb = lib().moe_norm_backward_workspace_size(T, d) if want_dweight or want_dbias else 0
+    ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
+    _launch(dev, "moe_norm_backward", _ptr(dy), _ROW_DT[dy.dtype], dy.stride(0), _ptr(x),
+            _ROW_DT[x.dtype] if x is not None else MOE_BF16, x.stride(0) if x is not None else d, _ptr(q), _ptr(s),
+            _ptr(mean), _ptr(rstd), _ptr(weight), wdt, T, d, MOE_NORM_RMS if rms else MOE_NORM_LAYER, _ptr(dx),
+            _ROW_DT[odt], d, _ptr(dw), _ptr(db), _ptr(ws), wsb)
+    return dx, dw, db
+
+
+def fp8_ckpt_pack(x):
+    """x [rows, cols] bf16 or f32 (row stride may exceed cols) -> its 8-bit checkpoint (codes u8
+    [rows, cols], E8M0 scale codes u8 [rows, ceil(cols/128)])."""
+    _rows(x, "x")
+    rows, cols = x.shape
+    q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
+    s = torch.empty((rows, (cols + 127) // 128), dtype=torch.uint8, device=x.device)
+    _launch(x.device, "fp8_ckpt_pack", _ptr(x), _ROW_DT[x.dtype], rows, cols, x.stride(0), _ptr(q), _ptr(s))
+    return q, s
+
+
+def fp8_ckpt_unpack(q, scale, weight=None, bias=None, out_dtype=torch.bfloat16):
+    """The values of an 8-bit checkpoint (times weight [cols], plus bias [cols], where given) as bf16
+    or f32 [rows, cols]."""
+    rows, cols = _checkpoint(q, scale, "checkpoint")
+    wdt = _vectors(cols, weight, bias)
+    _same_device(q.device, scales=scale, weight=weight, bias=bias)
+    if out_dtype not in _ROW_DT:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    out = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
+    _launch(q.device, "fp8_ckpt_unpack", _ptr(q), _ptr(scale), rows, cols, _ptr(weight), _ptr(bias), wdt, _ptr(out),
+            _ROW_DT[out_dtype], cols)
+    return out
+
+
+def moe_swiglu_backward_ckpt(ac_q, ac_scale, dh, want_h: bool = True, fp8: bool = False):
+    """moe_swiglu_backward with a | c [rows, 2I] from its 8-bit checkpoint, dh f32 [rows, I]: (dac bf16
+    [rows, 2I], h bf16 [rows, I]|None); with fp8=True (dac, dac_q u8 [rows, 2I], dac_scale f32
+    [rows, 2I/128], h)."""
+    rows, c2 = _checkpoint(ac_q, ac_scale, "a | c")
+    _dev(dh, torch.float32, "dh")
+    if c2 % 2:
+        raise ValueError("a | c needs an even number of columns")
+    I = c2 // 2
+    _shape(dh, (rows, I), "dh")
+    dev = dh.device
+    _same_device(dev, codes=ac_q, scales=ac_scale)
+    dac = torch.empty((rows, c2), dtype=torch.bfloat16, device=dev)
+    h = torch.empty((rows, I), dtype=torch.bfloat16, device=dev) if want_h else None
+    dq = ds = None
+    if fp8:
+        dq = torch.empty((rows, c2), dtype=torch.uint8, device=dev)
+        ds = torch.empty((rows, c2 // 128), dtype=torch.float32, device=dev)
+    _launch(dev, "moe_swiglu_backward_ckpt", _ptr(ac_q), _ptr(ac_scale), _ptr(dh), rows, I, _ptr(dac), _ptr(dq), _ptr(ds),
+            _ptr(h))
+    return (dac, dq, ds, h) if fp8 else (dac, h)
+
+
+def moe_combine_backward_ckpt(d_out, y_q, y_scale, topk_idx, topk_gate, scores, pair_pos, fp8: bool = False):
+    """moe_combine_backward with the routed expert outputs [T*K, d] from their 8-bit checkpoint."""
+    _dev(d_out, torch.bfloat16, "d_out")
+    _dev(topk_idx, torch.int32, "topk_idx")
+    _dev(topk_gate, torch.float32, "topk_gate")
+    _dev(scores, torch.float32, "scores")
+    _dev(pair_pos, torch.int32, "pair_pos")
+    T, K = topk_idx.shape
+    d = d_out.shape[1]
+    _checkpoint(y_q, y_scale, "y")
+    _shape(d_out, (T, d), "d_out")
+    _shape(y_q, (T * K, d), "y codes")
+    _shape(topk_gate, (T, K), "topk_gate")
+    _shape(pair_pos, (T, K), "pair_pos")
+    if scores.dim() != 2 or scores.shape[0] != T:
+        raise ValueError("scores must be [T, n_experts]")
+    dev = d_out.device
+    _same_device(dev, codes=y_q, scales=y_scale, topk_idx=topk_idx, topk_gate=topk_gate, scores=scores, pair_pos=pair_pos)
+    dy = torch.empty((T * (K + 1), d), dtype=torch.bfloat16, device=dev)
+    du = torch.empty((T, K), dtype=torch.float32, device=dev)
+    du_row = torch.empty(T * K, dtype=torch.float32, device=dev)
+    dyq = dys = None
+    if fp8:
+        dyq = torch.empty((T * (K + 1), d), dtype=torch.uint8, device=dev)
+        dys = torch.empty((T * (K + 1), d // 128), dtype=torch.float32, device=dev)
+    _launch(dev, "moe_combine_backward_ckpt", _ptr(d_out), _ptr(y_q), _ptr(y_scale), _ptr(topk_idx), _ptr(topk_gate),
+            _ptr(scores), _ptr(pair_pos), T, K, d, scores.shape[1], _ptr(dy), _ptr(du), _ptr(du_row), _ptr(dyq), _ptr(dys))
+    return (dy, du, du_row, dyq, dys) if fp8 else (dy, du, du_row)
+
+
+def w4_quant(w):
+    """w [n_mats, n, k] (or [n, k]) bf16 -> 4-bit weights (codes u8 [n_mats, n, k/2], scale codes u8
+    [n_mats, n, k/32])."""
+    _dev(w, torch.bfloat16, "w")
+    if w.dim() not in (2, 3):
+        raise ValueError("w must be [n, k] or [n_mats, n, k]")
+    k = w.shape[-1]
+    q = torch.empty((*w.shape[:-1], k // 2), dtype=torch.uint8, device=w.device)
+    s = torch.empty((*w.shape[:-1], k // 32), dtype=torch.uint8, device=w.device)
+    mats = w.shape[0] if w.dim() == 3 else 1
+    _launch(w.device, "w4_quant", _ptr(w), mats, w.shape[-2], k, _ptr(q), _ptr(s))
+    return q, s
+
+
+def moe_w4_gemm(a, w_q, w_scale, group_offsets, first_group: int, n_groups: int, m_total: int, out, a_rows=None,
+                swiglu: bool = False, out_tail=None, tail_groups: int = 0):
+    """moe_grouped_gemm with bf16 rows a [*, K] and 4-bit weights (w4_quant's codes [G, N, K/2] and scale
+    codes [G, N, K/32]): out[r - off[first_group]] = epilogue(a[a_rows[r] or r] . W[g]^T), out bf16 or f32;
+    the last tail_groups groups write f32 rows to out_tail instead."""
+    if not isinstance(a, torch.Tensor) or not a.is_cuda or a.dtype != torch.bfloat16:
+        raise TypeError("a must be a bfloat16 GPU tensor")
+    _dev(w_q, torch.uint8, "w_q")
+    _dev(w_scale, torch.uint8, "w_scale")
+    _dev(group_offsets, torch.int32, "group_offsets")
+    _rows(out, "out")
+    if w_q.dim() != 3 or a.dim() != 2:
+        raise ValueError("w_q must be [G, N, K/2] and a two-dimensional")
+    G, N, K = w_q.shape[0], w_q.shape[1], 2 * w_q.shape[2]
+    _shape(w_scale, (G, N, K // 32), "w_scale")
+    if a.shape[1] != K or (K > 1 and a.stride(1) != 1):
+        raise ValueError(f"a must have contiguous rows of {K} elements")
+    if first_group < 0 or n_groups < 1 or first_group + n_groups > G:
+        raise ValueError(f"groups [{first_group}, {first_group + n_groups}) are not among the {G} weights")
+    if group_offsets.numel() < first_group + n_groups + 1:
+        raise ValueError("group_offsets needs first_group + n_groups + 1 entries")
+    cols = N // 2 if swiglu else N
+    if out.shape[1] != cols:
+        raise ValueError(f"out must have {cols} columns, got {out.shape[1]}")
+    if a_rows is not None:
+        _dev(a_rows, torch.int32, "a_rows")
+    if tail_groups:
+        _rows(out_tail, "out_tail")
+        if out_tail.dtype != torch.float32 or out_tail.shape[1] != cols:
+            raise ValueError(f"out_tail must be float32 with {cols} columns")
+    dev = a.device
+    _same_device(dev, w_q=w_q, w_scale=w_scale, group_offsets=group_offsets, out=out, a_rows=a_rows,
+                 out_tail=out_tail if tail_groups else None)
+    lead = lambda t: t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])  # noqa: E731
+    desc = MoeW4Desc(
+        a=a.data_ptr(), a_rows=a_rows.data_ptr() if a_rows is not None else None, lda=lead(a) if a.shape[0] > 1 else K,
+        w_q=w_q.data_ptr(), w_scale=w_scale.data_ptr(), group_offsets=group_offsets.data_ptr(), first_group=first_group,
+        n_groups=n_groups, m_total=m_total, N=N, K=K, epilogue=MOE_EPI_SWIGLU if swiglu else MOE_EPI_NONE,
+        out=out.data_ptr(), out_dtype=_ROW_DT[out.dtype], ldo=lead(out), tail_groups=tail_groups,
+        out_tail=out_tail.data_ptr() if tail_groups else None, ldo_tail=lead(out_tail) if tail_groups else 0)
+    _launch(dev, "moe_w4_gemm", ctypes.byref(desc))
     return out

@@ -1,0 +1,483 @@
+// moe_norm / moe_norm_backward: layer norm (or root mean square norm) of the rows that enter the
+// layer, and its gradients.
+//
+//   mean = (1/d) sum_i x_i          (0 for the root mean square form)
+//   rstd = (1/d sum_i (x_i - mean)^2 + eps)^(-1/2),   xhat = (x - mean) rstd,   y = xhat w + b
+//   g = dy w;  dx = rstd (g - m1 - xhat m2),  m1 = (1/d) sum g (0 without the mean),
+//   m2 = (1/d) sum g xhat;  dw = sum_rows dy xhat,  db = sum_rows dy
+//
+// Everything between the loads and the final rounding is fp32.  Both kernels are bound by HBM:
+// each element is read once and written once.
+//
+//  * Forward: one workgroup holds a row in registers (chunks of 8 elements per lane), so the
+//    variance is summed over x - mean in a second pass over registers, not from squares that
+//    cancel.  With a checkpoint the normalised row is also stored as E4M3 with power-of-two 1x128
+//    scales: 16 lanes are a tile, so its maximum is four lane exchanges.
+//  * Backward: a workgroup owns all columns and walks rows b, b + grid, ...; each lane keeps dw
+//    and db of its columns in registers over all its rows, and the next row's loads are issued
+//    before the current row's two sums are exchanged.  The workgroups' partial dw / db rows go to
+//    the workspace and a second kernel adds them in workgroup order, so the result does not
+//    depend on timing.
+#include "abi_common.h"
+#include "device_common.h"
+#include "rows_common.h"
+
+namespace moe {
+namespace {
+
+constexpr int kMaxNormD = 16384;  // 1024 lanes x 2 chunks of 8
+
+enum { SRC_BF16 = ROW_BF16, SRC_F32 = ROW_F32, SRC_CKPT = 2 };
+
+// Sums v over the workgroup, the same value in every lane; `red` holds one float per wave.  The
+// caller alternates between two arrays, so one barrier per sum is enough.
+__device__ __forceinline__ float block_sum(float v, float* red, int nwaves) {
+  v = wave_sum(v);
+  if (nwaves == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  float s = 0.f;
+  for (int w = 0; w < nwaves; ++w) s += red[w];
+  return s;
+}
+
+struct NormArgs {
+  const void* x;
+  int64_t ldx_b;  // bytes
+  const void* w;
+  const void* b;
+  int w_dtype;
+  int d;
+  float eps;
+  int rms;
+  void* y;
+  int y_dtype;
+  int64_t ldy_b;
+  float* mean;
+  float* rstd;
+  uint8_t* q;
+  uint8_t* q_scale;
+  int tiles;  // scales per row: ceil(d / 128)
+};
+
+template <int XT, int NV, bool FULL>
+__global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
+  __shared__ float red[2][16];
+  const int64_t r = blockIdx.x;
+  const int t = threadIdx.x, G = blockDim.x, nw = G >> 6;
+  const char* xr = static_cast<const char*>(p.x) + r * p.ldx_b;
+  float f[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (t + i * G) * 8;
+    if (c < p.d) {
+      values8(load8<XT, FULL>(xr, c, p.d), f[i]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
+    }
+  }
+  const float inv_d = 1.0f / (float)p.d;
+  float mean = 0.f;
+  if (!p.rms) {
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += f[i][e];
+    mean = block_sum(s, red[0], nw) * inv_d;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (t + i * G) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) f[i][e] = c + e < p.d ? f[i][e] - mean : 0.f;
+    }
+  }
+  // the squares are summed times 2^-k >= 1/d > 2^-k-1 (exact products), so the sum overflows only
+  // where the mean of the squares nearly does
+  const int k = 31 - __clz(p.d);
+  const float down = pow2f(-k);
+  float ss = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(f[i][e] * down, f[i][e], ss);
+  const float rstd = 1.0f / sqrtf(block_sum(ss, red[1], nw) * (inv_d * pow2f(k)) + p.eps);
+  if (t == 0) {
+    if (p.mean) p.mean[r] = mean;
+    if (p.rstd) p.rstd[r] = rstd;
+  }
+  char* yr = static_cast<char*>(p.y) + r * p.ldy_b;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int ch = t + i * G, c = ch * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) f[i][e] *= rstd;
+    if (p.q) {  // a whole 16-lane tile shares this test, and lanes past the row hold zeros
+      uint32_t code;
+      const u32x2 q = ckpt_encode8(f[i], code);
+      if (c < p.d) {
+        store_codes8<FULL>(p.q + r * p.d, c, p.d, q);
+        if ((ch & 15) == 0) p.q_scale[r * p.tiles + ch / 16] = (uint8_t)code;
+      }
+    }
+    if (c < p.d) {
+      float w[8], b[8];
+      if (p.w) {
+        load8_any<FULL>(p.w_dtype, p.w, c, p.d, w);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[i][e] *= w[e];
+      }
+      if (p.b) {
+        load8_any<FULL>(p.w_dtype, p.b, c, p.d, b);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[i][e] += b[e];
+      }
+      store8_any<FULL>(p.y_dtype, yr, c, p.d, f[i]);
+    }
+  }
+}
+
+struct NormBwdArgs {
+  const void* dy;
+  int64_t lddy_b;
+  const void* x;  // rows, or the checkpoint's codes
+  int64_t ldx_b;
+  const uint8_t* q_scale;
+  int tiles;
+  const float* mean;
+  const float* rstd;
+  const void* w;
+  int w_dtype;
+  int rows;
+  int d;
+  int rms;
+  void* dx;
+  int dx_dtype;
+  int64_t lddx_b;
+  float* part_w;  // [grid][d] partial sums (or the results themselves when grid == 1), or null
+  float* part_b;
+};
+
+template <int SRC>
+struct RawX {
+  Raw8<SRC> v;
+};
+template <>
+struct RawX<SRC_CKPT> {
+  u32x2 q;
+  uint32_t s;
+};
+
+// Makes the compiler take a row's raw values as new ones here (it would keep what it computed
+// from them instead).
+__device__ __forceinline__ void keep(Raw8<ROW_BF16>& r) { asm volatile("" : "+v"(r.v)); }
+__device__ __forceinline__ void keep(Raw8<ROW_F32>& r) { asm volatile("" : "+v"(r.lo), "+v"(r.hi)); }
+__device__ __forceinline__ void keep(RawX<SRC_CKPT>& r) { asm volatile("" : "+v"(r.q), "+v"(r.s)); }
+template <int SRC>
+__device__ __forceinline__ void keep(RawX<SRC>& r) { keep(r.v); }
+
+template <int SRC, int DYT, int NV, bool FULL>
+__global__ __launch_bounds__(1024) void norm_backward_kernel(NormBwdArgs p) {
+  __shared__ float red[2][2][16];
+  const int t = threadIdx.x, G = blockDim.x, nw = G >> 6;
+  const float inv_d = 1.0f / (float)p.d;
+  float w[NV][8], aw[NV][8], ab[NV][8];
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (t + i * G) * 8;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      w[i][e] = 1.f;
+      aw[i][e] = ab[i][e] = 0.f;
+    }
+    if (p.w && c < p.d) load8_any<FULL>(p.w_dtype, p.w, c, p.d, w[i]);
+  }
+  Raw8<DYT> ndy[NV];
+  RawX<SRC> nx[NV];
+  float nmean = 0.f, nrstd = 0.f;
+  auto fetch = [&](int64_t r) __attribute__((always_inline)) {
+    const char* dyr = static_cast<const char*>(p.dy) + r * p.lddy_b;
+    const char* xr = static_cast<const char*>(p.x) + r * p.ldx_b;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int ch = t + i * G, c = ch * 8;
+      if (c < p.d) {
+        ndy[i] = load8<DYT, FULL>(dyr, c, p.d);
+        if constexpr (SRC == SRC_CKPT) {
+          nx[i].q = load_codes8<FULL>(reinterpret_cast<const uint8_t*>(xr), c, p.d);
+          nx[i].s = p.q_scale[r * p.tiles + ch / 16];
+        } else {
+          nx[i].v = load8<SRC, FULL>(xr, c, p.d);
+        }
+      }
+    }
+    nmean = p.mean ? p.mean[r] : 0.f;
+    nrstd = p.rstd[r];
+  };
+  int64_t r = blockIdx.x;
+  if (r < p.rows) fetch(r);
+  for (int it = 0; r < p.rows; r += gridDim.x, ++it) {
+    const float mean = nmean, rstd = nrstd;
+    Raw8<DYT> dy[NV];
+    RawX<SRC> x[NV];
+    float s1 = 0.f, s2 = 0.f;
+    // g = dy w and xhat of chunk i, from the row's raw values: taken twice, so that only the raw
+    // values (8 registers a chunk in bf16, 16 for g and xhat) live across the exchange of the sums
+    auto values = [&](int i, float(&g)[8], float(&xh)[8]) __attribute__((always_inline)) {
+      values8(dy[i], g);
+      if constexpr (SRC == SRC_CKPT) {
+        ckpt_decode8(x[i].q, x[i].s, xh);
+      } else {
+        values8(x[i].v, xh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) xh[e] = (xh[e] - mean) * rstd;
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (t + i * G) * 8;
+      dy[i] = ndy[i];
+      x[i] = nx[i];
+      if (c < p.d) {
+        float g[8], xh[8];
+        values(i, g, xh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          // past the row's end dy (and so g) reads as zero
+          aw[i][e] = fmaf(g[e], xh[e], aw[i][e]);
+          ab[i][e] += g[e];
+          g[e] *= w[i][e];
+          s1 += g[e];
+          s2 = fmaf(g[e], xh[e], s2);
+        }
+      }
+    }
+    if (r + gridDim.x < p.rows) fetch(r + gridDim.x);
+    s1 = wave_sum(s1);
+    s2 = wave_sum(s2);
+    if (nw > 1) {
+      float(*rd)[16] = red[it & 1];
+      if ((t & 63) == 0) {
+        rd[0][t >> 6] = s1;
+        rd[1][t >> 6] = s2;
+      }
+      __syncthreads();
+      s1 = s2 = 0.f;
+      for (int k = 0; k < nw; ++k) {
+        s1 += rd[0][k];
+        s2 += rd[1][k];
+      }
+    }
+    const float m1 = p.rms ? 0.f : s1 * inv_d, m2 = s2 * inv_d;
+    char* dxr = static_cast<char*>(p.dx) + r * p.lddx_b;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (t + i * G) * 8;
+      if (c < p.d) {
+        keep(dy[i]);
+        keep(x[i]);
+        float g[8], xh[8];
+        values(i, g, xh);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) g[e] = rstd * (g[e] * w[i][e] - m1 - xh[e] * m2);
+        store8_any<FULL>(p.dx_dtype, dxr, c, p.d, g);
+      }
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (t + i * G) * 8;
+    if (c < p.d) {
+      if (p.part_w) store8_any<FULL>(ROW_F32, p.part_w + (int64_t)blockIdx.x * p.d, c, p.d, aw[i]);
+      if (p.part_b) store8_any<FULL>(ROW_F32, p.part_b + (int64_t)blockIdx.x * p.d, c, p.d, ab[i]);
+    }
+  }
+}
+
+// out[c] = sum over the n partial rows, in a fixed order: 16 strips of rows (one per wave), then the strips.
+__global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part_w,
+                                                           const float* __restrict__ part_b, int n, int d,
+                                                           float* __restrict__ dw, float* __restrict__ db) {
+  __shared__ float red[16][64];
+  const float* part = blockIdx.y == 0 ? part_w : part_b;
+  float* out = blockIdx.y == 0 ? dw : db;
+  if (!out) return;  // the whole workgroup
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float s = 0.f;
+  if (c < d) {
+#pragma unroll 8
+    for (int r = w; r < n; r += 16) s += part[(int64_t)r * d + c];
+  }
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < d) {
+    float v = 0.f;
+#pragma unroll
+    for (int k = 0; k < 16; ++k) v += red[k][lane];
+    out[c] = v;
+  }
+}
+
+// Chunks per lane: a row in one wave while its chunks fit 4 to a lane, else 4 to a lane.
+int norm_chunks_per_lane(int d) {
+  const int chunks = (d + 7) / 8;
+  return chunks <= 64 ? 1 : chunks <= 128 ? 2 : 4;
+}
+
+int norm_bwd_chunks_per_lane(int d) { return (d + 7) / 8 <= 64 ? 1 : 2; }
+
+int group_threads(int d, int nv) {
+  const int chunks = (d + 7) / 8;
+  return ((chunks + nv - 1) / nv + 63) / 64 * 64;
+}
+
+// Workgroups of the backward kernel: two resident per CU at the largest rows, more of the small
+// ones; every one writes a partial row of dw and db, so no more than that.
+int norm_bwd_grid(int rows, int d) {
+  const int threads = group_threads(d, norm_bwd_chunks_per_lane(d));
+  const int per_cu = threads >= 448 ? 2 : threads >= 256 ? 4 : threads >= 128 ? 8 : 16;
+  const int n = 256 * per_cu;
+  return rows < n ? rows : n;
+}
+
+template <int SRC, int DYT>
+void launch_norm_backward(const NormBwdArgs& a, int nv, int grid, int threads, hipStream_t stream) {
+  const bool full = a.d % 8 == 0;
+  auto kernel = nv == 1 ? (full ? norm_backward_kernel<SRC, DYT, 1, true> : norm_backward_kernel<SRC, DYT, 1, false>)
+                        : (full ? norm_backward_kernel<SRC, DYT, 2, true> : norm_backward_kernel<SRC, DYT, 2, false>);
+  kernel<<<grid, threads, 0, stream>>>(a);
+}
+
+template <int XT, bool FULL>
+void launch_norm(const NormArgs& a, int rows, int nv, int threads, hipStream_t stream) {
+  auto kernel = nv == 1 ? norm_kernel<XT, 1, FULL> : nv == 2 ? norm_kernel<XT, 2, FULL> : norm_kernel<XT, 4, FULL>;
+  kernel<<<rows, threads, 0, stream>>>(a);
+}
+
+bool row_dtype(int t) { return t == MOE_BF16 || t == MOE_F32; }
+int row_esz(int t) { return t == MOE_BF16 ? 2 : 4; }
+bool elem_aligned(const void* p, int esz) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(esz - 1)) == 0; }
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const void* weight, const void* bias,
+                               int w_dtype, int rows, int d, float eps, int kind, void* y, int y_dtype, int64_t ldy,
+                               float* mean, float* rstd, uint8_t* ck_q, uint8_t* ck_scale, hipStream_t stream) {
+  using namespace moe;
+  clear_error();
+  MOE_REQUIRE(rows == 0 || (x && y), MOE_ERR_NULL, "moe_norm: a required pointer is NULL");
+  MOE_REQUIRE(!ck_q == !ck_scale, MOE_ERR_NULL, "moe_norm: ck_q and ck_scale go together");
+  MOE_REQUIRE(row_dtype(x_dtype) && row_dtype(y_dtype) && row_dtype(w_dtype), MOE_ERR_DTYPE,
+              "moe_norm: x, y and weights must be MOE_BF16 or MOE_F32 (%d, %d, %d)", x_dtype, y_dtype, w_dtype);
+  MOE_REQUIRE(kind == MOE_NORM_LAYER || kind == MOE_NORM_RMS, MOE_ERR_DTYPE, "moe_norm: unknown kind %d", kind);
+  MOE_REQUIRE(rows >= 0 && d >= 1 && d <= kMaxNormD && eps >= 0.f && eps < 1e30f, MOE_ERR_SHAPE,
+              "moe_norm: rows=%d d=%d (1..%d) eps=%g (finite, >= 0)", rows, d, kMaxNormD, (double)eps);
+  MOE_REQUIRE((ldx >= d && ldy >= d) || rows <= 1, MOE_ERR_ALIGN, "moe_norm: ldx=%lld ldy=%lld must be >= d=%d",
+              (long long)ldx, (long long)ldy, d);
+  MOE_REQUIRE(elem_aligned(x, row_esz(x_dtype)) && elem_aligned(y, row_esz(y_dtype)) &&
+                  elem_aligned(weight, row_esz(w_dtype)) && elem_aligned(bias, row_esz(w_dtype)) &&
+                  elem_aligned(mean, 4) && elem_aligned(rstd, 4),
+              MOE_ERR_ALIGN, "moe_norm: pointers must be aligned to their elements");
+  if (rows > 0) {
+    NormArgs a;
+    a.x = x;
+    a.ldx_b = ldx * row_esz(x_dtype);
+    a.w = weight;
+    a.b = bias;
+    a.w_dtype = w_dtype;
+    a.d = d;
+    a.eps = eps;
+    a.rms = kind == MOE_NORM_RMS;
+    a.y = y;
+    a.y_dtype = y_dtype;
+    a.ldy_b = ldy * row_esz(y_dtype);
+    a.mean = mean;
+    a.rstd = rstd;
+    a.q = ck_q;
+    a.q_scale = ck_scale;
+    a.tiles = (d + 127) / 128;
+    const int nv = norm_chunks_per_lane(d), threads = group_threads(d, nv);
+    const bool full = d % 8 == 0;
+    if (x_dtype == MOE_BF16) full ? launch_norm<ROW_BF16, true>(a, rows, nv, threads, stream) : launch_norm<ROW_BF16, false>(a, rows, nv, threads, stream);
+    else full ? launch_norm<ROW_F32, true>(a, rows, nv, threads, stream) : launch_norm<ROW_F32, false>(a, rows, nv, threads, stream);
+  }
+  return check_launch("moe_norm");
+}
+
+extern "C" size_t moe_norm_backward_workspace_size(int rows, int d) {
+  if (rows <= 0 || d < 1 || d > moe::kMaxNormD) return 0;
+  return (size_t)2 * moe::norm_bwd_grid(rows, d) * d * sizeof(float);
+}
+
+extern "C" moe_status moe_norm_backward(const void* dy, int dy_dtype, int64_t lddy, const void* x, int x_dtype,
+                                        int64_t ldx, const uint8_t* ck_q, const uint8_t* ck_scale, const float* mean,
+                                        const float* rstd, const void* weight, int w_dtype, int rows, int d, int kind,
+                                        void* dx, int dx_dtype, int64_t lddx, float* dweight, float* dbias, void* ws,
+                                        size_t ws_bytes, hipStream_t stream) {
+  using namespace moe;
+  clear_error();
+  MOE_REQUIRE(rows == 0 || (dy && rstd && dx), MOE_ERR_NULL, "moe_norm_backward: a required pointer is NULL");
+  MOE_REQUIRE(!ck_q == !ck_scale, MOE_ERR_NULL, "moe_norm_backward: ck_q and ck_scale go together");
+  MOE_REQUIRE(rows == 0 || !x == !!ck_q, MOE_ERR_NULL, "moe_norm_backward: either x or the checkpoint is given");
+  MOE_REQUIRE(row_dtype(dy_dtype) && row_dtype(x_dtype) && row_dtype(w_dtype) && row_dtype(dx_dtype), MOE_ERR_DTYPE,
+              "moe_norm_backward: tensors must be MOE_BF16 or MOE_F32 (%d, %d, %d, %d)", dy_dtype, x_dtype, w_dtype,
+              dx_dtype);
+  MOE_REQUIRE(kind == MOE_NORM_LAYER || kind == MOE_NORM_RMS, MOE_ERR_DTYPE, "moe_norm_backward: unknown kind %d", kind);
+  MOE_REQUIRE(rows == 0 || ck_q || kind == MOE_NORM_RMS || mean, MOE_ERR_NULL,
+              "moe_norm_backward: the layer norm's backward from x needs mean");
+  MOE_REQUIRE(rows >= 0 && d >= 1 && d <= kMaxNormD, MOE_ERR_SHAPE, "moe_norm_backward: rows=%d d=%d (1..%d)", rows, d,
+              kMaxNormD);
+  MOE_REQUIRE((lddy >= d && lddx >= d && (ck_q || ldx >= d)) || rows <= 1, MOE_ERR_ALIGN,
+              "moe_norm_backward: lddy=%lld ldx=%lld lddx=%lld must be >= d=%d", (long long)lddy, (long long)ldx,
+              (long long)lddx, d);
+  MOE_REQUIRE(elem_aligned(dy, row_esz(dy_dtype)) && elem_aligned(x, row_esz(x_dtype)) &&
+                  elem_aligned(dx, row_esz(dx_dtype)) && elem_aligned(weight, row_esz(w_dtype)) &&
+                  elem_aligned(mean, 4) && elem_aligned(rstd, 4) && elem_aligned(dweight, 4) && elem_aligned(dbias, 4),
+              MOE_ERR_ALIGN, "moe_norm_backward: pointers must be aligned to their elements");
+  const size_t need = moe_norm_backward_workspace_size(rows, d);
+  MOE_REQUIRE(!(dweight || dbias) || (ws && ws_bytes >= need && aligned16(ws)) || rows == 0, MOE_ERR_WORKSPACE,
+              "moe_norm_backward: workspace %zu < %zu bytes (or NULL / unaligned)", ws_bytes, need);
+  int grid = 0;
+  float* pw = static_cast<float*>(ws);
+  float* pb = nullptr;
+  if (rows > 0) {
+    grid = norm_bwd_grid(rows, d);
+    pb = pw + (size_t)grid * d;
+    NormBwdArgs a;
+    a.dy = dy;
+    a.lddy_b = lddy * row_esz(dy_dtype);
+    a.x = ck_q ? static_cast<const void*>(ck_q) : x;
+    a.ldx_b = ck_q ? (int64_t)d : ldx * row_esz(x_dtype);
+    a.q_scale = ck_scale;
+    a.tiles = (d + 127) / 128;
+    a.mean = ck_q || kind == MOE_NORM_RMS ? nullptr : mean;
+    a.rstd = rstd;
+    a.w = weight;
+    a.w_dtype = w_dtype;
+    a.rows = rows;
+    a.d = d;
+    a.rms = kind == MOE_NORM_RMS;
+    a.dx = dx;
+    a.dx_dtype = dx_dtype;
+    a.lddx_b = lddx * row_esz(dx_dtype);
+    a.part_w = dweight ? (grid == 1 ? dweight : pw) : nullptr;
+    a.part_b = dbias ? (grid == 1 ? dbias : pb) : nullptr;
+    const int nv = norm_bwd_chunks_per_lane(d), threads = group_threads(d, nv);
+    if (ck_q) {
+      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_CKPT, ROW_BF16>(a, nv, grid, threads, stream);
+      else launch_norm_backward<SRC_CKPT, ROW_F32>(a, nv, grid, threads, stream);
+    } else if (x_dtype == MOE_BF16) {
+      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_BF16, ROW_BF16>(a, nv, grid, threads, stream);
+      else launch_norm_backward<SRC_BF16, ROW_F32>(a, nv, grid, threads, stream);
+    } else {
+      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_F32, ROW_BF16>(a, nv, grid, threads, stream);
+      else launch_norm_backward<SRC_F32, ROW_F32>(a, nv, grid, threads, stream);
+    }
+  }
+  if (grid != 1 && (dweight || dbias))  // with no rows the sums are zero
+    norm_reduce_kernel<<<dim3((d + 63) / 64, dbias ? 2 : 1), 1024, 0, stream>>>(pw, pb, grid, d, dweight, dbias);
+  return check_launch("moe_norm_backward");
+}

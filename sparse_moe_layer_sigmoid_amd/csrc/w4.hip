@@ -1,0 +1,369 @@
+// w4_quant / moe_w4_gemm: the experts' products with 4-bit weights, for batches of few tokens.
+//
+// A weight is an E2M1 code (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives; two codes a byte, the
+// even column in the low nibble) times a power of two shared by 32 consecutive inputs of its row
+// (an E8M0 code): 4.25 bits.  With few rows per expert the products are bound by the bytes of the
+// active experts' weights, so a 4-bit weight is worth 3.8 bf16 ones and nothing else matters much.
+//
+// Design:
+//  * Matrix cores with the weights as the first operand (16 weight rows x 32 inputs against 16
+//    token rows): a lane's 16-byte load is 32 inputs of one weight row, exactly one scale group,
+//    and four K steps of the MFMA; the K order is the same on the token side, so nothing is
+//    shuffled.  gfx950 converts two codes and applies the group's power of two in one instruction
+//    (exact in bf16), so scales cost nothing and every product accumulates in fp32.
+//  * A workgroup owns 16 * NT weight rows (SwiGLU: half gate, half matching up rows) against up to
+//    32 token rows of one expert; its four waves split K in turns of 128 inputs, so together they
+//    read 256 contiguous bytes of each row, and add up through LDS in wave order (deterministic).
+//    Each wave keeps a ring of weight loads in flight; the token rows come from L2.
+//  * Work items (expert, column block, row block) come from the device-side offsets, as in
+//    moe_grouped_gemm: only experts that hold rows are read.
+#include <type_traits>
+
+#include "abi_common.h"
+#include "device_common.h"
+#include "rows_common.h"
+
+namespace moe {
+namespace {
+
+typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+
+constexpr int kMaxGroups = 1024;
+constexpr int kGroup = 32;      // inputs per scale
+constexpr int kRowBlock = 32;   // token rows of a work item
+constexpr int kWaves = 4;
+
+// E2M1 code of |v| rounded to nearest, ties to the even code, saturating at 6.
+__device__ __forceinline__ uint32_t e2m1_code(float v) {
+  const float a = fabsf(v);
+  uint32_t c = (a > 0.25f) + (a >= 0.75f) + (a > 1.25f) + (a >= 1.75f) + (a > 2.5f) + (a >= 3.5f) + (a > 5.0f);
+  return c | ((__float_as_uint(v) >> 28) & 8u);
+}
+
+// One lane per 8 inputs, 4 lanes per scale group.
+__global__ __launch_bounds__(256) void w4_quant_kernel(const uint16_t* __restrict__ w, int64_t n8,
+                                                       uint8_t* __restrict__ q, uint8_t* __restrict__ scale) {
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= n8) return;  // n8 is a multiple of 4: whole groups leave together
+  float f[8];
+  unpack_bf16x8(*(const u32x4*)(w + i * 8), f);
+  uint32_t top = 0;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) top = max(top, __float_as_uint(f[e]) & 0x7fffffffu);
+  top = max(top, (uint32_t)__shfl_xor((int)top, 1, kWave));
+  top = max(top, (uint32_t)__shfl_xor((int)top, 2, kWave));
+  // the least 2^k with amax <= 6 * 2^k = 1.5 * 2^(k + 2); 0 for a group of zeros
+  const int e = (int)(top >> 23) - 127;
+  int k = e - 2 + ((top & 0x7fffffu) > 0x400000u ? 1 : 0);
+  k = top == 0 ? 0 : top < 0x00800000u ? -127 : max(-127, k);
+  const bool bad = top >= 0x7f800000u;  // an infinity or NaN: E2M1 holds neither, the scale says NaN
+  const float inv = pow2f(-(bad ? 0 : k));
+  uint32_t o = 0;
+#pragma unroll
+  for (int j = 0; j < 8; ++j) o |= e2m1_code(bad ? 0.f : f[j] * inv) << (4 * j);
+  *(uint32_t*)(q + i * 4) = o;
+  if ((i & 3) == 0) scale[i / 4] = bad ? 255 : (uint8_t)(k + 127);
+}
+
+struct W4Args {
+  const uint8_t* a;  // bf16 token rows
+  const int32_t* a_rows;
+  int64_t lda_b;
+  const uint8_t* q;
+  const uint8_t* s;
+  const int32_t* offs;  // group_offsets + first_group
+  int first_group;
+  int n_groups;
+  int N;  // weight rows per group
+  int K;
+  int n_tiles;
+  int out_cols;
+  uint8_t* out;
+  int out_dtype;
+  int64_t ldo_b;
+  int tail_first;  // first group (relative) of the f32 tail output; n_groups if none
+  uint8_t* out_tail;
+  int64_t ldo_tail_b;
+};
+
+__device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+
+// 8 codes -> 8 bf16 weights (code * scale, exact unless it overflows).
+__device__ __forceinline__ bf16x8_t decode_w4(uint32_t q, float scale) {
+  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0);
+  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1);
+  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2);
+  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3);
+  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
+}
+
+template <bool SWIGLU, int NT>
+__global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
+  constexpr int BN = NT * 16;                   // weight rows per item
+  constexpr int OC = SWIGLU ? BN / 2 : BN;      // output columns per item
+  __shared__ int s_pre[kMaxGroups + 1];         // row blocks before each group
+  __shared__ int s_wsum[kWaves];
+  __shared__ __attribute__((aligned(16))) float s_red[kWaves][16][BN + 4];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int lr = lane & 15, lg = lane >> 4;
+
+  // prefix of the groups' row blocks, four consecutive groups per lane
+  {
+    int c[4], sum = 0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int g = tid * 4 + j;
+      const int len = g < p.n_groups ? p.offs[g + 1] - p.offs[g] : 0;
+      c[j] = (max(len, 0) + kRowBlock - 1) / kRowBlock;
+      sum += c[j];
+    }
+    int incl = sum;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+      const int v = __shfl_up(incl, o, kWave);
+      if (lane >= o) incl += v;
+    }
+    if (lane == 63) s_wsum[wave] = incl;
+    __syncthreads();
+    int base = incl - sum;
+    for (int w = 0; w < wave; ++w) base += s_wsum[w];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (tid * 4 + j <= kMaxGroups) s_pre[tid * 4 + j] = base;
+      base += c[j];
+    }
+    if (tid == 255) s_pre[kMaxGroups] = base;
+    __syncthreads();
+  }
+  const int64_t total = (int64_t)s_pre[kMaxGroups] * p.n_tiles;
+  const int base_row = p.offs[0];
+  const int kblocks = (p.K + 127) / 128;
+  const uint32_t w_row_b = p.K / 2, s_row_b = p.K / kGroup;
+
+  for (int64_t L = blockIdx.x; L < total; L += gridDim.x) {
+    // the group: the last one whose items start at or before L
+    int lo = 0, hi = p.n_groups;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if ((int64_t)s_pre[mid] * p.n_tiles <= L) lo = mid;
+      else hi = mid;
+    }
+    const int g = lo;
+    const int blocks = s_pre[g + 1] - s_pre[g];
+    const int local = (int)(L - (int64_t)s_pre[g] * p.n_tiles);
+    const int nt = local / blocks, rb = local - nt * blocks;
+    const int row0 = p.offs[g] + rb * kRowBlock;
+    const int rows = min(kRowBlock, p.offs[g + 1] - row0);
+
+    // weight rows of this lane (past N: the last one again, not stored)
+    const int half = p.N / 2;
+    const uint8_t* wq = p.q + (int64_t)(p.first_group + g) * p.N * w_row_b;  // uniform; offsets fit 32 bits
+    const uint8_t* ws = p.s + (int64_t)(p.first_group + g) * p.N * s_row_b;
+    uint32_t oq[NT], os[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      int r;
+      if constexpr (SWIGLU) {
+        const int c = min(nt * OC + (n % (NT / 2)) * 16 + lr, half - 1);
+        r = n < NT / 2 ? c : half + c;
+      } else {
+        r = min(nt * OC + n * 16 + lr, p.N - 1);
+      }
+      oq[n] = (uint32_t)r * w_row_b + lg * 16;
+      os[n] = (uint32_t)r * s_row_b + lg;
+    }
+
+    auto run = [&](auto mt_c) __attribute__((always_inline)) {
+      constexpr int MT = decltype(mt_c)::value;
+      constexpr int kRing = MT == 1 ? 4 : 3;  // weight loads in flight per wave and weight tile
+      const uint8_t* xr[MT];
+      bool live[MT];
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        live[m] = m * 16 + lr < rows;
+        const int r = row0 + (live[m] ? m * 16 + lr : 0);
+        const int64_t ar = p.a_rows ? p.a_rows[r] : r;
+        xr[m] = p.a + ar * p.lda_b + lg * 64;
+      }
+      f32x4 acc[NT][MT];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) acc[n][m] = f32x4{0.f, 0.f, 0.f, 0.f};
+      u32x4 q[kRing][NT];
+      uint32_t sc[kRing][NT];
+      auto fetch = [&](int slot, int kb) __attribute__((always_inline)) {
+        const bool ok = kb * 128 + lg * 32 < p.K;  // K is a multiple of 32: a lane's inputs are all in or all out
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          q[slot][n] = u32x4{0u, 0u, 0u, 0u};
+          sc[slot][n] = 127;
+          if (ok) {
+            q[slot][n] = *(const u32x4*)(wq + (oq[n] + (uint32_t)kb * 64u));
+            sc[slot][n] = ws[os[n] + (uint32_t)kb * 4u];
+          }
+        }
+      };
+#pragma unroll
+      for (int d = 0; d < kRing; ++d) fetch(d, wave + d * kWaves);
+      for (int kb0 = wave; kb0 < kblocks; kb0 += kRing * kWaves) {
+#pragma unroll
+        for (int d = 0; d < kRing; ++d) {
+          const int kb = kb0 + d * kWaves;
+          const bool ok = kb * 128 + lg * 32 < p.K;
+          u32x4 x[MT][4];
+#pragma unroll
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              x[m][j] = u32x4{0u, 0u, 0u, 0u};
+              if (ok && live[m]) x[m][j] = *(const u32x4*)(xr[m] + (int64_t)kb * 256 + j * 16);
+            }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            const float s = __uint_as_float(sc[d][n] << 23);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const bf16x8_t w = decode_w4(q[d][n][j], s);
+#pragma unroll
+              for (int m = 0; m < MT; ++m) acc[n][m] = mfma_bf16(w, __builtin_bit_cast(bf16x8_t, x[m][j]), acc[n][m]);
+            }
+          }
+          fetch(d, kb + kRing * kWaves);
+        }
+      }
+      // add the waves' sums in wave order, 16 token rows at a time, and store
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int mrows = min(16, rows - m * 16);
+        if (mrows <= 0) break;
+        __syncthreads();
+#pragma unroll
+        for (int n = 0; n < NT; ++n) *(f32x4*)&s_red[wave][lr][n * 16 + lg * 4] = acc[n][m];
+        __syncthreads();
+        for (int i = tid; i < mrows * (OC / 4); i += 256) {
+          const int r = i / (OC / 4), c4 = (i - r * (OC / 4)) * 4;
+          f32x4 v = *(const f32x4*)&s_red[0][r][c4];
+#pragma unroll
+          for (int w = 1; w < kWaves; ++w) v += *(const f32x4*)&s_red[w][r][c4];
+          if constexpr (SWIGLU) {
+            f32x4 u = *(const f32x4*)&s_red[0][r][OC + c4];
+#pragma unroll
+            for (int w = 1; w < kWaves; ++w) u += *(const f32x4*)&s_red[w][r][OC + c4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = silu(v[e]) * u[e];
+          }
+          const int col = nt * OC + c4;
+          const int left = p.out_cols - col;
+          if (left <= 0) continue;
+          const int grow = row0 + m * 16 + r;
+          const bool tail = g >= p.tail_first;
+          uint8_t* orow = tail ? p.out_tail + (int64_t)(grow - p.offs[p.tail_first]) * p.ldo_tail_b
+                               : p.out + (int64_t)(grow - base_row) * p.ldo_b;
+          if (tail || p.out_dtype == ROW_F32) {
+            float* o = reinterpret_cast<float*>(orow) + col;
+            if (left >= 4) {
+              *reinterpret_cast<f32x4_u*>(o) = v;
+            } else {
+              for (int e = 0; e < left; ++e) o[e] = v[e];
+            }
+          } else {
+            uint16_t* o = reinterpret_cast<uint16_t*>(orow) + col;
+            const u32x2 b = {f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
+                             f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
+            if (left >= 4) {
+              *reinterpret_cast<u32x2_u*>(o) = b;
+            } else {
+              for (int e = 0; e < left; ++e) o[e] = (uint16_t)(b[e / 2] >> (16 * (e & 1)));
+            }
+          }
+        }
+      }
+    };
+    if (rows <= 16) run(std::integral_constant<int, 1>{});
+    else run(std::integral_constant<int, 2>{});
+  }
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status w4_quant(const uint16_t* w, int n_mats, int n, int k, uint8_t* q, uint8_t* scale,
+                               hipStream_t stream) {
+  using namespace moe;
+  clear_error();
+  const bool empty = n_mats == 0;
+  MOE_REQUIRE(empty || (w && q && scale), MOE_ERR_NULL, "w4_quant: a required pointer is NULL");
+  MOE_REQUIRE(n_mats >= 0 && n >= 1 && k >= kGroup && k % kGroup == 0, MOE_ERR_SHAPE,
+              "w4_quant: n_mats=%d n=%d k=%d (k a positive multiple of %d)", n_mats, n, k, kGroup);
+  MOE_REQUIRE(aligned16(w) && aligned16(q), MOE_ERR_ALIGN, "w4_quant: w and q must be 16-byte aligned");
+  const int64_t rows = (int64_t)n_mats * n;
+  MOE_REQUIRE(rows <= ((int64_t)1 << 38) / (k / 8), MOE_ERR_SHAPE, "w4_quant: too many weights");
+  const int64_t n8 = rows * (k / 8);
+  if (n8 > 0) w4_quant_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, stream>>>(w, n8, q, scale);
+  return check_launch("w4_quant");
+}
+
+extern "C" moe_status moe_w4_gemm(const moe_w4_desc* d, hipStream_t stream) {
+  using namespace moe;
+  clear_error();
+  MOE_REQUIRE(d != nullptr, MOE_ERR_NULL, "moe_w4_gemm: desc is NULL");
+  MOE_REQUIRE(d->w_q && d->w_scale && d->group_offsets && (d->m_total == 0 || (d->a && (d->out || d->tail_groups == d->n_groups))),
+              MOE_ERR_NULL, "moe_w4_gemm: a, w_q, w_scale, group_offsets and out are required");
+  MOE_REQUIRE(d->epilogue == MOE_EPI_NONE || d->epilogue == MOE_EPI_SWIGLU, MOE_ERR_DTYPE,
+              "moe_w4_gemm: unknown epilogue %d", d->epilogue);
+  MOE_REQUIRE(d->out_dtype == MOE_BF16 || d->out_dtype == MOE_F32, MOE_ERR_DTYPE,
+              "moe_w4_gemm: out_dtype must be MOE_BF16 or MOE_F32 (%d)", d->out_dtype);
+  const bool swiglu = d->epilogue == MOE_EPI_SWIGLU;
+  MOE_REQUIRE(d->n_groups >= 1 && d->n_groups <= kMaxGroups && d->first_group >= 0, MOE_ERR_SHAPE,
+              "moe_w4_gemm: n_groups=%d (1..%d) first_group=%d", d->n_groups, kMaxGroups, d->first_group);
+  MOE_REQUIRE(d->m_total >= 0 && d->m_total < ((int64_t)1 << 31), MOE_ERR_SHAPE, "moe_w4_gemm: m_total=%lld",
+              (long long)d->m_total);
+  MOE_REQUIRE(d->K >= kGroup && d->K % kGroup == 0 && d->N >= 1 && (!swiglu || d->N % 2 == 0), MOE_ERR_SHAPE,
+              "moe_w4_gemm: K=%d must be a positive multiple of %d, N=%d positive%s", d->K, kGroup, d->N,
+              swiglu ? " and even" : "");
+  MOE_REQUIRE(d->tail_groups >= 0 && d->tail_groups <= d->n_groups, MOE_ERR_SHAPE,
+              "moe_w4_gemm: tail_groups=%d must be in [0, n_groups=%d]", d->tail_groups, d->n_groups);
+  const int out_cols = swiglu ? d->N / 2 : d->N;
+  const int osz = d->out_dtype == MOE_F32 ? 4 : 2;
+  MOE_REQUIRE(d->lda >= d->K && d->lda % 8 == 0 && aligned16(d->a), MOE_ERR_ALIGN,
+              "moe_w4_gemm: lda=%lld must be >= K, a multiple of 8, and a 16-byte aligned", (long long)d->lda);
+  MOE_REQUIRE(aligned16(d->w_q), MOE_ERR_ALIGN, "moe_w4_gemm: w_q must be 16-byte aligned");
+  MOE_REQUIRE(d->ldo >= out_cols && (reinterpret_cast<uintptr_t>(d->out) & (uintptr_t)(osz - 1)) == 0, MOE_ERR_ALIGN,
+              "moe_w4_gemm: ldo=%lld must be >= %d and out aligned to its elements", (long long)d->ldo, out_cols);
+  if (d->tail_groups > 0) {
+    MOE_REQUIRE(d->m_total == 0 || d->out_tail, MOE_ERR_NULL, "moe_w4_gemm: out_tail is NULL");
+    MOE_REQUIRE(d->ldo_tail >= out_cols && (reinterpret_cast<uintptr_t>(d->out_tail) & 3u) == 0, MOE_ERR_ALIGN,
+                "moe_w4_gemm: ldo_tail=%lld must be >= %d and out_tail 4-byte aligned", (long long)d->ldo_tail, out_cols);
+  }
+  MOE_REQUIRE((int64_t)d->N * (d->K / 2) < ((int64_t)1 << 31), MOE_ERR_SHAPE, "moe_w4_gemm: one W[g] exceeds 2 GiB");
+  if (d->m_total == 0) return MOE_OK;
+  W4Args a;
+  a.a = static_cast<const uint8_t*>(d->a);
+  a.a_rows = d->a_rows;
+  a.lda_b = d->lda * 2;
+  a.q = d->w_q;
+  a.s = d->w_scale;
+  a.offs = d->group_offsets + d->first_group;
+  a.first_group = d->first_group;
+  a.n_groups = d->n_groups;
+  a.N = d->N;
+  a.K = d->K;
+  a.out_cols = out_cols;
+  a.out = static_cast<uint8_t*>(d->out);
+  a.out_dtype = d->out_dtype == MOE_F32 ? ROW_F32 : ROW_BF16;
+  a.ldo_b = d->ldo * osz;
+  a.tail_first = d->n_groups - d->tail_groups;
+  a.out_tail = static_cast<uint8_t*>(d->out_tail);
+  a.ldo_tail_b = d->ldo_tail * 4;
+  constexpr int NT = 2;
+  const int oc = swiglu ? NT * 8 : NT * 16;
+  a.n_tiles = (out_cols + oc - 1) / oc;
+  // row blocks: at most one short one per group that holds rows, and never more than rows
+  const int64_t full = d->m_total / kRowBlock + d->n_groups;
+  const int64_t items = (full < d->m_total ? full : d->m_total) * a.n_tiles;
+  const int grid = (int)(items < 256 * 5 ? items : 256 * 5);
+  if (swiglu) w4_gemm_kernel<true, NT><<<grid, 256, 0, stream>>>(a);
+  else w4_gemm_kernel<false, NT><<<grid, 256, 0, stream>>>(a);
+  return check_launch("moe_w4_gemm");
+}

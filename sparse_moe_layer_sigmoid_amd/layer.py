@@ -3,9 +3,11 @@
 Holds the (device-resident) weights and allocates the per-batch buffers; every step runs
 in libmoe's kernels:
 
-    route -> permute -> [fp8: quantise x per 1x128] -> gate/up grouped GEMM + SwiGLU
+    [norm ->] route -> permute -> [fp8: quantise x per 1x128] -> gate/up grouped GEMM + SwiGLU
           -> down grouped GEMM (routed experts to bf16 rows, the shared expert to fp32 rows)
           -> combine -> [bias update]
+
+With 4-bit weights (w4=True, for decode batches) the two GEMMs are moe_w4_gemm.
 
 Layer definition: "DeepSeek-V3 Technical Report" (wiki summary), "DeepSeekMoE と補助損失
 なしの負荷分散" (1 shared + N routed experts, top-K by sigmoid affinity + bias, gates from
@@ -21,13 +23,26 @@ from . import _lib as L
 
 class MoELayer:
     def __init__(self, w_router, W13, W2, bias, top_k: int, n_group: int = 1, topk_group: int = 1,
-                 fp8: bool = False, fp8_scales: str = "f32"):
+                 fp8: bool = False, fp8_scales: str = "f32", w4: bool = False, norm: str | None = None,
+                 norm_weight=None, norm_bias=None, norm_eps: float = 1e-6):
         """w_router [N, d] bf16; W13 [N+1, 2I, d] bf16 (rows [0,I) gate, [I,2I) up; expert N is
         the shared one); W2 [N+1, d, I] bf16; bias [N] f32.  With fp8=True the weights are
         block-quantised once (128x128, E4M3) and the layer runs the FP8 path, with f32 tile
-        scales (fp8_scales="f32") or power-of-two ones stored as E8M0 codes ("e8m0")."""
+        scales (fp8_scales="f32") or power-of-two ones stored as E8M0 codes ("e8m0").  With w4=True
+        they are quantised once to 4 bits (E2M1, a power of two per 32 inputs) and the layer runs
+        forward only.  norm="layer" or "rms" normalises the layer's input rows first (norm_weight,
+        norm_bias [d], bf16 or f32, optional): the input may then be f32 as well as bf16."""
         if fp8_scales not in ("f32", "e8m0"):
             raise ValueError(f"fp8_scales must be 'f32' or 'e8m0', got {fp8_scales!r}")
+        if norm not in (None, "layer", "rms"):
+            raise ValueError(f"norm must be None, 'layer' or 'rms', got {norm!r}")
+        if norm is None and (norm_weight is not None or norm_bias is not None):
+            raise ValueError("norm_weight and norm_bias need norm='layer' or 'rms'")
+        if fp8 and w4:
+            raise ValueError("the experts' weights are either E4M3 (fp8) or 4-bit (w4)")
+        self.w4 = w4
+        self.norm = norm
+        self.norm_weight, self.norm_bias, self.norm_eps = norm_weight, norm_bias, norm_eps
         self.w_router = w_router
         self.bias = bias
         self.N = w_router.shape[0]
@@ -44,20 +59,33 @@ class MoELayer:
             qw = L.fp8_quant_128x128_e8m0 if self.e8m0 else L.fp8_quant_128x128
             self.W13, self.W13_s = qw(W13)
             self.W2, self.W2_s = qw(W2)
+        elif w4:
+            self.W13, self.W13_s = L.w4_quant(W13)
+            self.W2, self.W2_s = L.w4_quant(W2)
         else:
             self.W13, self.W13_s = W13, None
             self.W2, self.W2_s = W2, None
 
     def forward(self, x, out_dtype=torch.bfloat16, update_bias: bool = False, gamma: float = 0.001,
-                keep: bool = False, train: bool = False):
+                keep: bool = False, train: bool = False, checkpoint: bool = False):
         """x [T, d] bf16 -> out [T, d] (bf16 or f32).  With keep=True returns (out, buffers), which
         the backward takes.  train=True (implies keep) is the training forward: the buffers then
         also hold the gate/up products a | c (f32, written by the gate/up GEMM beside h), which
-        the backward takes instead of running the gate/up GEMM again."""
+        the backward takes instead of running the gate/up GEMM again.  checkpoint=True (implies
+        train) keeps what the backward takes in 8 bits instead: the input (the normalised rows
+        where the layer has a norm), a | c and the expert outputs as E4M3 with power-of-two 1x128
+        scales, and (bf16 path) no h, which the backward forms again from a | c.  The output is the
+        same; the gradients carry the checkpoints' rounding."""
+        train = train or checkpoint
         if train:
-            if self.e8m0:
+            if self.e8m0 or self.w4:
                 raise NotImplementedError("the backward pass runs on the bf16 and the f32-scale FP8 paths")
             keep = True
+        x_in, norm_buf = x, None
+        if self.norm is not None:
+            x, mean, rstd, ck = L.moe_norm(x_in, self.norm_weight, self.norm_bias, self.norm_eps, self.norm == "rms",
+                                           torch.bfloat16, want_stats=keep, checkpoint=checkpoint)
+            norm_buf = {"x": None if checkpoint else x_in, "mean": None if checkpoint else mean, "rstd": rstd, "ckpt": ck}
         T, d = x.shape
         N, K, I = self.N, self.top_k, self.I
         dev = x.device
@@ -80,22 +108,43 @@ class MoELayer:
         else:
             xq = xs = hs = None
             h = torch.empty((rows, I), dtype=torch.bfloat16, device=dev)
-            L.moe_grouped_gemm(x, self.W13, offs, 0, N + 1, rows, h, a_rows=sorted_token, swiglu=True,
-                               out_preact=ac)
+            if self.w4:
+                L.moe_w4_gemm(x, self.W13, self.W13_s, offs, 0, N + 1, rows, h, a_rows=sorted_token, swiglu=True)
+            else:
+                L.moe_grouped_gemm(x, self.W13, offs, 0, N + 1, rows, h, a_rows=sorted_token, swiglu=True,
+                                   out_preact=ac)
+        ac_ckpt = None
+        if checkpoint:
+            ac_ckpt = L.fp8_ckpt_pack(ac)
+            ac = None
         y = torch.empty((T * K, d), dtype=torch.bfloat16, device=dev)
         ysh = torch.empty((T, d), dtype=torch.float32, device=dev)
         # one launch for all N + 1 down projections: routed rows to y (bf16), the shared
         # expert's rows (the last group) to ysh (f32)
-        L.moe_grouped_gemm(h, self.W2, offs, 0, N + 1, rows, y, a_scale=hs, w_scale=self.W2_s, out_tail=ysh,
-                           tail_groups=1)
+        if self.w4:
+            L.moe_w4_gemm(h, self.W2, self.W2_s, offs, 0, N + 1, rows, y, out_tail=ysh, tail_groups=1)
+        else:
+            L.moe_grouped_gemm(h, self.W2, offs, 0, N + 1, rows, y, a_scale=hs, w_scale=self.W2_s, out_tail=ysh,
+                               tail_groups=1)
         out = L.moe_combine(y, ysh, pair_pos, gate, out_dtype)
         if update_bias:
             L.moe_bias_update(self.bias, counts, T * K, gamma)
+        x_ckpt = y_ckpt = None
+        if checkpoint:
+            y_ckpt = L.fp8_ckpt_pack(y)
+            if not self.fp8:
+                x_ckpt = L.fp8_ckpt_pack(x) if norm_buf is None else None
+                h = None
+            elif norm_buf is not None:  # x comes back from the norm's checkpoint; else xq is it
+                xq = xs = None
+            x = y = ysh = None
         if keep:
             return out, {"x": x, "scores": scores, "topk_idx": idx, "topk_gate": gate, "expert_counts": counts,
                          "expert_offsets": offs, "expert_offsets_host": (offs_host, offs_ready),
                          "sorted_token": sorted_token, "pair_pos": pair_pos,
-                         "xq": xq, "xs": xs, "h": h, "hs": hs, "ac": ac, "y": y, "y_shared": ysh}
+                         "xq": xq, "xs": xs, "h": h, "hs": hs, "ac": ac, "y": y, "y_shared": ysh,
+                         "norm": norm_buf, "checkpoint": checkpoint, "x_ckpt": x_ckpt, "ac_ckpt": ac_ckpt,
+                         "y_ckpt": y_ckpt}
         return out
 
     # ------------------------------------------------------------------ backward (bf16 path)
@@ -105,7 +154,7 @@ class MoELayer:
         the FP8 path E4M3 with 128x128 block scales (the blocks of W^T are those of W,
         transposed, so these are the forward's codes and scales in transposed order)."""
         if getattr(self, "_WT", None) is None:
-            if self.e8m0:
+            if self.e8m0 or self.w4:
                 raise NotImplementedError("the backward pass runs on the bf16 and the f32-scale FP8 paths")
             W13, W2 = self._src if self.fp8 else (self.W13, self.W2)
             G, I2, d = W13.shape
@@ -125,9 +174,19 @@ class MoELayer:
                 self._WT = (W13T, W2T, None, None)
         return self._WT
 
+    def _checkpointed_x(self, buf):
+        """The layer's (normalised) bf16 input rows [T, d] from what forward(checkpoint=True) kept."""
+        if buf["norm"] is not None:
+            return L.fp8_ckpt_unpack(*buf["norm"]["ckpt"], self.norm_weight, self.norm_bias)
+        if self.fp8:
+            return L.fp8_dequant_1x128(buf["xq"], buf["xs"])
+        return L.fp8_ckpt_unpack(*buf["x_ckpt"])
+
     def backward(self, d_out, buf, grads=None, keep: bool = False):
         """Gradients of sum(d_out * out) for the forward that returned `buf` (keep=True):
-        dict of dx [T, d], dw_router [N, d], dw13 [N+1, 2I, d], dw2 [N+1, d, I], all f32.
+        dict of dx [T, d], dw_router [N, d], dw13 [N+1, 2I, d], dw2 [N+1, d, I], all f32; with a norm
+        also dnorm_weight, dnorm_bias [d] (None without that parameter), and dx is with respect to
+        the rows before it.  Buffers of forward(checkpoint=True) are read from their 8-bit form.
         `grads` may hold preallocated dw13 / dw2 tensors (overwritten) to reuse across steps;
         keep=True adds the intermediates (dy, du, dac, the input-gradient rows, FP8 operands).
         On the FP8 path ([TR] "FP8 混合精度訓練": Dgrad and Wgrad in E4M3) every GEMM operand is
@@ -139,11 +198,13 @@ class MoELayer:
         (dh = dy W2) -> [a | c from the forward, or the gate/up GEMM again without SwiGLU when the
         buffers lack them] -> SwiGLU backward -> Dgrad of
         the gate/up projection (dx rows) -> two combines (router term + shared rows, then the
-        routed rows) -> Wgrad per expert over transposed row segments -> router Wgrad."""
+        routed rows) -> Wgrad per expert over transposed row segments -> router Wgrad -> [norm
+        backward]."""
         W13T, W2T, W13T_s, W2T_s = self._transposed_weights()
         fp8 = self.fp8
         q1 = L.fp8_quant_1x128
-        x = buf["x"]
+        ckpt, norm_buf = buf.get("checkpoint", False), buf.get("norm")
+        x = buf["x"] if not ckpt else self._checkpointed_x(buf)
         T, d = x.shape
         N, K, I = self.N, self.top_k, self.I
         G = N + 1
@@ -157,13 +218,17 @@ class MoELayer:
         offs_ready.synchronize()
         lens = offs_host[1:] - offs_host[:-1]
         d_out = d_out.to(torch.bfloat16).contiguous()
-        cb = L.moe_combine_backward(d_out, buf["y"], buf["topk_idx"], buf["topk_gate"], buf["scores"], pp, fp8=fp8)
+        if ckpt:
+            cb = L.moe_combine_backward_ckpt(d_out, *buf["y_ckpt"], buf["topk_idx"], buf["topk_gate"], buf["scores"], pp,
+                                             fp8=fp8)
+        else:
+            cb = L.moe_combine_backward(d_out, buf["y"], buf["topk_idx"], buf["topk_gate"], buf["scores"], pp, fp8=fp8)
         dy, du, du_row = cb[:3]
         extra = {}
         dh = torch.empty((rows, I), dtype=torch.float32, device=dev)
         # a | c: cached by the forward's gate/up GEMM (the same fp32 values), else recomputed
         ac = buf.get("ac")
-        recompute = ac is None
+        recompute = ac is None and not ckpt
         if recompute:
             ac = torch.empty((rows, 2 * I), dtype=torch.float32, device=dev)
         dxr = torch.empty((T * K, d), dtype=torch.bfloat16, device=dev)
@@ -174,7 +239,10 @@ class MoELayer:
             if recompute:
                 L.moe_grouped_gemm(buf["xq"], self.W13, offs, 0, G, rows, ac, a_scale=buf["xs"], a_rows=st_,
                                    w_scale=self.W13_s)
-            dac, dacq, dacs = L.moe_swiglu_backward(ac, dh, fp8=True)
+            if ckpt:
+                dac, dacq, dacs, _ = L.moe_swiglu_backward_ckpt(*buf["ac_ckpt"], dh, want_h=False, fp8=True)
+            else:
+                dac, dacq, dacs = L.moe_swiglu_backward(ac, dh, fp8=True)
             L.moe_grouped_gemm(dacq, W13T, offs, 0, G, rows, dxr, a_scale=dacs, w_scale=W13T_s, out_tail=dxs,
                                tail_groups=1)
             extra.update(dyq=dyq, dys=dys, dacq=dacq, dacs=dacs)
@@ -182,7 +250,10 @@ class MoELayer:
             L.moe_grouped_gemm(dy, W2T, offs, 0, G, rows, dh)
             if recompute:
                 L.moe_grouped_gemm(x, self.W13, offs, 0, G, rows, ac, a_rows=st_)
-            dac = L.moe_swiglu_backward(ac, dh)
+            if ckpt:
+                dac, h = L.moe_swiglu_backward_ckpt(*buf["ac_ckpt"], dh)
+            else:
+                dac, h = L.moe_swiglu_backward(ac, dh), buf["h"]
             L.moe_grouped_gemm(dac, W13T, offs, 0, G, rows, dxr, out_tail=dxs, tail_groups=1)
         del ac, dh
         # dx = sum_k dxr[pair] + dxs + sum_k du_k e_{idx_k}: the router term and the shared rows
@@ -199,7 +270,8 @@ class MoELayer:
         kmax = max(kq, (int(lens[:N].max()) + kq - 1) // kq * kq)
         kp_s = (int(lens[N]) + kq - 1) // kq * kq
         seg_r, seg_s = offs[:N + 1], offs[N:N + 2]
-        h = L.fp8_dequant_1x128(buf["h"], buf["hs"]) if fp8 else buf["h"]
+        if fp8:
+            h = L.fp8_dequant_1x128(buf["h"], buf["hs"])
         grads = grads or {}
         dw2 = grads.get("dw2")
         dw13 = grads.get("dw13")
@@ -239,6 +311,12 @@ class MoELayer:
             dw13[N].zero_()
         dwr = L.moe_router_wgrad(x, st_, offs, du_row, N)
         res = {"dx": dx, "dw_router": dwr, "dw13": dw13, "dw2": dw2}
+        if norm_buf is not None:
+            dxn, dnw, dnb = L.moe_norm_backward(dx, norm_buf["x"], norm_buf["mean"], norm_buf["rstd"], self.norm_weight,
+                                                self.norm == "rms", norm_buf["ckpt"],
+                                                want_dweight=self.norm_weight is not None,
+                                                want_dbias=self.norm_bias is not None)
+            res.update(dx=dxn, dnorm_weight=dnw, dnorm_bias=dnb)
         if keep:
             res.update(du=du, du_row=du_row, dy=dy, dac=dac, dx_routed=dxr, dx_shared=dxs, **extra)
         return res
