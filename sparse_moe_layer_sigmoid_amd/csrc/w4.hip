@@ -97,6 +97,335 @@ __device__ __forceinline__ bf16x8_t decode_w4(uint32_t q, float scale) {
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Row blocks before each group (s_pre[g], of kMaxGroups + 1 entries) for row blocks of RB rows, built by a workgroup of THREADS lanes.
+template <int RB, int THREADS>
+__device__ __forceinline__ void row_block_prefix(const int32_t* __restrict__ offs, int n_groups, int* s_pre, int* s_wsum) {
+  constexpr int PER = kMaxGroups / THREADS;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int c[PER], sum = 0;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int g = tid * PER + j;
+    const int len = g < n_groups ? offs[g + 1] - offs[g] : 0;
+    c[j] = (max(len, 0) + RB - 1) / RB;
+    sum += c[j];
+  }
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 64; o <<= 1) {
+    const int v = __shfl_up(incl, o, kWave);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 63) s_wsum[wave] = incl;
+  __syncthreads();
+  int base = incl - sum;
+  for (int w = 0; w < wave; ++w) base += s_wsum[w];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    s_pre[tid * PER + j] = base;
+    base += c[j];
+  }
+  if (tid == THREADS - 1) s_pre[kMaxGroups] = base;
+  __syncthreads();
+}
+
+// The group whose row blocks, `per` work units each, hold unit L: the last one that starts at or before L.
+__device__ __forceinline__ int find_group(const int* s_pre, int n_groups, int64_t per, int64_t L) {
+  int lo = 0, hi = n_groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) >> 1;
+    if ((int64_t)s_pre[mid] * per <= L) lo = mid;
+    else hi = mid;
+  }
+  return lo;
+}
+
+// Stores four consecutive output columns (those below out_cols) of sorted row `row` of group g.
+__device__ __forceinline__ void store_columns(const W4Args& p, int g, int row, int base_row, int col, const f32x4& v) {
+  const int left = p.out_cols - col;
+  if (left <= 0) return;
+  const bool tail = g >= p.tail_first;
+  uint8_t* orow = tail ? p.out_tail + (int64_t)(row - p.offs[p.tail_first]) * p.ldo_tail_b
+                       : p.out + (int64_t)(row - base_row) * p.ldo_b;
+  if (tail || p.out_dtype == ROW_F32) {
+    float* o = reinterpret_cast<float*>(orow) + col;
+    if (left >= 4) {
+      *reinterpret_cast<f32x4_u*>(o) = v;
+    } else {
+      for (int e = 0; e < left; ++e) o[e] = v[e];
+    }
+  } else {
+    uint16_t* o = reinterpret_cast<uint16_t*>(orow) + col;
+    const u32x2 b = {f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
+                     f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
+    if (left >= 4) {
+      *reinterpret_cast<u32x2_u*>(o) = b;
+    } else {
+      for (int e = 0; e < left; ++e) o[e] = (uint16_t)(b[e / 2] >> (16 * (e & 1)));
+    }
+  }
+}
+
+// Workgroup barrier that waits for this wave's LDS operations but not for its loads in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// The streaming kernel: K a multiple of 128 and at most 128 * NW * KPW, N a multiple of 16.  A
+// workgroup walks weight tiles (16 rows; SwiGLU: 8 gate rows and their 8 up rows) against a block of
+// up to 16 token rows, whose values it holds in registers as matrix operands for as long as its
+// tiles stay in that block, so that its loads are the weights alone.  A tile's bytes come by loads
+// of whole 64-byte row pieces (the operand order, 16 rows to a load at 16 bytes each, measured 25%
+// slower) and pass through LDS into operand order.  The code is kept short: a launch starts with
+// a cold instruction cache, which for one token costs about a microsecond per kilobyte executed.
+template <bool SWIGLU, int NW, int KPW>
+__global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
+  constexpr int D = KPW > 4 ? 2 : 4;         // ring: weight tiles in flight per wave
+  constexpr int SR = (KPW + 3) / 4;          // scale loads (4 dwords of each row) per tile
+  constexpr int STRIDE = KPW * 64 + 16;      // bytes of a tile row in LDS, spread over the banks
+  constexpr int SSTRIDE = SR * 4 + 1;        // dwords of a tile row's scales in LDS
+  constexpr int THREADS = NW * 64;
+  __shared__ int s_off[kMaxGroups + 1];      // the groups' offsets
+  __shared__ int s_pre[kMaxGroups + 1];      // row blocks before each group
+  __shared__ int s_wsum[NW];
+  __shared__ int s_first;
+  __shared__ __attribute__((aligned(16))) uint8_t s_w[NW][16 * STRIDE];
+  __shared__ uint32_t s_s[NW][16 * SSTRIDE];
+  __shared__ __attribute__((aligned(16))) f32x4 s_red[NW > 1 ? 2 * D : 1][NW][64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int lr = lane & 15, lg = lane >> 4;
+  const int G = p.n_groups, n_tiles = p.n_tiles;
+
+  // prefix of the groups' row blocks, `per` consecutive groups to a lane; the lane whose groups hold
+  // the workgroup's first unit says which one
+  int64_t u0;
+  const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
+  int count;  // units of this workgroup: u0, u0 + step, ...
+  {
+    const int per = (G + THREADS - 1) / THREADS, g0 = min(tid * per, G), g1 = min(g0 + per, G);
+    int sum = 0, o = p.offs[g0];
+    for (int g = g0; g < g1; ++g) {
+      const int next = p.offs[g + 1];
+      s_off[g] = o;
+      sum += (max(next - o, 0) + 15) >> 4;
+      o = next;
+    }
+    if (g1 == G) s_off[G] = o;  // the same value from every lane that ends there
+    int incl = sum;
+#pragma unroll
+    for (int k = 1; k < 64; k <<= 1) {
+      const int v = __shfl_up(incl, k, kWave);
+      if (lane >= k) incl += v;
+    }
+    if (lane == 63) s_wsum[wave] = incl;
+    __syncthreads();
+    int base = incl - sum, all = 0;
+    for (int w = 0; w < NW; ++w) {
+      if (w < wave) base += s_wsum[w];
+      all += s_wsum[w];
+    }
+    // each of the 8 XCDs (workgroup b runs on XCD b mod 8) takes a contiguous eighth of the units,
+    // its workgroups neighbouring tiles in turn
+    const int64_t units = (int64_t)all * n_tiles;
+    u0 = (units * xcd >> 3) + (blockIdx.x >> 3);
+    const int64_t left = (units * (xcd + 1) >> 3) - u0;
+    if (left <= 0) return;  // the whole workgroup
+    count = (int)((left + step - 1) >> __builtin_ctz(step));  // step is a power of two
+    for (int g = g0; g < g1; ++g) {
+      s_pre[g] = base;
+      const int upto = base + ((max(s_off[g + 1] - s_off[g], 0) + 15) >> 4);
+      if ((int64_t)base * n_tiles <= u0 && u0 < (int64_t)upto * n_tiles) s_first = g;
+      base = upto;
+    }
+    if (g1 == G) s_pre[G] = all;
+    __syncthreads();
+  }
+  const int base_row = s_off[0];
+  const uint32_t w_row_b = p.K / 2, s_row_b = p.K / kGroup;
+  const int kblocks = p.K / 128, kper = (kblocks + NW - 1) / NW;
+  const int kb0 = wave * kper;                             // this wave's K blocks
+  const int nkb = min(max(kblocks - kb0, 0), kper);
+
+  // a position in the unit order (group, row block, tile); everything uniform
+  struct Cursor {
+    int g, rb, t;
+  };
+  auto advance = [&](Cursor& c) __attribute__((always_inline)) {  // by `step` units, to one that exists
+    c.t += step;
+    while (c.t >= n_tiles) {
+      c.t -= n_tiles;
+      ++c.rb;
+    }
+    int b = s_pre[c.g] + c.rb, e;
+    while ((e = s_pre[c.g + 1]) <= b) {
+      ++c.g;
+      c.rb = b - e;
+    }
+    c.rb = __builtin_amdgcn_readfirstlane(c.rb);
+    c.g = __builtin_amdgcn_readfirstlane(c.g);
+  };
+
+  // loads of a tile: load j reads K block j, four neighbouring lanes the 64 bytes of one row
+  const int r4 = lane >> 2, c4 = lane & 3;
+  const uint32_t row_in_tile = SWIGLU && r4 >= 8 ? p.N / 2 + r4 - 8 : r4;
+  const uint32_t off_q = row_in_tile * w_row_b + kb0 * 64 + c4 * 16;
+  const uint32_t off_s = row_in_tile * s_row_b + (kb0 + c4) * 4;
+  // Buffer loads from one group's weights: past its end they read zero and touch no memory, so the
+  // loop runs without branches around its loads (at a join the compiler waits for the path with
+  // the fewest loads in flight): a tile that does not exist is fetched from a buffer of no bytes, and K
+  // blocks past a wave's last one hold what follows, which meets zeros of x.
+  const uint32_t q_bytes = p.N * w_row_b, s_bytes = p.N * s_row_b;
+  u32x4 rq[D][KPW];
+  uint32_t rs[D][SR];
+  auto fetch = [&](int slot, const Cursor& c, bool exists) __attribute__((always_inline)) {
+    const int64_t first = (int64_t)(p.first_group + c.g) * p.N;
+    const uint32_t row = c.t * (SWIGLU ? 8 : 16);
+    const auto bq = __builtin_amdgcn_make_buffer_rsrc((void*)(p.q + first * w_row_b), 0, exists ? q_bytes : 0u, 0x00020000);
+    const auto bs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.s + first * s_row_b), 0, exists ? s_bytes : 0u, 0x00020000);
+#pragma unroll
+    for (int j = 0; j < KPW; ++j)
+      rq[slot][j] = __builtin_amdgcn_raw_buffer_load_b128(bq, off_q, row * w_row_b + j * 64, 0);
+#pragma unroll
+    for (int j = 0; j < SR; ++j) rs[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(bs, off_s, row * s_row_b + j * 16, 0);
+  };
+
+  // the token rows of a block; lanes past its last row hold its first one again and store nothing
+  u32x4 x[KPW][4];
+  auto load_x = [&](const Cursor& c) __attribute__((always_inline)) {
+    const int row0 = s_off[c.g] + c.rb * 16;
+    const int r = row0 + (lr < s_off[c.g + 1] - row0 ? lr : 0);
+    const uint8_t* xr = p.a + (int64_t)(p.a_rows ? p.a_rows[r] : r) * p.lda_b + lg * 64;
+#pragma unroll
+    for (int k = 0; k < KPW; ++k) {
+      const uint8_t* xk = xr + min(kb0 + k, kblocks - 1) * 256;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) x[k][j] = *(const u32x4*)(xk + j * 16);
+    }
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): nothing of x is pending where the paths join
+    if (nkb < KPW) {
+#pragma unroll
+      for (int k = 0; k < KPW; ++k) {  // past this wave's K blocks: zeros
+        const uint32_t keep = k < nkb ? 0xffffffffu : 0u;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) x[k][j] &= keep;
+      }
+    }
+  };
+
+  uint8_t* lw = s_w[wave];
+  uint32_t* ls = s_s[wave];
+  // one tile: the ring's registers to LDS (the slot then takes the tile D ahead), back in operand
+  // order, decode and multiply.  LDS operations of one wave execute in order, so its lanes need no
+  // barrier to see each other's bytes.
+  auto tile = [&](int slot, const Cursor& next, bool exists) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < KPW; ++j) *(u32x4*)(lw + r4 * STRIDE + c4 * 16 + j * 64) = rq[slot][j];
+#pragma unroll
+    for (int j = 0; j < SR; ++j)  // past this wave's K blocks: 1
+      ls[r4 * SSTRIDE + c4 + j * 4] = c4 + j * 4 < nkb ? rs[slot][j] : 0x7f7f7f7fu;
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    fetch(slot, next, exists);
+    f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+    for (int k = 0; k < KPW; ++k) {
+      const u32x4 q = *(const u32x4*)(lw + lr * STRIDE + k * 64 + lg * 16);
+      const uint32_t sc = reinterpret_cast<const uint8_t*>(ls)[(lr * SSTRIDE + k) * 4 + lg];
+      const float s = __uint_as_float(sc << 23);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        acc[j & 1] = mfma_bf16(decode_w4(q[j], s), __builtin_bit_cast(bf16x8_t, x[k][j]), acc[j & 1]);
+    }
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_wave_barrier();
+    f32x4 v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = acc[0][e] + acc[1][e];
+    return v;
+  };
+
+  // a summed tile: SwiGLU's gate columns sit in lanes 0..31, the up columns of the same token row in
+  // lanes 32..63; a lane stores four consecutive columns
+  auto store = [&](f32x4 v, const Cursor& c) __attribute__((always_inline)) {
+    const int row = s_off[c.g] + c.rb * 16 + lr;
+    int col = c.t * 16 + lg * 4;
+    bool live = row < s_off[c.g + 1];
+    if constexpr (SWIGLU) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] = silu(v[e]) * __shfl_xor(v[e], 32, kWave);
+      live = live && lg < 2;
+      col = c.t * 8 + lg * 4;
+    }
+    if (!live) return;
+    const bool tail = c.g >= p.tail_first;
+    uint8_t* orow = tail ? p.out_tail + (int64_t)(row - s_off[p.tail_first]) * p.ldo_tail_b
+                         : p.out + (int64_t)(row - base_row) * p.ldo_b;
+    if (tail || p.out_dtype == ROW_F32) {
+      *reinterpret_cast<f32x4_u*>(orow + col * 4) = v;
+    } else {
+      *reinterpret_cast<u32x2_u*>(orow + col * 2) = u32x2{f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
+                                                           f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
+    }
+  };
+
+  Cursor cur;
+  cur.g = __builtin_amdgcn_readfirstlane(s_first);
+  {
+    const uint32_t local = (uint32_t)(u0 - (int64_t)s_pre[cur.g] * n_tiles);
+    cur.rb = __builtin_amdgcn_readfirstlane(local / (uint32_t)n_tiles);
+    cur.t = __builtin_amdgcn_readfirstlane(local - cur.rb * n_tiles);
+  }
+  Cursor pre = cur, done = cur;  // the next tile to fetch, the first one whose sums are not joined
+  int ahead = 0;                 // tiles fetched
+  int xg = -1, xrb = 0, buf = 0;
+#pragma unroll
+  for (int d = 0; d < D; ++d) {
+    fetch(d, pre, ahead < count);
+    if (++ahead < count) advance(pre);
+  }
+  for (int u = 0; u < count; u += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {  // past the last tile: zeros, not stored
+      if (cur.g != xg || cur.rb != xrb) {
+        load_x(cur);
+        xg = cur.g;
+        xrb = cur.rb;
+      }
+      const f32x4 v = tile(d, pre, ahead < count);
+      if (++ahead < count) advance(pre);
+      if constexpr (NW > 1) {
+        s_red[buf + d][wave][lane] = v;
+      } else {
+        if (u + d < count) store(v, cur);
+      }
+      if (u + d + 1 < count) advance(cur);
+    }
+    if constexpr (NW > 1) {
+      // D tiles' sums change hands at a time.  Two sets of buffers alternate: a wave writes a set
+      // again only after the barrier of the other, which the waves that read it have then passed.
+      lds_barrier();
+      const int n = min(D, count - u);
+      for (int i = 0; i < n; ++i) {
+        if (wave == ((u + i) & (NW - 1))) {  // the waves' sums, in wave order
+          f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+          for (int w = 0; w < NW; ++w) {
+            const f32x4 o = s_red[buf + i][w][lane];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sum[e] += o[e];
+          }
+          store(sum, done);
+        }
+        if (u + i + 1 < count) advance(done);
+      }
+      buf ^= D;
+    }
+  }
+}
+
 template <bool SWIGLU, int NT>
 __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
   constexpr int BN = NT * 16;                   // weight rows per item
@@ -107,48 +436,14 @@ __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4;
 
-  // prefix of the groups' row blocks, four consecutive groups per lane
-  {
-    int c[4], sum = 0;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int g = tid * 4 + j;
-      const int len = g < p.n_groups ? p.offs[g + 1] - p.offs[g] : 0;
-      c[j] = (max(len, 0) + kRowBlock - 1) / kRowBlock;
-      sum += c[j];
-    }
-    int incl = sum;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-      const int v = __shfl_up(incl, o, kWave);
-      if (lane >= o) incl += v;
-    }
-    if (lane == 63) s_wsum[wave] = incl;
-    __syncthreads();
-    int base = incl - sum;
-    for (int w = 0; w < wave; ++w) base += s_wsum[w];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      if (tid * 4 + j <= kMaxGroups) s_pre[tid * 4 + j] = base;
-      base += c[j];
-    }
-    if (tid == 255) s_pre[kMaxGroups] = base;
-    __syncthreads();
-  }
+  row_block_prefix<kRowBlock, 256>(p.offs, p.n_groups, s_pre, s_wsum);
   const int64_t total = (int64_t)s_pre[kMaxGroups] * p.n_tiles;
   const int base_row = p.offs[0];
   const int kblocks = (p.K + 127) / 128;
   const uint32_t w_row_b = p.K / 2, s_row_b = p.K / kGroup;
 
   for (int64_t L = blockIdx.x; L < total; L += gridDim.x) {
-    // the group: the last one whose items start at or before L
-    int lo = 0, hi = p.n_groups;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if ((int64_t)s_pre[mid] * p.n_tiles <= L) lo = mid;
-      else hi = mid;
-    }
-    const int g = lo;
+    const int g = find_group(s_pre, p.n_groups, p.n_tiles, L);
     const int blocks = s_pre[g + 1] - s_pre[g];
     const int local = (int)(L - (int64_t)s_pre[g] * p.n_tiles);
     const int nt = local / blocks, rb = local - nt * blocks;
@@ -253,36 +548,37 @@ __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = silu(v[e]) * u[e];
           }
-          const int col = nt * OC + c4;
-          const int left = p.out_cols - col;
-          if (left <= 0) continue;
-          const int grow = row0 + m * 16 + r;
-          const bool tail = g >= p.tail_first;
-          uint8_t* orow = tail ? p.out_tail + (int64_t)(grow - p.offs[p.tail_first]) * p.ldo_tail_b
-                               : p.out + (int64_t)(grow - base_row) * p.ldo_b;
-          if (tail || p.out_dtype == ROW_F32) {
-            float* o = reinterpret_cast<float*>(orow) + col;
-            if (left >= 4) {
-              *reinterpret_cast<f32x4_u*>(o) = v;
-            } else {
-              for (int e = 0; e < left; ++e) o[e] = v[e];
-            }
-          } else {
-            uint16_t* o = reinterpret_cast<uint16_t*>(orow) + col;
-            const u32x2 b = {f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
-                             f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
-            if (left >= 4) {
-              *reinterpret_cast<u32x2_u*>(o) = b;
-            } else {
-              for (int e = 0; e < left; ++e) o[e] = (uint16_t)(b[e / 2] >> (16 * (e & 1)));
-            }
-          }
+          store_columns(p, g, row0 + m * 16 + r, base_row, nt * OC + c4, v);
         }
       }
     };
     if (rows <= 16) run(std::integral_constant<int, 1>{});
     else run(std::integral_constant<int, 2>{});
   }
+}
+
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+// K blocks of 128 inputs that the streaming kernel can hold: 8 waves of 8.
+constexpr int kMaxStreamBlocks = 64;
+
+template <int NW, int KPW>
+void launch_stream_as(const W4Args& a, bool swiglu, hipStream_t stream) {
+  const int grid = 256 * (8 / NW);  // two waves per SIMD: every workgroup resident
+  if (swiglu) w4_stream_kernel<true, NW, KPW><<<grid, NW * 64, 0, stream>>>(a);
+  else w4_stream_kernel<false, NW, KPW><<<grid, NW * 64, 0, stream>>>(a);
+}
+
+// As few waves as hold K in 4 blocks each (fewer partial sums to add), then more blocks.
+void launch_stream(const W4Args& a, bool swiglu, hipStream_t stream) {
+  const int kb = a.K / 128;
+  if (kb <= 4) launch_stream_as<1, 4>(a, swiglu, stream);
+  else if (kb <= 8) launch_stream_as<2, 4>(a, swiglu, stream);
+  else if (kb <= 16) launch_stream_as<4, 4>(a, swiglu, stream);
+  else if (kb <= 32) launch_stream_as<8, 4>(a, swiglu, stream);
+  else if (kb <= 48) launch_stream_as<8, 6>(a, swiglu, stream);
+  else if (kb <= 56) launch_stream_as<8, 7>(a, swiglu, stream);
+  else launch_stream_as<8, 8>(a, swiglu, stream);
 }
 
 }  // namespace
@@ -356,6 +652,11 @@ extern "C" moe_status moe_w4_gemm(const moe_w4_desc* d, hipStream_t stream) {
   a.tail_first = d->n_groups - d->tail_groups;
   a.out_tail = static_cast<uint8_t*>(d->out_tail);
   a.ldo_tail_b = d->ldo_tail * 4;
+  if (d->K % 128 == 0 && d->K <= 128 * kMaxStreamBlocks && d->N % 16 == 0 && aligned4(d->w_scale)) {
+    a.n_tiles = d->N / 16;
+    launch_stream(a, swiglu, stream);
+    return check_launch("moe_w4_gemm");
+  }
   constexpr int NT = 2;
   const int oc = swiglu ? NT * 8 : NT * 16;
   a.n_tiles = (out_cols + oc - 1) / oc;
