@@ -5,18 +5,23 @@
 // (an E8M0 code): 4.25 bits.  With few rows per expert the products are bound by the bytes of the
 // active experts' weights, so a 4-bit weight is worth 3.8 bf16 ones and nothing else matters much.
 //
-// Design:
-//  * Matrix cores with the weights as the first operand (16 weight rows x 32 inputs against 16
-//    token rows): a lane's 16-byte load is 32 inputs of one weight row, exactly one scale group,
-//    and four K steps of the MFMA; the K order is the same on the token side, so nothing is
-//    shuffled.  gfx950 converts two codes and applies the group's power of two in one instruction
-//    (exact in bf16), so scales cost nothing and every product accumulates in fp32.
-//  * A workgroup owns 16 * NT weight rows (SwiGLU: half gate, half matching up rows) against up to
-//    32 token rows of one expert; its four waves split K in turns of 128 inputs, so together they
-//    read 256 contiguous bytes of each row, and add up through LDS in wave order (deterministic).
-//    Each wave keeps a ring of weight loads in flight; the token rows come from L2.
-//  * Work items (expert, column block, row block) come from the device-side offsets, as in
-//    moe_grouped_gemm: only experts that hold rows are read.
+// Both kernels put the weights on the matrix cores as the first operand (16 weight rows x 32 inputs
+// against 16 token rows): 16 bytes of a weight row are 32 inputs, exactly one scale group, and four
+// K steps of the MFMA for the lane that holds them, so nothing is shuffled along K.  gfx950 converts
+// two codes and applies the group's power of two in one instruction, exact in bf16, so scales cost
+// no product of their own and every product accumulates in fp32.  K is split over the waves of a
+// workgroup, whose sums are added through LDS in wave order (deterministic).  Work items (expert,
+// row block, weight tile) come from the device-side offsets, as in moe_grouped_gemm: only experts
+// that hold rows are read.
+//
+//  * w4_stream_kernel (K up to 8192, N a multiple of 16): the weights stream at 5.5-6 TB/s.  Widths
+//    7168 -> 4096 (SwiGLU), 257 experts of 2048: one token 33 us (140 MB; about 9 us of that is the
+//    start of the launch and its first loads), 64 tokens 590 us (3.5 GB, 5.9 TB/s), 256 tokens 795
+//    us; the down projection of 16 tokens 145 us (806 MB, 5.6 TB/s).  Experts with more than 16
+//    rows are read once per 16 rows (from the Infinity Cache mostly), which is what 256 tokens with
+//    skewed routing pay for: 310 row blocks of 229 experts.
+//  * w4_gemm_kernel takes the other shapes, operands loaded straight into registers, up to 32
+//    token rows an item: 2.2-2.5 TB/s on the sizes above.
 #include <type_traits>
 
 #include "abi_common.h"
@@ -173,7 +178,7 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// The streaming kernel: K a multiple of 128 and at most 128 * NW * KPW, N a multiple of 16.  A
+// The streaming kernel: K at most 128 * NW * KPW, N a multiple of 16.  A
 // workgroup walks weight tiles (16 rows; SwiGLU: 8 gate rows and their 8 up rows) against a block of
 // up to 16 token rows, whose values it holds in registers as matrix operands for as long as its
 // tiles stay in that block, so that its loads are the weights alone.  A tile's bytes come by loads
@@ -202,8 +207,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   // prefix of the groups' row blocks, `per` consecutive groups to a lane; the lane whose groups hold
   // the workgroup's first unit says which one
   int64_t u0;
-  const int xcd = blockIdx.x & 7, step = gridDim.x >> 3;
-  int count;  // units of this workgroup: u0, u0 + step, ...
+  int step, count;  // units of this workgroup: u0, u0 + step, ...
   {
     const int per = (G + THREADS - 1) / THREADS, g0 = min(tid * per, G), g1 = min(g0 + per, G);
     int sum = 0, o = p.offs[g0];
@@ -227,13 +231,29 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
       if (w < wave) base += s_wsum[w];
       all += s_wsum[w];
     }
-    // each of the 8 XCDs (workgroup b runs on XCD b mod 8) takes a contiguous eighth of the units,
-    // its workgroups neighbouring tiles in turn
-    const int64_t units = (int64_t)all * n_tiles;
-    u0 = (units * xcd >> 3) + (blockIdx.x >> 3);
-    const int64_t left = (units * (xcd + 1) >> 3) - u0;
-    if (left <= 0) return;  // the whole workgroup
-    count = (int)((left + step - 1) >> __builtin_ctz(step));  // step is a power of two
+    // Workgroup b runs on XCD b mod 8; `slice` numbers them XCD by XCD.  Few row blocks (one or two
+    // tokens): each gets `share` workgroups of its own, every one a contiguous run of its tiles, so
+    // none meets a second block and an XCD touches most of its 2 MiB pages of weights at once.
+    // Else (less than 8 workgroups to a block, where whole shares would leave up to 1 / share of
+    // them idle) the units are cut into eighths, one per XCD, its workgroups neighbouring tiles in
+    // turn.  Gate/up of one token: 42 us dealt in turn, 33 us in shares; down of 16 tokens
+    // (114 blocks): 145 us in turn, 151 us in contiguous runs.
+    const int xcd = blockIdx.x & 7, seat = blockIdx.x >> 3, seats = gridDim.x >> 3;
+    if (all * 8 <= (int)gridDim.x) {
+      const uint32_t share = gridDim.x / max(all, 1), slice = xcd * seats + seat;
+      const uint32_t rb = slice / share, part = slice - rb * share;
+      const uint32_t t0 = (uint32_t)n_tiles * part / share;
+      u0 = (int64_t)rb * n_tiles + t0;
+      step = 1;
+      count = (int)rb < all ? (int)((uint32_t)n_tiles * (part + 1) / share - t0) : 0;
+    } else {
+      const int64_t units = (int64_t)all * n_tiles;
+      u0 = (units * xcd >> 3) + seat;
+      const int64_t left = (units * (xcd + 1) >> 3) - u0;
+      step = seats;  // a power of two
+      count = left > 0 ? (int)((left + step - 1) >> __builtin_ctz(step)) : 0;
+    }
+    if (count == 0) return;  // the whole workgroup
     for (int g = g0; g < g1; ++g) {
       s_pre[g] = base;
       const int upto = base + ((max(s_off[g + 1] - s_off[g], 0) + 15) >> 4);
@@ -245,7 +265,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   }
   const int base_row = s_off[0];
   const uint32_t w_row_b = p.K / 2, s_row_b = p.K / kGroup;
-  const int kblocks = p.K / 128, kper = (kblocks + NW - 1) / NW;
+  const int kblocks = (p.K + 127) / 128, kper = (kblocks + NW - 1) / NW;
   const int kb0 = wave * kper;                             // this wave's K blocks
   const int nkb = min(max(kblocks - kb0, 0), kper);
 
@@ -259,7 +279,8 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
       c.t -= n_tiles;
       ++c.rb;
     }
-    int b = s_pre[c.g] + c.rb, e;
+    const int b = s_pre[c.g] + c.rb;
+    int e;
     while ((e = s_pre[c.g + 1]) <= b) {
       ++c.g;
       c.rb = b - e;
@@ -268,6 +289,14 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
     c.g = __builtin_amdgcn_readfirstlane(c.g);
   };
 
+  Cursor cur;
+  cur.g = __builtin_amdgcn_readfirstlane(s_first);
+  {
+    const uint32_t local = (uint32_t)(u0 - (int64_t)s_pre[cur.g] * n_tiles);
+    cur.rb = __builtin_amdgcn_readfirstlane(local / (uint32_t)n_tiles);
+    cur.t = __builtin_amdgcn_readfirstlane(local - cur.rb * n_tiles);
+  }
+
   // loads of a tile: load j reads K block j, four neighbouring lanes the 64 bytes of one row
   const int r4 = lane >> 2, c4 = lane & 3;
   const uint32_t row_in_tile = SWIGLU && r4 >= 8 ? p.N / 2 + r4 - 8 : r4;
@@ -275,9 +304,16 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   const uint32_t off_s = row_in_tile * s_row_b + (kb0 + c4) * 4;
   // Buffer loads from one group's weights: past its end they read zero and touch no memory, so the
   // loop runs without branches around its loads (at a join the compiler waits for the path with
-  // the fewest loads in flight): a tile that does not exist is fetched from a buffer of no bytes, and K
-  // blocks past a wave's last one hold what follows, which meets zeros of x.
+  // the fewest loads in flight): a tile that does not exist is fetched from a buffer of no bytes, and
+  // inputs past a wave's last one or the row's end are what follows there, codes that meet zeros
+  // of x under a scale of 1.
   const uint32_t q_bytes = p.N * w_row_b, s_bytes = p.N * s_row_b;
+  uint32_t sc_keep[SR];  // the bytes of this lane's scale dwords that are its own
+#pragma unroll
+  for (int j = 0; j < SR; ++j) {
+    const int groups = min(max(p.K / kGroup - (kb0 + c4 + j * 4) * 4, 0), 4);
+    sc_keep[j] = c4 + j * 4 < nkb ? (groups == 4 ? 0xffffffffu : (1u << (8 * groups)) - 1u) : 0u;
+  }
   u32x4 rq[D][KPW];
   uint32_t rs[D][SR];
   auto fetch = [&](int slot, const Cursor& c, bool exists) __attribute__((always_inline)) {
@@ -289,7 +325,8 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
     for (int j = 0; j < KPW; ++j)
       rq[slot][j] = __builtin_amdgcn_raw_buffer_load_b128(bq, off_q, row * w_row_b + j * 64, 0);
 #pragma unroll
-    for (int j = 0; j < SR; ++j) rs[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(bs, off_s, row * s_row_b + j * 16, 0);
+    for (int j = 0; j < SR; ++j)  // a dword that would straddle the group's end is its last one instead
+      rs[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(bs, min(off_s + row * s_row_b + j * 16, s_bytes - 4), 0, 0);
   };
 
   // the token rows of a block; lanes past its last row hold its first one again and store nothing
@@ -297,22 +334,27 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   auto load_x = [&](const Cursor& c) __attribute__((always_inline)) {
     const int row0 = s_off[c.g] + c.rb * 16;
     const int r = row0 + (lr < s_off[c.g + 1] - row0 ? lr : 0);
-    const uint8_t* xr = p.a + (int64_t)(p.a_rows ? p.a_rows[r] : r) * p.lda_b + lg * 64;
+    const uint8_t* xr = p.a + (int64_t)(p.a_rows ? p.a_rows[r] : r) * p.lda_b;
+    if (nkb == KPW && (kb0 + KPW) * 128 <= p.K) {
+      const uint8_t* xk = xr + kb0 * 256 + lg * 64;
 #pragma unroll
-    for (int k = 0; k < KPW; ++k) {
-      const uint8_t* xk = xr + min(kb0 + k, kblocks - 1) * 256;
+      for (int k = 0; k < KPW; ++k)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) x[k][j] = *(const u32x4*)(xk + j * 16);
-    }
-    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): nothing of x is pending where the paths join
-    if (nkb < KPW) {
+        for (int j = 0; j < 4; ++j) x[k][j] = *(const u32x4*)(xk + k * 256 + j * 16);
+    } else {  // past this wave's K blocks or the row: zeros
 #pragma unroll
-      for (int k = 0; k < KPW; ++k) {  // past this wave's K blocks: zeros
-        const uint32_t keep = k < nkb ? 0xffffffffu : 0u;
+      for (int k = 0; k < KPW; ++k) {
+        const int at = (kb0 + k) * 128 + lg * 32;
+        const bool in = k < nkb && at < p.K;
+        const uint8_t* xk = xr + (in ? at : 0) * 2;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) x[k][j] &= keep;
+        for (int j = 0; j < 4; ++j) {
+          x[k][j] = u32x4{0u, 0u, 0u, 0u};
+          if (in) x[k][j] = *(const u32x4*)(xk + j * 16);
+        }
       }
     }
+    __builtin_amdgcn_s_waitcnt(0x0f70);  // vmcnt(0): nothing of x is pending where the paths join
   };
 
   uint8_t* lw = s_w[wave];
@@ -323,9 +365,16 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   auto tile = [&](int slot, const Cursor& next, bool exists) __attribute__((always_inline)) {
 #pragma unroll
     for (int j = 0; j < KPW; ++j) *(u32x4*)(lw + r4 * STRIDE + c4 * 16 + j * 64) = rq[slot][j];
+    if (s_row_b & 3) {  // rows of scales at odd bytes: move the bytes of such a dword into place
 #pragma unroll
-    for (int j = 0; j < SR; ++j)  // past this wave's K blocks: 1
-      ls[r4 * SSTRIDE + c4 + j * 4] = c4 + j * 4 < nkb ? rs[slot][j] : 0x7f7f7f7fu;
+      for (int j = 0; j < SR; ++j) {
+        const uint32_t at = off_s + cur.t * (SWIGLU ? 8 : 16) * s_row_b + j * 16;
+        rs[slot][j] >>= (at - min(at, s_bytes - 4)) * 8 & 31;
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < SR; ++j)  // past this wave's K blocks or the row: 1
+      ls[r4 * SSTRIDE + c4 + j * 4] = (rs[slot][j] & sc_keep[j]) | (0x7f7f7f7fu & ~sc_keep[j]);
     asm volatile("" ::: "memory");
     __builtin_amdgcn_wave_barrier();
     fetch(slot, next, exists);
@@ -371,13 +420,6 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
     }
   };
 
-  Cursor cur;
-  cur.g = __builtin_amdgcn_readfirstlane(s_first);
-  {
-    const uint32_t local = (uint32_t)(u0 - (int64_t)s_pre[cur.g] * n_tiles);
-    cur.rb = __builtin_amdgcn_readfirstlane(local / (uint32_t)n_tiles);
-    cur.t = __builtin_amdgcn_readfirstlane(local - cur.rb * n_tiles);
-  }
   Cursor pre = cur, done = cur;  // the next tile to fetch, the first one whose sums are not joined
   int ahead = 0;                 // tiles fetched
   int xg = -1, xrb = 0, buf = 0;
@@ -408,6 +450,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
       // again only after the barrier of the other, which the waves that read it have then passed.
       lds_barrier();
       const int n = min(D, count - u);
+#pragma unroll 1
       for (int i = 0; i < n; ++i) {
         if (wave == ((u + i) & (NW - 1))) {  // the waves' sums, in wave order
           f32x4 sum = {0.f, 0.f, 0.f, 0.f};
@@ -571,7 +614,7 @@ void launch_stream_as(const W4Args& a, bool swiglu, hipStream_t stream) {
 
 // As few waves as hold K in 4 blocks each (fewer partial sums to add), then more blocks.
 void launch_stream(const W4Args& a, bool swiglu, hipStream_t stream) {
-  const int kb = a.K / 128;
+  const int kb = (a.K + 127) / 128;
   if (kb <= 4) launch_stream_as<1, 4>(a, swiglu, stream);
   else if (kb <= 8) launch_stream_as<2, 4>(a, swiglu, stream);
   else if (kb <= 16) launch_stream_as<4, 4>(a, swiglu, stream);
@@ -652,7 +695,7 @@ extern "C" moe_status moe_w4_gemm(const moe_w4_desc* d, hipStream_t stream) {
   a.tail_first = d->n_groups - d->tail_groups;
   a.out_tail = static_cast<uint8_t*>(d->out_tail);
   a.ldo_tail_b = d->ldo_tail * 4;
-  if (d->K % 128 == 0 && d->K <= 128 * kMaxStreamBlocks && d->N % 16 == 0 && aligned4(d->w_scale)) {
+  if (d->K <= 128 * kMaxStreamBlocks && d->N % 16 == 0 && aligned4(d->w_scale)) {
     a.n_tiles = d->N / 16;
     launch_stream(a, swiglu, stream);
     return check_launch("moe_w4_gemm");

@@ -117,7 +117,11 @@ def _reference(a, w, offs, rows, swiglu):
 # lens of the groups (empty ones, one row, a full tile of 16, one past it, a full block of 32, several blocks), N, K
 CASES = [([1], 16, 32), ([0, 1, 0, 2], 32, 64), ([3, 16, 17, 0, 32, 33], 34, 160), ([70, 0, 0, 5], 100, 224),
          ([1, 1, 1, 1, 1], 130, 1056), ([0, 0, 129, 1], 64, 128), ([2] * 40, 48, 96), ([9, 0, 40], 258, 7168),
-         ([1, 0, 1, 1], 7, 512), ([5, 31], 2, 32), ([16, 15], 1, 288)]
+         ([1, 0, 1, 1], 7, 512), ([5, 31], 2, 32), ([16, 15], 1, 288),
+         # each number of waves and K blocks, whole and short last blocks, more weight tiles than workgroups
+         ([2, 0, 17], 48, 544), ([1, 20], 32, 992), ([0, 3], 64, 1184), ([40], 16, 2048), ([1, 1], 32, 2080),
+         ([5], 80, 4064), ([17, 1], 32, 4128), ([2], 16, 6144), ([3], 32, 6176), ([1, 2], 16, 7136), ([33], 48, 7200),
+         ([4], 32, 8192), ([4], 32, 8224), ([1, 1, 0, 16, 2], 12288, 64), ([60] * 9, 3200, 96)]
 
 
 @pytest.mark.parametrize("swiglu", [False, True])
