@@ -12,12 +12,16 @@
 //  * Forward: one workgroup holds a row in registers (chunks of 8 elements per lane), so the
 //    variance is summed over x - mean in a second pass over registers, not from squares that
 //    cancel.  With a checkpoint the normalised row is also stored as E4M3 with power-of-two 1x128
-//    scales: 16 lanes are a tile, so its maximum is four lane exchanges.
+//    scales: 16 lanes are a tile, so its maximum is four lane rotations.  Stores are non-temporal
+//    (4096 x 7168 bf16: 21.5 us, 5.5 TB/s, against 29 us; with the checkpoint 26 us, 5.6 TB/s,
+//    against 38 us).  Walking several rows with the weights in registers measured slower (33 us).
 //  * Backward: a workgroup owns all columns and walks rows b, b + grid, ...; each lane keeps dw
 //    and db of its columns in registers over all its rows, and the next row's loads are issued
-//    before the current row's two sums are exchanged.  The workgroups' partial dw / db rows go to
-//    the workspace and a second kernel adds them in workgroup order, so the result does not
-//    depend on timing.
+//    before the current row's two sums are exchanged (two rows ahead measured no faster).  The
+//    workgroups' partial dw / db rows go to the workspace and a second kernel adds them in
+//    workgroup order, so the result does not depend on timing.  4096 x 7168 from bf16 x, f32 dy and
+//    dx: 61 us (4.8 TB/s); 16384 x 7168 from the checkpoint, bf16: 120 us (4.9 TB/s, the rate of a
+//    large copy).
 #include "abi_common.h"
 #include "device_common.h"
 #include "rows_common.h"
@@ -117,7 +121,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
       uint32_t code;
       const u32x2 q = ckpt_encode8(f[i], code);
       if (c < p.d) {
-        store_codes8<FULL>(p.q + r * p.d, c, p.d, q);
+        store_codes8<FULL, true>(p.q + r * p.d, c, p.d, q);
         if ((ch & 15) == 0) p.q_scale[r * p.tiles + ch / 16] = (uint8_t)code;
       }
     }
@@ -133,7 +137,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) f[i][e] += b[e];
       }
-      store8_any<FULL>(p.y_dtype, yr, c, p.d, f[i]);
+      store8_any<FULL, true>(p.y_dtype, yr, c, p.d, f[i]);
     }
   }
 }
@@ -295,34 +299,49 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBwdArgs p) {
   }
 }
 
-// out[c] = sum over the n partial rows, in a fixed order: 16 strips of rows (one per wave), then the strips.
+// out[c] = sum over the n partial rows in a fixed order: 1024 / COLS strips of rows, COLS columns
+// each, then the strips in order.
+template <int COLS>
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part_w,
                                                            const float* __restrict__ part_b, int n, int d,
                                                            float* __restrict__ dw, float* __restrict__ db) {
-  __shared__ float red[16][64];
+  constexpr int STRIPS = 1024 / COLS;
+  __shared__ float red[STRIPS][COLS + 1];
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   float* out = blockIdx.y == 0 ? dw : db;
   if (!out) return;  // the whole workgroup
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  const int col = threadIdx.x % COLS, strip = threadIdx.x / COLS;
+  const int c = blockIdx.x * COLS + col;
   float s = 0.f;
   if (c < d) {
 #pragma unroll 8
-    for (int r = w; r < n; r += 16) s += part[(int64_t)r * d + c];
+    for (int r = strip; r < n; r += STRIPS) s += part[(int64_t)r * d + c];
   }
-  red[w][lane] = s;
+  red[strip][col] = s;
   __syncthreads();
-  if (w == 0 && c < d) {
+  if (strip == 0 && c < d) {
     float v = 0.f;
-#pragma unroll
-    for (int k = 0; k < 16; ++k) v += red[k][lane];
+#pragma unroll 8
+    for (int k = 0; k < STRIPS; ++k) v += red[k][col];
     out[c] = v;
   }
 }
 
-// Chunks per lane: a row in one wave while its chunks fit 4 to a lane, else 4 to a lane.
-int norm_chunks_per_lane(int d) {
+// Many partial rows of few columns need more strips to fill the chip (2048 x 512: 8 us with 16
+// columns to a workgroup, 14 us with 64), few of many columns fewer workgroups (64 x 7168: 4 us
+// with 64 columns, 5.5 us with 16).
+void launch_reduce(const float* pw, const float* pb, int n, int d, float* dw, float* db, hipStream_t stream) {
+  const int two = db ? 2 : 1;
+  if (n > 512) norm_reduce_kernel<16><<<dim3((d + 15) / 16, two), 1024, 0, stream>>>(pw, pb, n, d, dw, db);
+  else norm_reduce_kernel<64><<<dim3((d + 63) / 64, two), 1024, 0, stream>>>(pw, pb, n, d, dw, db);
+}
+
+// Forward: chunks per lane.  Few rows: one, so that a row's loads are all in flight together (one row
+// of 7168: 4.2 us against 5.0 us with four).  Many rows: a row in one wave while its chunks fit 4 to a
+// lane, else 4 to a lane (4096 rows of 7168: 21 us, 28 us with two chunks).
+int norm_chunks_per_lane(int rows, int d) {
   const int chunks = (d + 7) / 8;
+  if (rows <= 256) return chunks <= 1024 ? 1 : 2;
   return chunks <= 64 ? 1 : chunks <= 128 ? 2 : 4;
 }
 
@@ -333,12 +352,14 @@ int group_threads(int d, int nv) {
   return ((chunks + nv - 1) / nv + 63) / 64 * 64;
 }
 
-// Workgroups of the backward kernel: two resident per CU at the largest rows, more of the small
-// ones; every one writes a partial row of dw and db, so no more than that.
+// Workgroups of the backward kernel.  Every one writes a partial row of dw and db that is read again,
+// so each should walk 16 rows or more, down to one workgroup per CU: 4096 rows of 7168, 256
+// workgroups 61 us, 512 70 us; 16384 rows, 256 143 us, 512 (32 rows each) 121 us.
 int norm_bwd_grid(int rows, int d) {
   const int threads = group_threads(d, norm_bwd_chunks_per_lane(d));
   const int per_cu = threads >= 448 ? 2 : threads >= 256 ? 4 : threads >= 128 ? 8 : 16;
-  const int n = 256 * per_cu;
+  int n = rows / 16;
+  n = n < 256 ? 256 : n > 256 * per_cu ? 256 * per_cu : n;
   return rows < n ? rows : n;
 }
 
@@ -351,9 +372,9 @@ void launch_norm_backward(const NormBwdArgs& a, int nv, int grid, int threads, h
 }
 
 template <int XT, bool FULL>
-void launch_norm(const NormArgs& a, int rows, int nv, int threads, hipStream_t stream) {
+void launch_norm(const NormArgs& a, int rows, int nv, hipStream_t stream) {
   auto kernel = nv == 1 ? norm_kernel<XT, 1, FULL> : nv == 2 ? norm_kernel<XT, 2, FULL> : norm_kernel<XT, 4, FULL>;
-  kernel<<<rows, threads, 0, stream>>>(a);
+  kernel<<<rows, group_threads(a.d, nv), 0, stream>>>(a);
 }
 
 bool row_dtype(int t) { return t == MOE_BF16 || t == MOE_F32; }
@@ -399,10 +420,10 @@ extern "C" moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const vo
     a.q = ck_q;
     a.q_scale = ck_scale;
     a.tiles = (d + 127) / 128;
-    const int nv = norm_chunks_per_lane(d), threads = group_threads(d, nv);
+    const int nv = norm_chunks_per_lane(rows, d);
     const bool full = d % 8 == 0;
-    if (x_dtype == MOE_BF16) full ? launch_norm<ROW_BF16, true>(a, rows, nv, threads, stream) : launch_norm<ROW_BF16, false>(a, rows, nv, threads, stream);
-    else full ? launch_norm<ROW_F32, true>(a, rows, nv, threads, stream) : launch_norm<ROW_F32, false>(a, rows, nv, threads, stream);
+    if (x_dtype == MOE_BF16) full ? launch_norm<ROW_BF16, true>(a, rows, nv, stream) : launch_norm<ROW_BF16, false>(a, rows, nv, stream);
+    else full ? launch_norm<ROW_F32, true>(a, rows, nv, stream) : launch_norm<ROW_F32, false>(a, rows, nv, stream);
   }
   return check_launch("moe_norm");
 }
@@ -478,6 +499,6 @@ extern "C" moe_status moe_norm_backward(const void* dy, int dy_dtype, int64_t ld
     }
   }
   if (grid != 1 && (dweight || dbias))  // with no rows the sums are zero
-    norm_reduce_kernel<<<dim3((d + 63) / 64, dbias ? 2 : 1), 1024, 0, stream>>>(pw, pb, grid, d, dweight, dbias);
+    launch_reduce(pw, pb, grid, d, dweight, dbias, stream);
   return check_launch("moe_norm_backward");
 }

@@ -86,13 +86,15 @@ __device__ __forceinline__ u32x4 pack_bf16x8(const float f[8]) {
 }
 
 // Stores 8 values at [c, c + 8) of a row of d elements (bf16: rounded to nearest even).
-template <bool FULL>
+// With NT the stores are non-temporal: whole 16-byte pieces of lines that nothing reads again soon.
+template <bool FULL, bool NT = false>
 __device__ __forceinline__ void store8_any(int dtype, void* row, int c, int d, const float f[8]) {
   if (dtype == ROW_BF16) {
     uint16_t* p = static_cast<uint16_t*>(row) + c;
     const u32x4 o = pack_bf16x8(f);
     if (FULL || c + 8 <= d) {
-      *reinterpret_cast<u32x4_u*>(p) = o;
+      if constexpr (NT) __builtin_nontemporal_store(o, reinterpret_cast<u32x4_u*>(p));
+      else *reinterpret_cast<u32x4_u*>(p) = o;
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -101,8 +103,14 @@ __device__ __forceinline__ void store8_any(int dtype, void* row, int c, int d, c
   } else {
     float* p = static_cast<float*>(row) + c;
     if (FULL || c + 8 <= d) {
-      *reinterpret_cast<f32x4_u*>(p) = f32x4{f[0], f[1], f[2], f[3]};
-      *reinterpret_cast<f32x4_u*>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+      const f32x4 lo = {f[0], f[1], f[2], f[3]}, hi = {f[4], f[5], f[6], f[7]};
+      if constexpr (NT) {
+        __builtin_nontemporal_store(lo, reinterpret_cast<f32x4_u*>(p));
+        __builtin_nontemporal_store(hi, reinterpret_cast<f32x4_u*>(p + 4));
+      } else {
+        *reinterpret_cast<f32x4_u*>(p) = lo;
+        *reinterpret_cast<f32x4_u*>(p + 4) = hi;
+      }
     } else {
 #pragma unroll
       for (int i = 0; i < 8; ++i)
@@ -122,10 +130,11 @@ __device__ __forceinline__ u32x2 load_codes8(const uint8_t* row, int c, int d) {
   return r;
 }
 
-template <bool FULL>
+template <bool FULL, bool NT = false>
 __device__ __forceinline__ void store_codes8(uint8_t* row, int c, int d, const u32x2& q) {
   if (FULL || c + 8 <= d) {
-    *reinterpret_cast<u32x2_u*>(row + c) = q;
+    if constexpr (NT) __builtin_nontemporal_store(q, reinterpret_cast<u32x2_u*>(row + c));
+    else *reinterpret_cast<u32x2_u*>(row + c) = q;
   } else {
 #pragma unroll
     for (int i = 0; i < 8; ++i)
