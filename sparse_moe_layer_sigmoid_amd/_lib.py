@@ -504,15 +504,22 @@ def _shape(t, shape, name):
     return t
 
 
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
 def _launch(dev, fn: str, *args):
-    """Call `fn` with the current stream of `dev` as its last argument, on that device."""
-    stream = ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+    """Call `fn` with the current stream of `dev` as its last argument, on that device.  Pointers are
+    plain integers (the argument types convert them) and the stream is asked for as one: for the
+    small calls the host's part is most of the time."""
+    stream = torch._C._cuda_getCurrentRawStream(dev.index)
     if torch.cuda.current_device() == dev.index:
         st = getattr(lib(), fn)(*args, stream)
     else:
         with torch.cuda.device(dev):
             st = getattr(lib(), fn)(*args, stream)
-    _check(fn, st)
+    if st != MOE_OK:
+        _check(fn, st)
 
 
 _ROW_DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
@@ -578,8 +585,8 @@ def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, rms: bool = False, ou
     rstd = torch.empty(T, dtype=torch.float32, device=dev) if want_stats or checkpoint else None
     q = torch.empty((T, d), dtype=torch.uint8, device=dev) if checkpoint else None
     s = torch.empty((T, (d + 127) // 128), dtype=torch.uint8, device=dev) if checkpoint else None
-    _launch(dev, "moe_norm", _ptr(x), _ROW_DT[x.dtype], x.stride(0), _ptr(weight), _ptr(bias), wdt, T, d, float(eps),
-            MOE_NORM_RMS if rms else MOE_NORM_LAYER, _ptr(y), _ROW_DT[odt], d, _ptr(mean), _ptr(rstd), _ptr(q), _ptr(s))
+    _launch(dev, "moe_norm", _addr(x), _ROW_DT[x.dtype], x.stride(0), _addr(weight), _addr(bias), wdt, T, d, float(eps),
+            MOE_NORM_RMS if rms else MOE_NORM_LAYER, _addr(y), _ROW_DT[odt], d, _addr(mean), _addr(rstd), _addr(q), _addr(s))
     return y, mean, rstd, ((q, s) if checkpoint else None)
 
 
@@ -620,10 +627,10 @@ def moe_norm_backward(dy, x, mean, rstd, weight=None, rms: bool = False, checkpo
     db = torch.empty(d, dtype=torch.float32, device=dev) if want_dbias else None
     wsb = lib().moe_norm_backward_workspace_size(T, d) if want_dweight or want_dbias else 0
     ws = torch.empty(wsb, dtype=torch.uint8, device=dev) if wsb else None
-    _launch(dev, "moe_norm_backward", _ptr(dy), _ROW_DT[dy.dtype], dy.stride(0), _ptr(x),
-            _ROW_DT[x.dtype] if x is not None else MOE_BF16, x.stride(0) if x is not None else d, _ptr(q), _ptr(s),
-            _ptr(mean), _ptr(rstd), _ptr(weight), wdt, T, d, MOE_NORM_RMS if rms else MOE_NORM_LAYER, _ptr(dx),
-            _ROW_DT[odt], d, _ptr(dw), _ptr(db), _ptr(ws), wsb)
+    _launch(dev, "moe_norm_backward", _addr(dy), _ROW_DT[dy.dtype], dy.stride(0), _addr(x),
+            _ROW_DT[x.dtype] if x is not None else MOE_BF16, x.stride(0) if x is not None else d, _addr(q), _addr(s),
+            _addr(mean), _addr(rstd), _addr(weight), wdt, T, d, MOE_NORM_RMS if rms else MOE_NORM_LAYER, _addr(dx),
+            _ROW_DT[odt], d, _addr(dw), _addr(db), _addr(ws), wsb)
     return dx, dw, db
 
 
@@ -634,7 +641,7 @@ def fp8_ckpt_pack(x):
     rows, cols = x.shape
     q = torch.empty((rows, cols), dtype=torch.uint8, device=x.device)
     s = torch.empty((rows, (cols + 127) // 128), dtype=torch.uint8, device=x.device)
-    _launch(x.device, "fp8_ckpt_pack", _ptr(x), _ROW_DT[x.dtype], rows, cols, x.stride(0), _ptr(q), _ptr(s))
+    _launch(x.device, "fp8_ckpt_pack", _addr(x), _ROW_DT[x.dtype], rows, cols, x.stride(0), _addr(q), _addr(s))
     return q, s
 
 
@@ -647,7 +654,7 @@ def fp8_ckpt_unpack(q, scale, weight=None, bias=None, out_dtype=torch.bfloat16):
     if out_dtype not in _ROW_DT:
         raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
     out = torch.empty((rows, cols), dtype=out_dtype, device=q.device)
-    _launch(q.device, "fp8_ckpt_unpack", _ptr(q), _ptr(scale), rows, cols, _ptr(weight), _ptr(bias), wdt, _ptr(out),
+    _launch(q.device, "fp8_ckpt_unpack", _addr(q), _addr(scale), rows, cols, _addr(weight), _addr(bias), wdt, _addr(out),
             _ROW_DT[out_dtype], cols)
     return out
 
@@ -670,8 +677,8 @@ def moe_swiglu_backward_ckpt(ac_q, ac_scale, dh, want_h: bool = True, fp8: bool 
     if fp8:
         dq = torch.empty((rows, c2), dtype=torch.uint8, device=dev)
         ds = torch.empty((rows, c2 // 128), dtype=torch.float32, device=dev)
-    _launch(dev, "moe_swiglu_backward_ckpt", _ptr(ac_q), _ptr(ac_scale), _ptr(dh), rows, I, _ptr(dac), _ptr(dq), _ptr(ds),
-            _ptr(h))
+    _launch(dev, "moe_swiglu_backward_ckpt", _addr(ac_q), _addr(ac_scale), _addr(dh), rows, I, _addr(dac), _addr(dq), _addr(ds),
+            _addr(h))
     return (dac, dq, ds, h) if fp8 else (dac, h)
 
 
@@ -700,8 +707,8 @@ def moe_combine_backward_ckpt(d_out, y_q, y_scale, topk_idx, topk_gate, scores, 
     if fp8:
         dyq = torch.empty((T * (K + 1), d), dtype=torch.uint8, device=dev)
         dys = torch.empty((T * (K + 1), d // 128), dtype=torch.float32, device=dev)
-    _launch(dev, "moe_combine_backward_ckpt", _ptr(d_out), _ptr(y_q), _ptr(y_scale), _ptr(topk_idx), _ptr(topk_gate),
-            _ptr(scores), _ptr(pair_pos), T, K, d, scores.shape[1], _ptr(dy), _ptr(du), _ptr(du_row), _ptr(dyq), _ptr(dys))
+    _launch(dev, "moe_combine_backward_ckpt", _addr(d_out), _addr(y_q), _addr(y_scale), _addr(topk_idx), _addr(topk_gate),
+            _addr(scores), _addr(pair_pos), T, K, d, scores.shape[1], _addr(dy), _addr(du), _addr(du_row), _addr(dyq), _addr(dys))
     return (dy, du, du_row, dyq, dys) if fp8 else (dy, du, du_row)
 
 
@@ -715,7 +722,7 @@ def w4_quant(w):
     q = torch.empty((*w.shape[:-1], k // 2), dtype=torch.uint8, device=w.device)
     s = torch.empty((*w.shape[:-1], k // 32), dtype=torch.uint8, device=w.device)
     mats = w.shape[0] if w.dim() == 3 else 1
-    _launch(w.device, "w4_quant", _ptr(w), mats, w.shape[-2], k, _ptr(q), _ptr(s))
+    _launch(w.device, "w4_quant", _addr(w), mats, w.shape[-2], k, _addr(q), _addr(s))
     return q, s
 
 

@@ -16,10 +16,11 @@
 //
 //  * w4_stream_kernel (K up to 8192, N a multiple of 16): the weights stream at 5.5-6 TB/s.  Widths
 //    7168 -> 4096 (SwiGLU), 257 experts of 2048: one token 33 us (140 MB; about 9 us of that is the
-//    start of the launch and its first loads), 64 tokens 590 us (3.5 GB, 5.9 TB/s), 256 tokens 795
-//    us; the down projection of 16 tokens 145 us (806 MB, 5.6 TB/s).  Experts with more than 16
-//    rows are read once per 16 rows (from the Infinity Cache mostly), which is what 256 tokens with
-//    skewed routing pay for: 310 row blocks of 229 experts.
+//    start of the launch and its first loads), 64 tokens 590 us (3.5 GB, 5.9 TB/s), 256 tokens 740
+//    us; the down projection of 16 tokens 144 us (806 MB, 5.6 TB/s).  An expert with more than 16
+//    rows is read by several workgroups, at the same time and on one XCD (802 us when they followed
+//    each other); 256 tokens with skewed routing have 310 row blocks of 229 experts.  Sharing the
+//    XCDs' work out by what a set costs instead of by units gained 2% there and lost 3% elsewhere.
 //  * w4_gemm_kernel takes the other shapes, operands loaded straight into registers, up to 32
 //    token rows an item: 2.2-2.5 TB/s on the sizes above.
 #include <type_traits>
@@ -269,32 +270,54 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   const int kb0 = wave * kper;                             // this wave's K blocks
   const int nkb = min(max(kblocks - kb0, 0), kper);
 
-  // a position in the unit order (group, row block, tile); everything uniform
+  // A position in the unit order; everything uniform.  A group's row blocks go in sets of a power
+  // of two (14 blocks: 8 + 4 + 2), and a set's units run over the blocks first, then the tiles: the
+  // XCD's workgroups (a multiple of the set) each keep to one block while they read a tile's
+  // weights together, so that they come over the fabric once per set instead of once per block.
   struct Cursor {
-    int g, rb, t;
+    int g, base, size, idx;  // row blocks [base, base + size) of group g, unit idx of that set
+    __device__ __forceinline__ int rb() const { return base + (idx & (size - 1)); }
+    __device__ __forceinline__ int tile() const { return idx >> __builtin_ctz(size); }
+  };
+  auto set_size = [&](int blocks) __attribute__((always_inline)) { return blocks >= 32 ? 32 : 1 << (31 - __clz(blocks)); };
+  auto settle = [&](Cursor& c) __attribute__((always_inline)) {  // idx past the set: on to the set it is in
+    int span = c.size * n_tiles;
+    while (c.idx >= span) {
+      c.idx -= span;
+      c.base += c.size;
+      int blocks = s_pre[c.g + 1] - s_pre[c.g];
+      if (c.base >= blocks) {
+        c.base = 0;
+        do {
+          ++c.g;
+          blocks = s_pre[c.g + 1] - s_pre[c.g];
+        } while (blocks == 0);
+      }
+      c.size = __builtin_amdgcn_readfirstlane(set_size(blocks - c.base));
+      span = c.size * n_tiles;
+    }
+    c.g = __builtin_amdgcn_readfirstlane(c.g);
+    c.base = __builtin_amdgcn_readfirstlane(c.base);
+    c.idx = __builtin_amdgcn_readfirstlane(c.idx);
   };
   auto advance = [&](Cursor& c) __attribute__((always_inline)) {  // by `step` units, to one that exists
-    c.t += step;
-    while (c.t >= n_tiles) {
-      c.t -= n_tiles;
-      ++c.rb;
-    }
-    const int b = s_pre[c.g] + c.rb;
-    int e;
-    while ((e = s_pre[c.g + 1]) <= b) {
-      ++c.g;
-      c.rb = b - e;
-    }
-    c.rb = __builtin_amdgcn_readfirstlane(c.rb);
-    c.g = __builtin_amdgcn_readfirstlane(c.g);
+    c.idx += step;
+    settle(c);
   };
-
   Cursor cur;
-  cur.g = __builtin_amdgcn_readfirstlane(s_first);
   {
-    const uint32_t local = (uint32_t)(u0 - (int64_t)s_pre[cur.g] * n_tiles);
-    cur.rb = __builtin_amdgcn_readfirstlane(local / (uint32_t)n_tiles);
-    cur.t = __builtin_amdgcn_readfirstlane(local - cur.rb * n_tiles);
+    cur.g = __builtin_amdgcn_readfirstlane(s_first);
+    const int local = (int)(u0 - (int64_t)s_pre[cur.g] * n_tiles);
+    if (step == 1) {  // one row block
+      cur.base = __builtin_amdgcn_readfirstlane((uint32_t)local / (uint32_t)n_tiles);
+      cur.size = 1;
+      cur.idx = __builtin_amdgcn_readfirstlane(local - cur.base * n_tiles);
+    } else {
+      cur.base = 0;
+      cur.size = __builtin_amdgcn_readfirstlane(set_size(s_pre[cur.g + 1] - s_pre[cur.g]));
+      cur.idx = local;
+      settle(cur);
+    }
   }
 
   // loads of a tile: load j reads K block j, four neighbouring lanes the 64 bytes of one row
@@ -318,7 +341,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   uint32_t rs[D][SR];
   auto fetch = [&](int slot, const Cursor& c, bool exists) __attribute__((always_inline)) {
     const int64_t first = (int64_t)(p.first_group + c.g) * p.N;
-    const uint32_t row = c.t * (SWIGLU ? 8 : 16);
+    const uint32_t row = c.tile() * (SWIGLU ? 8 : 16);
     const auto bq = __builtin_amdgcn_make_buffer_rsrc((void*)(p.q + first * w_row_b), 0, exists ? q_bytes : 0u, 0x00020000);
     const auto bs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.s + first * s_row_b), 0, exists ? s_bytes : 0u, 0x00020000);
 #pragma unroll
@@ -332,7 +355,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   // the token rows of a block; lanes past its last row hold its first one again and store nothing
   u32x4 x[KPW][4];
   auto load_x = [&](const Cursor& c) __attribute__((always_inline)) {
-    const int row0 = s_off[c.g] + c.rb * 16;
+    const int row0 = s_off[c.g] + c.rb() * 16;
     const int r = row0 + (lr < s_off[c.g + 1] - row0 ? lr : 0);
     const uint8_t* xr = p.a + (int64_t)(p.a_rows ? p.a_rows[r] : r) * p.lda_b;
     if (nkb == KPW && (kb0 + KPW) * 128 <= p.K) {
@@ -368,7 +391,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
     if (s_row_b & 3) {  // rows of scales at odd bytes: move the bytes of such a dword into place
 #pragma unroll
       for (int j = 0; j < SR; ++j) {
-        const uint32_t at = off_s + cur.t * (SWIGLU ? 8 : 16) * s_row_b + j * 16;
+        const uint32_t at = off_s + cur.tile() * (SWIGLU ? 8 : 16) * s_row_b + j * 16;
         rs[slot][j] >>= (at - min(at, s_bytes - 4)) * 8 & 31;
       }
     }
@@ -399,14 +422,14 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   // a summed tile: SwiGLU's gate columns sit in lanes 0..31, the up columns of the same token row in
   // lanes 32..63; a lane stores four consecutive columns
   auto store = [&](f32x4 v, const Cursor& c) __attribute__((always_inline)) {
-    const int row = s_off[c.g] + c.rb * 16 + lr;
-    int col = c.t * 16 + lg * 4;
+    const int row = s_off[c.g] + c.rb() * 16 + lr;
+    int col = c.tile() * 16 + lg * 4;
     bool live = row < s_off[c.g + 1];
     if constexpr (SWIGLU) {
 #pragma unroll
       for (int e = 0; e < 4; ++e) v[e] = silu(v[e]) * __shfl_xor(v[e], 32, kWave);
       live = live && lg < 2;
-      col = c.t * 8 + lg * 4;
+      col = c.tile() * 8 + lg * 4;
     }
     if (!live) return;
     const bool tail = c.g >= p.tail_first;
@@ -431,10 +454,10 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   for (int u = 0; u < count; u += D) {
 #pragma unroll
     for (int d = 0; d < D; ++d) {  // past the last tile: zeros, not stored
-      if (cur.g != xg || cur.rb != xrb) {
+      if (cur.g != xg || cur.rb() != xrb) {
         load_x(cur);
         xg = cur.g;
-        xrb = cur.rb;
+        xrb = cur.rb();
       }
       const f32x4 v = tile(d, pre, ahead < count);
       if (++ahead < count) advance(pre);
