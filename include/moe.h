@@ -535,7 +535,8 @@ typedef struct {
   const int32_t* group_offsets; /* device i32, at least first_group + n_groups + 1 entries, non-decreasing */
   int first_group;
   int n_groups;                 /* 1..1024 */
-  int64_t m_total;              /* rows covered by the groups, an upper bound */
+  int64_t m_total;              /* upper bound of the rows covered by the groups: offsets past
+                                   off[first_group] + m_total count as that */
   int N;                        /* weight rows of each group (2*I for SWIGLU) */
   int K;                        /* inputs, a positive multiple of 32 */
   int epilogue;                 /* MOE_EPI_NONE or MOE_EPI_SWIGLU (N even) */

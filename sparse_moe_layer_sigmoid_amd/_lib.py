@@ -756,6 +756,10 @@ def moe_w4_gemm(a, w_q, w_scale, group_offsets, first_group: int, n_groups: int,
         _rows(out_tail, "out_tail")
         if out_tail.dtype != torch.float32 or out_tail.shape[1] != cols:
             raise ValueError(f"out_tail must be float32 with {cols} columns")
+    if (a_rows.numel() if a_rows is not None else a.shape[0]) < m_total and first_group == 0:
+        raise ValueError(f"{'a_rows' if a_rows is not None else 'a'} covers fewer than m_total={m_total} rows")
+    if out.shape[0] + (out_tail.shape[0] if tail_groups else 0) < m_total:
+        raise ValueError(f"the outputs hold fewer than m_total={m_total} rows")
     dev = a.device
     _same_device(dev, w_q=w_q, w_scale=w_scale, group_offsets=group_offsets, out=out, a_rows=a_rows,
                  out_tail=out_tail if tail_groups else None)

@@ -80,6 +80,7 @@ struct W4Args {
   const int32_t* offs;  // group_offsets + first_group
   int first_group;
   int n_groups;
+  int m_total;  // offsets past offs[0] + m_total count as that
   int N;  // weight rows per group
   int K;
   int n_tiles;
@@ -103,16 +104,22 @@ __device__ __forceinline__ bf16x8_t decode_w4(uint32_t q, float scale) {
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
+// Group offset i, held to the rows that the caller vouched for.
+__device__ __forceinline__ int group_offset(const W4Args& p, int i) {
+  const int first = p.offs[0];
+  return min(p.offs[i], (int)min((int64_t)first + p.m_total, (int64_t)INT32_MAX));
+}
+
 // Row blocks before each group (s_pre[g], of kMaxGroups + 1 entries) for row blocks of RB rows, built by a workgroup of THREADS lanes.
 template <int RB, int THREADS>
-__device__ __forceinline__ void row_block_prefix(const int32_t* __restrict__ offs, int n_groups, int* s_pre, int* s_wsum) {
+__device__ __forceinline__ void row_block_prefix(const W4Args& p, int* s_pre, int* s_wsum) {
   constexpr int PER = kMaxGroups / THREADS;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int c[PER], sum = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int g = tid * PER + j;
-    const int len = g < n_groups ? offs[g + 1] - offs[g] : 0;
+    const int len = g < p.n_groups ? group_offset(p, g + 1) - group_offset(p, g) : 0;
     c[j] = (max(len, 0) + RB - 1) / RB;
     sum += c[j];
   }
@@ -151,7 +158,7 @@ __device__ __forceinline__ void store_columns(const W4Args& p, int g, int row, i
   const int left = p.out_cols - col;
   if (left <= 0) return;
   const bool tail = g >= p.tail_first;
-  uint8_t* orow = tail ? p.out_tail + (int64_t)(row - p.offs[p.tail_first]) * p.ldo_tail_b
+  uint8_t* orow = tail ? p.out_tail + (int64_t)(row - group_offset(p, p.tail_first)) * p.ldo_tail_b
                        : p.out + (int64_t)(row - base_row) * p.ldo_b;
   if (tail || p.out_dtype == ROW_F32) {
     float* o = reinterpret_cast<float*>(orow) + col;
@@ -211,9 +218,9 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   int step, count;  // units of this workgroup: u0, u0 + step, ...
   {
     const int per = (G + THREADS - 1) / THREADS, g0 = min(tid * per, G), g1 = min(g0 + per, G);
-    int sum = 0, o = p.offs[g0];
+    int sum = 0, o = group_offset(p, g0);
     for (int g = g0; g < g1; ++g) {
-      const int next = p.offs[g + 1];
+      const int next = group_offset(p, g + 1);
       s_off[g] = o;
       sum += (max(next - o, 0) + 15) >> 4;
       o = next;
@@ -502,7 +509,7 @@ __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4;
 
-  row_block_prefix<kRowBlock, 256>(p.offs, p.n_groups, s_pre, s_wsum);
+  row_block_prefix<kRowBlock, 256>(p, s_pre, s_wsum);
   const int64_t total = (int64_t)s_pre[kMaxGroups] * p.n_tiles;
   const int base_row = p.offs[0];
   const int kblocks = (p.K + 127) / 128;
@@ -513,8 +520,8 @@ __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
     const int blocks = s_pre[g + 1] - s_pre[g];
     const int local = (int)(L - (int64_t)s_pre[g] * p.n_tiles);
     const int nt = local / blocks, rb = local - nt * blocks;
-    const int row0 = p.offs[g] + rb * kRowBlock;
-    const int rows = min(kRowBlock, p.offs[g + 1] - row0);
+    const int row0 = group_offset(p, g) + rb * kRowBlock;
+    const int rows = min(kRowBlock, group_offset(p, g + 1) - row0);
 
     // weight rows of this lane (past N: the last one again, not stored)
     const int half = p.N / 2;
@@ -709,6 +716,7 @@ extern "C" moe_status moe_w4_gemm(const moe_w4_desc* d, hipStream_t stream) {
   a.offs = d->group_offsets + d->first_group;
   a.first_group = d->first_group;
   a.n_groups = d->n_groups;
+  a.m_total = (int)d->m_total;
   a.N = d->N;
   a.K = d->K;
   a.out_cols = out_cols;

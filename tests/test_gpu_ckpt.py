@@ -347,3 +347,31 @@ def test_checkpointed_captured():
         torch.cuda.synchronize()
         for p, r in zip(out, ref):
             assert torch.equal(p, r), k
+
+
+def test_rows_past_32_bit_offsets():
+    """More than 2^31 elements (and bytes past 2^32): the last rows equal those of a call on them alone, to the bit."""
+    rows, cols, last = 270_000, 8200, 3
+    x = torch.empty((rows, cols), dtype=torch.bfloat16, device=DEV)
+    x.fill_(1.5)
+    x[-last:] = I.gen_normal(400, (last, cols), 1.0).to(DEV)
+    tail = x[-last:].clone()
+    q, s = M().fp8_ckpt_pack(x)
+    q2, s2 = M().fp8_ckpt_pack(tail)
+    assert torch.equal(q[-last:], q2) and torch.equal(s[-last:], s2)
+    assert torch.equal(M().fp8_ckpt_unpack(q, s)[-last:], M().fp8_ckpt_unpack(q2, s2))
+    y, mean, rstd, ck = M().moe_norm(x, want_stats=True, checkpoint=True)
+    y2, mean2, rstd2, ck2 = M().moe_norm(tail, want_stats=True, checkpoint=True)
+    # one chunk per lane for few rows, four for many: the sums' order differs, so not to the bit here
+    assert rel_err(np64(y[-last:]), np64(y2)) <= 2.0 ** -7 and rel_err(np64(rstd[-last:]), np64(rstd2)) <= 100 * U
+    assert torch.equal(y[:1], y[1:2]) and torch.equal(y[0], y[rows // 2])
+    dx = M().moe_norm_backward(x, x, mean, rstd)[0]
+    dx2 = M().moe_norm_backward(tail, tail, mean[-last:].contiguous(), rstd[-last:].contiguous())[0]
+    assert torch.equal(dx[-last:], dx2)
+    del y, dx, ck
+    inter = cols // 2
+    dh = torch.zeros((rows, inter), device=DEV)
+    dh[-last:] = 1.0
+    dac, h = M().moe_swiglu_backward_ckpt(q, s, dh)
+    dac2, h2 = M().moe_swiglu_backward_ckpt(q2, s2, dh[-last:].clone())
+    assert torch.equal(dac[-last:], dac2) and torch.equal(h[-last:], h2)

@@ -222,6 +222,10 @@ def test_w4_gemm_many_groups_and_no_rows():
     want, tol = _reference(np64(a), decode(q, s), offs, np.arange(rows), False)
     assert np.all(np.abs(np64(out) - want) <= tol)
     out.fill_(3.0)
+    # offsets that claim more rows than m_total are held to it
+    M().moe_w4_gemm(a, q, s, torch.from_numpy(offs).to(DEV), 0, G, 4, out)
+    assert np.all(np.abs(np64(out[:4]) - want[:4]) <= tol[:4]) and bool((out[4:] == 3.0).all())
+    out.fill_(3.0)
     M().moe_w4_gemm(a, q, s, torch.zeros(G + 1, dtype=torch.int32, device=DEV), 0, G, 5, out)
     M().moe_w4_gemm(a, q, s, torch.zeros(G + 1, dtype=torch.int32, device=DEV), 0, G, 0, out)
     assert bool((out == 3.0).all())
@@ -258,6 +262,78 @@ def test_w4_gemm_repeats_streams_and_capture():
         ref = go()
         torch.cuda.synchronize()
         assert torch.equal(out, ref), k
+
+
+def test_w4_gemm_refuses_short_tensors():
+    q, s = _weights(560, 2, 32, 64)
+    a = I.gen_normal(561, (4, 64), 1.0).to(DEV)
+    offs = torch.tensor([0, 2, 4], dtype=torch.int32, device=DEV)
+    out = torch.empty((4, 32), device=DEV)
+    bad = (dict(m_total=5), dict(out=out[:3]), dict(a_rows=offs[:3]), dict(n_groups=3), dict(offs=offs[:2]), dict(out=out[:, :31]),
+           dict(a=a[:, :32]), dict(s=s[:, :, :1].contiguous()), dict(tail_groups=1, out_tail=out[:0]), dict(out=out.double()),
+           dict(a=a.float()), dict(a=a.t()))
+    for kw in bad:
+        c = dict(a=a, q=q, s=s, offs=offs, n_groups=2, m_total=4, out=out, a_rows=None, tail_groups=0, out_tail=None)
+        c.update(kw)
+        if "out_tail" in kw:
+            c["out"] = out[:2]
+        with pytest.raises((ValueError, TypeError)):
+            M().moe_w4_gemm(c["a"], c["q"], c["s"], c["offs"], 0, c["n_groups"], c["m_total"], c["out"], a_rows=c["a_rows"],
+                            tail_groups=c["tail_groups"], out_tail=c["out_tail"])
+
+
+def test_w4_gemm_two_streams_at_once():
+    """Calls that run at the same time keep to themselves (the operator has no workspace)."""
+    lens, N, K = [1, 0, 40, 3], 2048, 2048
+    offs = torch.from_numpy(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)).to(DEV)
+    rows = sum(lens)
+    ops = []
+    for k in range(2):
+        q, s = _weights(570 + k, len(lens), N, K)
+        a = I.gen_normal(572 + k, (rows, K), 1.0).to(DEV)
+        ref = torch.empty((rows, N), device=DEV)
+        M().moe_w4_gemm(a, q, s, offs, 0, len(lens), rows, ref)
+        ops.append((a, q, s, ref, torch.empty((rows, N), device=DEV), torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for a, q, s, ref, out, st in ops:
+            with torch.cuda.stream(st):
+                M().moe_w4_gemm(a, q, s, offs, 0, len(lens), rows, out)
+    torch.cuda.synchronize()
+    for a, q, s, ref, out, st in ops:
+        assert torch.equal(ref, out)
+
+
+@pytest.mark.parametrize("fill", [0, 1, 254])
+def test_w4_gemm_scale_ends(fill):
+    """Every group at an end of the scale range.  Weights below 2^-126 are subnormal bf16 numbers; the activations are
+    scaled so that the exact sums are ordinary f32 numbers."""
+    N, K = 16, 64
+    q, s = _weights(580, 1, N, K)
+    s.fill_(fill)
+    a = (I.gen_normal(581, (3, K), 1.0).float() * 2.0 ** (100 if fill < 2 else -100)).to(torch.bfloat16).to(DEV)
+    offs = torch.tensor([0, 3], dtype=torch.int32, device=DEV)
+    out = torch.empty((3, N), device=DEV)
+    M().moe_w4_gemm(a, q, s, offs, 0, 1, 3, out)
+    w = decode(q, s)
+    # a weight of 4 or 6 times 2^127 is beyond bf16: infinite
+    big = np.abs(w[0]) > 3.4e38
+    w[0][big] = np.sign(w[0][big]) * np.inf
+    with np.errstate(invalid="ignore"):
+        want, tol = _reference(np64(a), w, [0, 3], np.arange(3), False)
+    o = np64(out)
+    fine = np.isfinite(want)
+    assert np.array_equal(fine, np.isfinite(o))
+    assert np.all(np.abs(o - want)[fine] <= tol[fine])
+
+
+def test_layer_w4_no_tokens():
+    cfg = I.small(I.V3_BF16, name="w4_empty", T=1, d=64, n_experts=8, top_k=2, inter=64)
+    ex = [I.gen_expert(cfg, e) for e in range(cfg.groups)]
+    W13, W2 = (torch.stack([e[k] for e in ex]).to(torch.bfloat16).to(DEV) for k in (0, 1))
+    layer = M().MoELayer(I.gen_router(cfg).to(DEV), W13, W2, I.gen_bias(cfg).to(DEV), 2, w4=True, norm="layer")
+    out = layer.forward(torch.empty((0, 64), dtype=torch.bfloat16, device=DEV))
+    assert out.shape == (0, 64)
 
 
 @pytest.mark.parametrize("T,norm", [(1, None), (1, "rms"), (5, None), (64, "layer")])
