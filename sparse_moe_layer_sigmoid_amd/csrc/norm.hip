@@ -81,15 +81,18 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
       for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
     }
   }
-  const float inv_d = 1.0f / (float)p.d;
+  // values and squares are summed times 2^-k >= 1/d > 2^-k-1 (exact products), so a sum overflows only
+  // where its mean nearly does
+  const int k = 31 - __clz(p.d);
+  const float down = pow2f(-k), up = pow2f(k) / (float)p.d;
   float mean = 0.f;
   if (!p.rms) {
     float s = 0.f;
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += f[i][e];
-    mean = block_sum(s, red[0], nw) * inv_d;
+      for (int e = 0; e < 8; ++e) s = fmaf(f[i][e], down, s);
+    mean = block_sum(s, red[0], nw) * up;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (t + i * G) * 8;
@@ -97,16 +100,12 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
       for (int e = 0; e < 8; ++e) f[i][e] = c + e < p.d ? f[i][e] - mean : 0.f;
     }
   }
-  // the squares are summed times 2^-k >= 1/d > 2^-k-1 (exact products), so the sum overflows only
-  // where the mean of the squares nearly does
-  const int k = 31 - __clz(p.d);
-  const float down = pow2f(-k);
   float ss = 0.f;
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(f[i][e] * down, f[i][e], ss);
-  const float rstd = 1.0f / sqrtf(block_sum(ss, red[1], nw) * (inv_d * pow2f(k)) + p.eps);
+  const float rstd = 1.0f / sqrtf(block_sum(ss, red[1], nw) * up + p.eps);
   if (t == 0) {
     if (p.mean) p.mean[r] = mean;
     if (p.rstd) p.rstd[r] = rstd;
@@ -235,7 +234,8 @@ __global__ __launch_bounds__(1024) void norm_backward_kernel(NormBwdArgs p) {
       } else {
         values8(x[i].v, xh);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) xh[e] = (xh[e] - mean) * rstd;
+        for (int e = 0; e < 8; ++e)  // past the row's end 0: there mean * rstd alone could overflow
+          xh[e] = FULL || (t + i * G) * 8 + e < p.d ? (xh[e] - mean) * rstd : 0.f;
       }
     };
 #pragma unroll

@@ -231,6 +231,40 @@ def test_norm_constant_and_extreme_rows():
     assert torch.isnan(y[4]).all() and torch.isnan(y[5]).all()
 
 
+def test_norm_large_constant_rows():
+    """Rows of 2^120: their sum passes the largest float although the mean does not (1024 columns), and the mean times
+    rstd does too, which must not reach the chunk's lanes past the row (4 columns).  All exact: the mean is 2^120, xhat 0,
+    rstd eps^-1/2, so dx = rstd (g - mean g) and dweight 0."""
+    for d in (1024, 4):
+        x = torch.full((3, d), 2.0 ** 120, device=DEV)
+        dy = I.gen_normal(93, (3, d), 1.0, torch.float32).to(DEV)
+        y, mean, rstd, _ = M().moe_norm(x, eps=1e-6, want_stats=True)
+        assert torch.equal(y, torch.zeros_like(y)) and torch.equal(mean, x[:, 0])
+        assert bool(((rstd - 1e3).abs() <= 1e3 * 4 * U).all())
+        dx, dw, db = M().moe_norm_backward(dy, x, mean, rstd, want_dbias=True)
+        g = np64(dy)
+        want = np64(rstd)[:, None] * (g - g.mean(1, keepdims=True))
+        assert np.all(np.abs(np64(dx) - want) <= 100 * U * 1e3 * (np.abs(g) + np.abs(g).mean(1, keepdims=True)))
+        assert torch.equal(dw, torch.zeros(d, device=DEV))
+        assert np.all(np.abs(np64(db) - g.sum(0)) <= 3 * U * np.abs(g).sum(0))
+
+
+def test_norm_one_row_of_any_stride():
+    """One row has no row stride: a transposed column and a row of an expanded tensor are taken like any other."""
+    d = 72
+    col = _vec(94, d, torch.float32).reshape(d, 1)
+    row = col.t()                                                          # strides (1, 1)
+    plain = col.reshape(1, d).clone()
+    assert row.stride(0) == 1
+    y, mean, rstd, ck = M().moe_norm(plain, want_stats=True, checkpoint=True)
+    for x in (row, plain.expand(4, d)[:1]):
+        y1, mean1, rstd1, ck1 = M().moe_norm(x, want_stats=True, checkpoint=True)
+        assert torch.equal(y, y1) and torch.equal(ck[0], ck1[0]) and torch.equal(ck[1], ck1[1])
+        for a, b in zip(M().moe_norm_backward(x, x, mean, rstd), M().moe_norm_backward(plain, plain, mean, rstd)):
+            assert (a is None and b is None) or torch.equal(a, b)
+        assert all(torch.equal(a, b) for a, b in zip(M().fp8_ckpt_pack(x), M().fp8_ckpt_pack(plain)))
+
+
 def test_norm_no_rows_and_untouched_neighbours():
     d = 72
     x = torch.empty((0, d), device=DEV)
