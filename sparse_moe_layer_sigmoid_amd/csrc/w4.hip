@@ -250,10 +250,10 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
     if (all * 8 <= (int)gridDim.x) {
       const uint32_t share = gridDim.x / max(all, 1), slice = xcd * seats + seat;
       const uint32_t rb = slice / share, part = slice - rb * share;
-      const uint32_t t0 = (uint32_t)n_tiles * part / share;
+      const uint32_t t0 = (uint32_t)((uint64_t)n_tiles * part / share);
       u0 = (int64_t)rb * n_tiles + t0;
       step = 1;
-      count = (int)rb < all ? (int)((uint32_t)n_tiles * (part + 1) / share - t0) : 0;
+      count = (int)rb < all ? (int)((uint32_t)((uint64_t)n_tiles * (part + 1) / share) - t0) : 0;
     } else {
       const int64_t units = (int64_t)all * n_tiles;
       u0 = (units * xcd >> 3) + seat;

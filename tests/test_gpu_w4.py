@@ -327,6 +327,18 @@ def test_w4_gemm_scale_ends(fill):
     assert np.all(np.abs(o - want)[fine] <= tol[fine])
 
 
+def test_w4_gemm_many_weight_rows():
+    """One token against 2^25 weight rows: the tiles of all workgroups together pass 32 bits in the products that deal
+    them out.  Weights 1, inputs 1, K = 32: every output is 32 exactly."""
+    N, K = 1 << 25, 32
+    q = torch.full((1, N, K // 2), 0x22, dtype=torch.uint8, device=DEV)
+    s = torch.full((1, N, 1), 127, dtype=torch.uint8, device=DEV)
+    out = torch.zeros((1, N), dtype=torch.bfloat16, device=DEV)
+    M().moe_w4_gemm(torch.ones((1, K), dtype=torch.bfloat16, device=DEV), q, s,
+                    torch.tensor([0, 1], dtype=torch.int32, device=DEV), 0, 1, 1, out)
+    assert bool((out == 32.0).all())
+
+
 def test_layer_w4_no_tokens():
     cfg = I.small(I.V3_BF16, name="w4_empty", T=1, d=64, n_experts=8, top_k=2, inter=64)
     ex = [I.gen_expert(cfg, e) for e in range(cfg.groups)]
