@@ -349,11 +349,14 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   auto fetch = [&](int slot, const Cursor& c, bool exists) __attribute__((always_inline)) {
     const int64_t first = (int64_t)(p.first_group + c.g) * p.N;
     const uint32_t row = c.tile() * (SWIGLU ? 8 : 16);
-    const auto bq = __builtin_amdgcn_make_buffer_rsrc((void*)(p.q + first * w_row_b), 0, exists ? q_bytes : 0u, 0x00020000);
+    const uint32_t row_b = row * w_row_b;
+    const auto bq = __builtin_amdgcn_make_buffer_rsrc((void*)(p.q + (first * w_row_b + row_b)), 0,
+                                                      exists ? q_bytes - row_b : 0u, 0x00020000);
     const auto bs = __builtin_amdgcn_make_buffer_rsrc((void*)(p.s + first * s_row_b), 0, exists ? s_bytes : 0u, 0x00020000);
+    uint32_t o = off_q;
+    asm volatile("" : "+v"(o));  // else the KPW sums below are kept in registers instead of the instructions
 #pragma unroll
-    for (int j = 0; j < KPW; ++j)
-      rq[slot][j] = __builtin_amdgcn_raw_buffer_load_b128(bq, off_q, row * w_row_b + j * 64, 0);
+    for (int j = 0; j < KPW; ++j) rq[slot][j] = __builtin_amdgcn_raw_buffer_load_b128(bq, o + j * 64, 0, 0);
 #pragma unroll
     for (int j = 0; j < SR; ++j)  // a dword that would straddle the group's end is its last one instead
       rs[slot][j] = __builtin_amdgcn_raw_buffer_load_b32(bs, min(off_s + row * s_row_b + j * 16, s_bytes - 4), 0, 0);
