@@ -263,6 +263,28 @@ def test_layer_checkpointed_training_step(fp8, norm):
         assert off <= 0.08, n
 
 
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("T", [1, 3])
+def test_layer_checkpointed_few_tokens(fp8, T):
+    """A checkpointed step of fewer tokens than experts, most experts without rows, against the plain backward run on
+    what the checkpoints stand for, with the tolerances of the larger step; an expert without rows has a zero gradient."""
+    cfg, layer, x, d_out = _layer(fp8, "rms", T=T, Inter=256 if fp8 else 128)
+    out0, buf0 = layer.forward(x, train=True)
+    out, buf = layer.forward(x, checkpoint=True)
+    assert torch.equal(out, out0)
+    ac = M().fp8_ckpt_unpack(*buf["ac_ckpt"], out_dtype=torch.float32)
+    rep = dict(buf0, x=layer._checkpointed_x(buf), y=M().fp8_ckpt_unpack(*buf["y_ckpt"]), ac=ac, checkpoint=False,
+               norm=buf["norm"])
+    if not fp8:
+        rep["h"] = M().moe_swiglu_backward_ckpt(*buf["ac_ckpt"], torch.zeros((ac.shape[0], ac.shape[1] // 2), device=DEV))[1]
+    g, gr = layer.backward(d_out, buf), layer.backward(d_out, rep)
+    for n in ("dx", "dw_router", "dw13", "dw2", "dnorm_weight"):
+        say(f"  T={T} fp8={fp8} {n}: vs the checkpoints' values {rel_err(np64(g[n]), np64(gr[n])):.2e}")
+        assert rel_err(np64(g[n]), np64(gr[n])) <= (2.0 ** -4 if fp8 else 2.0 ** -7), n
+    empty = torch.nonzero(buf["expert_counts"] == 0).flatten()
+    assert empty.numel() > 0 and not bool(g["dw13"][empty].any()) and not bool(g["dw2"][empty].any())
+
+
 @pytest.mark.parametrize("norm", ["rms", "layer"])
 def test_layer_with_norm_against_float64(norm):
     """The layer with a norm: the forward equals the layer on the norm's output, and the gradient of the rows before it
