@@ -435,7 +435,9 @@ moe_status moe_router_wgrad(const uint16_t* x, const int32_t* sorted_token,
  *
  * In this section rows may have any width and start at any element (pointers and leading
  * dimensions need only the alignment of one element) unless a call says otherwise; outputs must
- * not overlap inputs.
+ * not overlap inputs.  A call takes up to 2^35 elements less a few thousand (a launch of 2^32 lanes of
+ * 8; rows count as whole 1x128 tiles, in moe_norm and the combine as whole workgroups of 64 lanes
+ * or more); MOE_ERR_SHAPE past that.
  * ==================================================================================== */
 
 /* moe_norm -- y = xhat * weight + bias, xhat = (x - mean) * rstd, per row, in fp32:
@@ -516,14 +518,15 @@ moe_status moe_combine_backward_ckpt(const uint16_t* d_out, const uint8_t* y_q, 
  * weights (k in [-127, 126]; 0 for a group of zeros), codes = RNE(w / 2^k) (exact product, ties to
  * the even code).  A group that holds an infinity or NaN gets the scale code 255 (and codes 0).
  *   w  device bf16 [n_mats, n, k];  q device u8 [n_mats, n, k/2] out;  scale device u8
- *   [n_mats, n, k/32] out.  Limits: n_mats >= 0; n >= 1; k a positive multiple of 32. */
+ *   [n_mats, n, k/32] out.  Limits: n_mats >= 0; n >= 1; k a positive multiple of 32; less than 2^35
+ *   weights to a call. */
 moe_status w4_quant(const uint16_t* w, int n_mats, int n, int k, uint8_t* q, uint8_t* scale,
                     hipStream_t stream);
 
 /* moe_w4_gemm -- for every sorted row r of group g (groups and rows as in moe_grouped_gemm):
  *   out[r - off[first_group]] = epilogue(A[a_rows[r] or r] . W[g]^T)
- * with A bf16, W 4-bit, exact bf16 x weight products and fp32 sums (K split over four waves, added
- * in a fixed order).  SWIGLU: W[g] holds N/2 gate rows, then N/2 up rows; out = silu(a) c.  Any
+ * with A bf16, W 4-bit, exact bf16 x weight products and fp32 sums (K split over the waves of a
+ * workgroup, added in a fixed order: a row's result does not depend on the other rows).  SWIGLU: W[g] holds N/2 gate rows, then N/2 up rows; out = silu(a) c.  Any
  * number of rows per group is right; it is made for the few of a decode batch (moe_grouped_gemm's
  * bf16 or E4M3 weights suit the many rows of a training batch). */
 typedef struct {

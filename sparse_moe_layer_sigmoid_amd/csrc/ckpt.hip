@@ -275,7 +275,7 @@ extern "C" moe_status fp8_ckpt_pack(const void* x, int x_dtype, int64_t rows, in
               "fp8_ckpt_pack: ldx=%lld must be >= cols and x aligned to its elements", (long long)ldx);
   if (rows > 0) {
     const int tiles = (cols + 127) / 128;
-    MOE_REQUIRE(rows <= ((int64_t)1 << 34) / tiles, MOE_ERR_SHAPE, "fp8_ckpt_pack: too many tiles");
+    MOE_REQUIRE(rows <= kMaxLanes / (tiles * 16), MOE_ERR_SHAPE, "fp8_ckpt_pack: too many rows");
     const int64_t grid = (rows * tiles * 16 + 255) / 256;
     const RowSplit sp = make_row_split((uint32_t)tiles * 16);
     const bool full = cols % 8 == 0;
@@ -302,7 +302,7 @@ extern "C" moe_status fp8_ckpt_unpack(const uint8_t* q, const uint8_t* scale, in
               (long long)ldo);
   if (rows > 0) {
     const int tiles = (cols + 127) / 128, chunks = (cols + 7) / 8;
-    MOE_REQUIRE(rows <= ((int64_t)1 << 38) / chunks, MOE_ERR_SHAPE, "fp8_ckpt_unpack: too many rows");
+    MOE_REQUIRE(rows <= kMaxLanes / chunks, MOE_ERR_SHAPE, "fp8_ckpt_unpack: too many rows");
     const int64_t grid = (rows * chunks + 255) / 256;
     auto kernel = cols % 8 == 0 ? ckpt_unpack_kernel<true> : ckpt_unpack_kernel<false>;
     kernel<<<(unsigned)grid, 256, 0, stream>>>(q, scale, rows, cols, tiles, make_row_split(chunks), weight, bias, w_dtype,
@@ -329,7 +329,7 @@ extern "C" moe_status moe_swiglu_backward_ckpt(const uint8_t* ac_q, const uint8_
   if (rows > 0) {
     const bool wide = inter % 8 == 0;
     const int per_row = inter / (wide ? 8 : 4), tiles = (2 * inter + 127) / 128;
-    MOE_REQUIRE(rows <= ((int64_t)1 << 38) / per_row, MOE_ERR_SHAPE, "moe_swiglu_backward_ckpt: too many rows");
+    MOE_REQUIRE(rows <= kMaxLanes / per_row, MOE_ERR_SHAPE, "moe_swiglu_backward_ckpt: too many rows");
     const unsigned grid = (unsigned)((rows * per_row + 255) / 256);
     const RowSplit sp = make_row_split(per_row);
     if (wide)
@@ -362,6 +362,7 @@ extern "C" moe_status moe_combine_backward_ckpt(const uint16_t* d_out, const uin
               MOE_ERR_ALIGN, "moe_combine_backward_ckpt: d_out and dy must be 16-byte, y_q and dy_q 8-byte aligned");
   if (T > 0) {
     const int threads = d <= 512 ? 64 : d <= 2048 ? 256 : 448;
+    MOE_REQUIRE(T <= kMaxLanes / threads, MOE_ERR_SHAPE, "moe_combine_backward_ckpt: too many tokens (%d)", T);
     if (top_k <= 8)
       combine_backward_ckpt_kernel<8><<<T, threads, 0, stream>>>(d_out, y_q, y_scale, topk_idx, topk_gate, scores,
                                                                  pair_pos, T, top_k, d, n_experts, dy, du, du_row, dy_q,

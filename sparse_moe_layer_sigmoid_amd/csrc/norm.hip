@@ -424,6 +424,7 @@ extern "C" moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const vo
     a.q_scale = ck_scale;
     a.tiles = (d + 127) / 128;
     const int nv = norm_chunks_per_lane(rows, d);
+    MOE_REQUIRE(rows <= kMaxLanes / group_threads(d, nv), MOE_ERR_SHAPE, "moe_norm: too many rows (%d)", rows);
     const bool full = d % 8 == 0;
     if (x_dtype == MOE_BF16) full ? launch_norm<ROW_BF16, true>(a, rows, nv, stream) : launch_norm<ROW_BF16, false>(a, rows, nv, stream);
     else full ? launch_norm<ROW_F32, true>(a, rows, nv, stream) : launch_norm<ROW_F32, false>(a, rows, nv, stream);

@@ -205,6 +205,9 @@ __device__ __forceinline__ void ckpt_decode8(const u32x2& q, uint32_t code, floa
   ckpt_decode4(q[1], code, f + 4);
 }
 
+// Lanes of one launch: they are counted in 32 bits, and the last workgroup may be short.
+constexpr int64_t kMaxLanes = ((int64_t)1 << 32) - 1024;
+
 // Position of a lane's chunk when rows of `per_row` chunks are dealt out to workgroups of 256
 // lanes: the workgroup's first chunk is split once (uniform), the lane's offset with a
 // multiply-high (exact: offset < per_row + 256 and per_row < 2^15) or, where a row is longer than

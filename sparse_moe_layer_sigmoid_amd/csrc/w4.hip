@@ -670,7 +670,7 @@ extern "C" moe_status w4_quant(const uint16_t* w, int n_mats, int n, int k, uint
               "w4_quant: n_mats=%d n=%d k=%d (k a positive multiple of %d)", n_mats, n, k, kGroup);
   MOE_REQUIRE(aligned16(w) && aligned16(q), MOE_ERR_ALIGN, "w4_quant: w and q must be 16-byte aligned");
   const int64_t rows = (int64_t)n_mats * n;
-  MOE_REQUIRE(rows <= ((int64_t)1 << 38) / (k / 8), MOE_ERR_SHAPE, "w4_quant: too many weights");
+  MOE_REQUIRE(rows <= kMaxLanes / (k / 8), MOE_ERR_SHAPE, "w4_quant: too many weights");
   const int64_t n8 = rows * (k / 8);
   if (n8 > 0) w4_quant_kernel<<<(unsigned)((n8 + 255) / 256), 256, 0, stream>>>(w, n8, q, scale);
   return check_launch("w4_quant");

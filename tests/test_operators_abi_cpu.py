@@ -125,6 +125,22 @@ def test_w4_gemm_rejects(kw, code):
     assert L.lib().moe_w4_gemm(None, None) == 1
 
 
+def test_more_threads_than_a_launch_has():
+    """A launch counts its threads in 32 bits: calls with more chunks of 8 elements than that are refused (workgroups of
+    256 chunks; for the norms and the combine one workgroup a row)."""
+    L = _lib()
+    n = 1 << 32
+    for fn, args in (
+            ("fp8_ckpt_pack", (P(16), 1, n // 16, 128, 128, P(16), P(16), None)),
+            ("fp8_ckpt_unpack", (P(16), P(16), n // 16, 128, None, None, 1, P(16), 0, 128, None)),
+            ("moe_swiglu_backward_ckpt", (P(16), P(16), P(16), n // 16, 128, P(16), None, None, P(16), None)),
+            ("w4_quant", (P(16), 1 << 10, 1 << 18, 128, P(16), P(16), None)),
+            ("moe_combine_backward_ckpt", (P(16), P(16), P(16), P(16), P(16), P(16), P(16), n // 64, 1, 8, 8, P(16), P(16),
+                                           P(16), None, None, None)),
+            ("moe_norm", _norm(rows=n // 64, q=None, s=None))):
+        _expect(L, fn, args, 2)
+
+
 def test_binding_refuses_cpu_tensors():
     import sparse_moe_layer_sigmoid_amd as M
     x = torch.zeros((4, 128))
