@@ -327,6 +327,25 @@ def test_w4_gemm_scale_ends(fill):
     assert np.all(np.abs(o - want)[fine] <= tol[fine])
 
 
+@pytest.mark.parametrize("N,K", [(48, 544), (50, 544), (32, 8192), (34, 8224)])
+def test_w4_gemm_row_by_itself(N, K):
+    """A row's result has the same bits alone and among other rows, in any group size (streaming and general kernel)."""
+    q, s = _weights(520, 1, N, K)
+    a = I.gen_normal(521, (40, K), 1.0).to(DEV)
+
+    def go(x, swiglu):
+        out = torch.empty((x.shape[0], N // 2 if swiglu else N), device=DEV)
+        M().moe_w4_gemm(x, q, s, torch.tensor([0, x.shape[0]], dtype=torch.int32, device=DEV), 0, 1, x.shape[0], out,
+                        swiglu=swiglu)
+        return out
+
+    for swiglu in (False, True):
+        full = go(a, swiglu)
+        for r in (0, 15, 16, 39):
+            assert torch.equal(go(a[r:r + 1], swiglu)[0], full[r])
+        assert torch.equal(go(a[:17], swiglu), full[:17])
+
+
 def test_w4_gemm_many_weight_rows():
     """One token against 2^25 weight rows: the tiles of all workgroups together pass 32 bits in the products that deal
     them out.  Weights 1, inputs 1, K = 32: every output is 32 exactly."""
@@ -374,3 +393,26 @@ def test_layer_w4(T, norm):
         layer.forward(x.to(DEV), checkpoint=True)
     with pytest.raises(NotImplementedError):
         layer.backward(out, buf)
+
+
+@pytest.mark.parametrize("T", [1, 6])
+def test_layer_w4_captured(T):
+    """A decode step of the layer (norm, routing, both 4-bit products, combine) in one graph, replayed over changed tokens
+    with eager steps between the replays."""
+    cfg = I.small(I.V3_BF16, name="w4_graph", T=T, d=256, n_experts=16, top_k=4, inter=96, w_std=0.05, router_std=0.05, seed=12)
+    ex = [I.gen_expert(cfg, e) for e in range(cfg.groups)]
+    W13 = torch.stack([a for a, _ in ex]).to(torch.bfloat16).to(DEV)
+    W2 = torch.stack([b for _, b in ex]).to(torch.bfloat16).to(DEV)
+    layer = M().MoELayer(I.gen_router(cfg).to(DEV), W13, W2, I.gen_bias(cfg).to(DEV), cfg.top_k, w4=True, norm="rms")
+    x = I.gen_x(cfg).to(DEV)
+    layer.forward(x)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = layer.forward(x)
+    for k in range(4):
+        x.copy_(I.gen_normal(570 + k, (T, cfg.d), 1.0))
+        g.replay()
+        ref = layer.forward(x)
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref), k
