@@ -16,8 +16,8 @@
 //
 //  * w4_stream_kernel (K up to 8192, N a multiple of 16): the weights stream at 5.5-6 TB/s.  Widths
 //    7168 -> 4096 (SwiGLU), 257 experts of 2048: one token 33 us (140 MB; about 9 us of that is the
-//    start of the launch and its first loads), 64 tokens 590 us (3.5 GB, 5.9 TB/s), 256 tokens 740
-//    us; the down projection of 16 tokens 144 us (806 MB, 5.6 TB/s).  An expert with more than 16
+//    start of the launch and its first loads), 64 tokens 566 us (3.5 GB, 6.2 TB/s), 256 tokens 700
+//    us; the down projection of 16 tokens 142 us (806 MB, 5.7 TB/s).  An expert with more than 16
 //    rows is read by several workgroups, at the same time and on one XCD (802 us when they followed
 //    each other); 256 tokens with skewed routing have 310 row blocks of 229 experts.  Sharing the
 //    XCDs' work out by what a set costs instead of by units gained 2% there and lost 3% elsewhere.
@@ -243,9 +243,13 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
     // tokens): each gets `share` workgroups of its own, every one a contiguous run of its tiles, so
     // none meets a second block and an XCD touches most of its 2 MiB pages of weights at once.
     // Else (less than 8 workgroups to a block, where whole shares would leave up to 1 / share of
-    // them idle) the units are cut into eighths, one per XCD, its workgroups neighbouring tiles in
-    // turn.  Gate/up of one token: 42 us dealt in turn, 33 us in shares; down of 16 tokens
-    // (114 blocks): 145 us in turn, 151 us in contiguous runs.
+    // them idle) the units are cut into equal slices, each for `step` neighbouring workgroups of one
+    // XCD that take its tiles in turn.  `step` is as many as leave each 8 tiles of a block, or 16 where
+    // there are more blocks than groups, so that blocks of one expert read the same weights: fetching a
+    // block's token rows costs about as much as two tiles.  Gate/up of one token: 42 us dealt in turn, 33
+    // us in shares; down of 16 tokens (114 blocks): 142 us in turn, 151 us in contiguous runs.  2048 -> 768
+    // of 129 experts, 256 tokens: gate/up 106 us when all of an XCD's workgroups shared a block, 61 us
+    // with 8 tiles each, 59 us with 16; down 73, 41 and 39 us; 16 tiles for 16 tokens above: 144 us.
     const int xcd = blockIdx.x & 7, seat = blockIdx.x >> 3, seats = gridDim.x >> 3;
     if (all * 8 <= (int)gridDim.x) {
       const uint32_t share = gridDim.x / max(all, 1), slice = xcd * seats + seat;
@@ -256,9 +260,11 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
       count = (int)rb < all ? (int)((uint32_t)((uint64_t)n_tiles * (part + 1) / share) - t0) : 0;
     } else {
       const int64_t units = (int64_t)all * n_tiles;
-      u0 = (units * xcd >> 3) + seat;
-      const int64_t left = (units * (xcd + 1) >> 3) - u0;
-      step = seats;  // a power of two
+      step = min(seats, 1 << (31 - __clz(max(n_tiles / (all > G ? 16 : 8), 1))));  // powers of two
+      const int lg_step = __builtin_ctz(step), lg_slices = __builtin_ctz(gridDim.x) - lg_step;
+      const int slice = (xcd * seats + seat) >> lg_step;
+      u0 = (units * slice >> lg_slices) + (seat & (step - 1));
+      const int64_t left = (units * (slice + 1) >> lg_slices) - u0;
       count = left > 0 ? (int)((left + step - 1) >> __builtin_ctz(step)) : 0;
     }
     if (count == 0) return;  // the whole workgroup
@@ -278,15 +284,16 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   const int nkb = min(max(kblocks - kb0, 0), kper);
 
   // A position in the unit order; everything uniform.  A group's row blocks go in sets of a power
-  // of two (14 blocks: 8 + 4 + 2), and a set's units run over the blocks first, then the tiles: the
-  // XCD's workgroups (a multiple of the set) each keep to one block while they read a tile's
+  // of two (14 blocks: 8 + 4 + 2), and a set's units run over the blocks first, then the tiles: a
+  // slice's workgroups (a multiple of the set) each keep to one block while they read a tile's
   // weights together, so that they come over the fabric once per set instead of once per block.
   struct Cursor {
     int g, base, size, idx;  // row blocks [base, base + size) of group g, unit idx of that set
     __device__ __forceinline__ int rb() const { return base + (idx & (size - 1)); }
     __device__ __forceinline__ int tile() const { return idx >> __builtin_ctz(size); }
   };
-  auto set_size = [&](int blocks) __attribute__((always_inline)) { return blocks >= 32 ? 32 : 1 << (31 - __clz(blocks)); };
+  const int max_set = min(step, 32);
+  auto set_size = [&](int blocks) __attribute__((always_inline)) { return min(max_set, 1 << (31 - __clz(blocks))); };
   auto settle = [&](Cursor& c) __attribute__((always_inline)) {  // idx past the set: on to the set it is in
     int span = c.size * n_tiles;
     while (c.idx >= span) {
@@ -314,17 +321,13 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   Cursor cur;
   {
     cur.g = __builtin_amdgcn_readfirstlane(s_first);
-    const int local = (int)(u0 - (int64_t)s_pre[cur.g] * n_tiles);
-    if (step == 1) {  // one row block
-      cur.base = __builtin_amdgcn_readfirstlane((uint32_t)local / (uint32_t)n_tiles);
-      cur.size = 1;
-      cur.idx = __builtin_amdgcn_readfirstlane(local - cur.base * n_tiles);
-    } else {
-      cur.base = 0;
-      cur.size = __builtin_amdgcn_readfirstlane(set_size(s_pre[cur.g + 1] - s_pre[cur.g]));
-      cur.idx = local;
-      settle(cur);
-    }
+    const int local = (int)(u0 - (int64_t)s_pre[cur.g] * n_tiles), blocks = s_pre[cur.g + 1] - s_pre[cur.g];
+    const int span = max_set * n_tiles;  // past the whole sets at once
+    const int whole = min((int)((uint32_t)local / (uint32_t)span), blocks >> __builtin_ctz(max_set));
+    cur.base = __builtin_amdgcn_readfirstlane(whole * max_set);
+    cur.size = __builtin_amdgcn_readfirstlane(set_size(blocks - cur.base));
+    cur.idx = local - whole * span;
+    settle(cur);
   }
 
   // loads of a tile: load j reads K block j, four neighbouring lanes the 64 bytes of one row

@@ -155,6 +155,29 @@ def test_w4_gemm(lens, N, K, swiglu):
     assert torch.equal(out2, out[:rows])
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("lens,N,K", [
+    ([1] * 40, 16, 2080), ([1, 0] * 35, 272, 2080), ([3] * 20 + [100] + [1] * 20, 48, 2112), ([30, 0, 70, 1, 17] * 4, 544, 2080),
+    ([2] * 300, 160, 96), ([600, 0, 3900], 32, 64), ([5] * 130 + [40] * 20, 96, 1056), ([33] * 9, 272, 8192)])
+def test_w4_gemm_many_row_blocks(lens, N, K, swiglu):
+    """More row blocks than get workgroups of their own: few and many weight tiles, fewer and more blocks than groups,
+    groups of many blocks between groups of one and empty ones."""
+    G = len(lens)
+    offs = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    rows = int(offs[-1])
+    say(f"w4_gemm {rows} rows in {G} groups N={N} K={K} swiglu={swiglu}")
+    q, s = _weights(600 + K, G, N, K)
+    src = 50
+    a = I.gen_normal(601, (src, K), 1.0).to(DEV)
+    gather = np.random.default_rng(602).integers(0, src, rows).astype(np.int32)
+    want, tol = _reference(np64(a), decode(q, s), offs, gather, swiglu)
+    out = torch.full((rows + 1, want.shape[1]), 9.0, device=DEV)
+    M().moe_w4_gemm(a, q, s, torch.from_numpy(offs).to(DEV), 0, G, rows, out, a_rows=torch.from_numpy(gather).to(DEV),
+                    swiglu=swiglu)
+    got = np64(out)
+    assert np.all(np.abs(got[:rows] - want) <= tol * 1.01 + 1e-30) and np.all(got[rows:] == 9.0)
+
+
 def test_w4_gemm_group_range_and_tail():
     """A sub-range of the groups (rows relative to its first), and the last groups' f32 rows in their own output."""
     lens, N, K = [4, 0, 21, 3, 40, 6], 80, 192
