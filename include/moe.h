@@ -435,9 +435,8 @@ moe_status moe_router_wgrad(const uint16_t* x, const int32_t* sorted_token,
  *
  * In this section rows may have any width and start at any element (pointers and leading
  * dimensions need only the alignment of one element) unless a call says otherwise; outputs must
- * not overlap inputs.  A call takes up to 2^35 elements less a few thousand (a launch of 2^32 lanes of
- * 8; rows count as whole 1x128 tiles, in moe_norm and the combine as whole workgroups of 64 lanes
- * or more); MOE_ERR_SHAPE past that.
+ * not overlap inputs.  A call takes about 2^35 elements at most (a launch of 2^32 lanes of 8; short
+ * rows count as whole 1x128 tiles, in the combine as 64 lanes); MOE_ERR_SHAPE past that.
  * ==================================================================================== */
 
 /* moe_norm -- y = xhat * weight + bias, xhat = (x - mean) * rstd, per row, in fp32:

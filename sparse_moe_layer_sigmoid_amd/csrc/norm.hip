@@ -22,6 +22,10 @@
 //    workgroup order, so the result does not depend on timing.  4096 x 7168 from bf16 x, f32 dy and
 //    dx: 61 us (4.8 TB/s); 16384 x 7168 from the checkpoint, bf16: 120 us (4.9 TB/s, the rate of a
 //    large copy).
+//  * Rows of up to 512 elements: 16, 32 or 64 lanes hold a row, so a workgroup takes several, their sums
+//    stay inside a wave, and the backward adds its 16 to 64 rows' dw and db through LDS before it writes
+//    one partial row.  65536 x 64 bf16: 7 us (24 us with a workgroup per row), x 256: 15 us (26 us);
+//    backward 65536 x 128 bf16: 15 us (37 us), 32768 x 512: 24 us (32 us).
 #include "abi_common.h"
 #include "device_common.h"
 #include "rows_common.h"
@@ -30,6 +34,7 @@ namespace moe {
 namespace {
 
 constexpr int kMaxNormD = 16384;  // 1024 lanes x 2 chunks of 8
+constexpr int kNarrow = 256;      // lanes of a forward workgroup of several rows
 
 enum { SRC_BF16 = ROW_BF16, SRC_F32 = ROW_F32, SRC_CKPT = 2 };
 
@@ -45,7 +50,19 @@ __device__ __forceinline__ float block_sum(float v, float* red, int nwaves) {
   return s;
 }
 
+// Sums v over the L neighbouring lanes of a row (16: a DPP row, 32, or 64: the wave).
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  if constexpr (L == 64) return wave_sum(v);
+  v += __uint_as_float(row_ror<8>(__float_as_uint(v)));
+  v += __uint_as_float(row_ror<4>(__float_as_uint(v)));
+  v += __uint_as_float(row_ror<2>(__float_as_uint(v)));
+  v += __uint_as_float(row_ror<1>(__float_as_uint(v)));
+  return L == 16 ? v : v + __shfl_xor(v, 16, kWave);
+}
+
 struct NormArgs {
+  int rows;
   const void* x;
   int64_t ldx_b;  // bytes
   const void* w;
@@ -64,11 +81,18 @@ struct NormArgs {
   int tiles;  // scales per row: ceil(d / 128)
 };
 
-template <int XT, int NV, bool FULL>
-__global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
+// L: lanes of a row, 0 for the whole workgroup.
+template <int XT, int NV, bool FULL, int L>
+__global__ __launch_bounds__(L ? kNarrow : 1024) void norm_kernel(NormArgs p) {
   __shared__ float red[2][16];
-  const int64_t r = blockIdx.x;
-  const int t = threadIdx.x, G = blockDim.x, nw = G >> 6;
+  constexpr int D = L ? L : 1;
+  const int64_t r = L ? (int64_t)blockIdx.x * (kNarrow / D) + threadIdx.x / D : blockIdx.x;
+  const int t = L ? threadIdx.x % D : threadIdx.x, G = L ? L : blockDim.x, nw = G >> 6;
+  if (L && r >= p.rows) return;  // the row's lanes together
+  auto row_sum = [&](float v, float* red) __attribute__((always_inline)) {
+    if constexpr (L) return lanes_sum<L>(v);
+    else return block_sum(v, red, nw);
+  };
   const char* xr = static_cast<const char*>(p.x) + r * p.ldx_b;
   float f[NV][8];
 #pragma unroll
@@ -92,7 +116,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) s = fmaf(f[i][e], down, s);
-    mean = block_sum(s, red[0], nw) * up;
+    mean = row_sum(s, red[0]) * up;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (t + i * G) * 8;
@@ -105,7 +129,7 @@ __global__ __launch_bounds__(1024) void norm_kernel(NormArgs p) {
   for (int i = 0; i < NV; ++i)
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(f[i][e] * down, f[i][e], ss);
-  const float rstd = 1.0f / sqrtf(block_sum(ss, red[1], nw) * up + p.eps);
+  const float rstd = 1.0f / sqrtf(row_sum(ss, red[1]) * up + p.eps);
   if (t == 0) {
     if (p.mean) p.mean[r] = mean;
     if (p.rstd) p.rstd[r] = rstd;
@@ -180,12 +204,15 @@ __device__ __forceinline__ void keep(RawX<SRC_CKPT>& r) { asm volatile("" : "+v"
 template <int SRC>
 __device__ __forceinline__ void keep(RawX<SRC>& r) { keep(r.v); }
 
-// LANES: the largest workgroup.  Up to 512 lanes (d <= 8192) a wave may have more than 128 registers,
+// L: lanes of a row, 0 for the whole workgroup.  LANES: the largest workgroup.  Up to 512 lanes (d <= 8192) a wave may have more than 128 registers,
 // which the kernel takes where x and dy are f32: 4096 x 7168 72 us, 95 us held to 128.
-template <int SRC, int DYT, int NV, bool FULL, int LANES>
+template <int SRC, int DYT, int NV, bool FULL, int L, int LANES>
 __global__ __launch_bounds__(LANES) void norm_backward_kernel(NormBwdArgs p) {
+  constexpr int D = L ? L : 1;
+  constexpr int ROWS = L ? LANES / D : 1;  // of a workgroup at a time
   __shared__ float red[2][2][16];
-  const int t = threadIdx.x, G = blockDim.x, nw = G >> 6;
+  __shared__ float s_part[L ? ROWS : 1][L ? L * 8 + 1 : 1];
+  const int t = L ? threadIdx.x % D : threadIdx.x, G = L ? L : blockDim.x, nw = G >> 6;
   const float inv_d = 1.0f / (float)p.d;
   float w[NV][8], aw[NV][8], ab[NV][8];
 #pragma unroll
@@ -220,9 +247,10 @@ __global__ __launch_bounds__(LANES) void norm_backward_kernel(NormBwdArgs p) {
     nmean = p.mean ? p.mean[r] : 0.f;
     nrstd = p.rstd[r];
   };
-  int64_t r = blockIdx.x;
+  int64_t r = L ? (int64_t)blockIdx.x * ROWS + threadIdx.x / D : blockIdx.x;
+  const int step = gridDim.x * ROWS;
   if (r < p.rows) fetch(r);
-  for (int it = 0; r < p.rows; r += gridDim.x, ++it) {
+  for (int it = 0; r < p.rows; r += step, ++it) {
     const float mean = nmean, rstd = nrstd;
     Raw8<DYT> dy[NV];
     RawX<SRC> x[NV];
@@ -259,10 +287,10 @@ __global__ __launch_bounds__(LANES) void norm_backward_kernel(NormBwdArgs p) {
         }
       }
     }
-    if (r + gridDim.x < p.rows) fetch(r + gridDim.x);
-    s1 = wave_sum(s1);
-    s2 = wave_sum(s2);
-    if (nw > 1) {
+    if (r + step < p.rows) fetch(r + step);
+    s1 = lanes_sum<L ? L : 64>(s1);
+    s2 = lanes_sum<L ? L : 64>(s2);
+    if (!L && nw > 1) {
       float(*rd)[16] = red[it & 1];
       if ((t & 63) == 0) {
         rd[0][t >> 6] = s1;
@@ -290,6 +318,23 @@ __global__ __launch_bounds__(LANES) void norm_backward_kernel(NormBwdArgs p) {
         store8_any<FULL>(p.dx_dtype, dxr, c, p.d, g);
       }
     }
+  }
+  if constexpr (L > 0) {  // the rows' sums through LDS, added in row order
+    for (int which = 0; which < 2; ++which) {
+      float* part = which ? p.part_b : p.part_w;
+      if (!part) continue;
+      __syncthreads();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s_part[threadIdx.x / D][t * 8 + e] = which ? ab[0][e] : aw[0][e];
+      __syncthreads();
+      for (int c = threadIdx.x; c < p.d; c += LANES) {
+        float v = 0.f;
+#pragma unroll 8
+        for (int k = 0; k < ROWS; ++k) v += s_part[k][c];
+        part[(int64_t)blockIdx.x * p.d + c] = v;
+      }
+    }
+    return;
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i) {
@@ -344,10 +389,12 @@ void launch_reduce(const float* pw, const float* pb, int n, int d, float* dw, fl
 int norm_chunks_per_lane(int rows, int d) {
   const int chunks = (d + 7) / 8;
   if (rows <= 256) return chunks <= 1024 ? 1 : 2;
-  return chunks <= 64 ? 1 : chunks <= 128 ? 2 : 4;
+  return chunks <= 128 ? 2 : 4;
 }
 
-int norm_bwd_chunks_per_lane(int d) { return (d + 7) / 8 <= 64 ? 1 : 2; }
+// Rows of up to 64 chunks take 16, 32 or 64 lanes of one chunk each, several rows to a workgroup.
+int narrow_lanes(int d) { return d <= 128 ? 16 : d <= 256 ? 32 : d <= 512 ? 64 : 0; }
+constexpr int kNarrowBwd = 1024;  // lanes of such a workgroup in the backward
 
 int group_threads(int d, int nv) {
   const int chunks = (d + 7) / 8;
@@ -358,26 +405,48 @@ int group_threads(int d, int nv) {
 // so each should walk 16 rows or more, down to one workgroup per CU: 4096 rows of 7168, 256
 // workgroups 61 us, 512 70 us; 16384 rows, 256 143 us, 512 (32 rows each) 121 us.
 int norm_bwd_grid(int rows, int d) {
-  const int threads = group_threads(d, norm_bwd_chunks_per_lane(d));
+  if (const int lanes = narrow_lanes(d)) {
+    const int at_once = kNarrowBwd / lanes;
+    return rows < 256 * at_once ? (rows + at_once - 1) / at_once : 256;
+  }
+  const int threads = group_threads(d, 2);
   const int per_cu = threads >= 448 ? 2 : threads >= 256 ? 4 : threads >= 128 ? 8 : 16;
   int n = rows / 16;
   n = n < 256 ? 256 : n > 256 * per_cu ? 256 * per_cu : n;
   return rows < n ? rows : n;
 }
 
-template <int SRC, int DYT>
-void launch_norm_backward(const NormBwdArgs& a, int nv, int grid, int threads, hipStream_t stream) {
-  const bool full = a.d % 8 == 0;
-  auto kernel = nv == 1          ? (full ? norm_backward_kernel<SRC, DYT, 1, true, 512> : norm_backward_kernel<SRC, DYT, 1, false, 512>)
-                : threads <= 512 ? (full ? norm_backward_kernel<SRC, DYT, 2, true, 512> : norm_backward_kernel<SRC, DYT, 2, false, 512>)
-                                 : (full ? norm_backward_kernel<SRC, DYT, 2, true, 1024> : norm_backward_kernel<SRC, DYT, 2, false, 1024>);
+template <int SRC, int DYT, bool FULL>
+void launch_norm_backward_as(const NormBwdArgs& a, int grid, hipStream_t stream) {
+  const int lanes = narrow_lanes(a.d), threads = lanes ? kNarrowBwd : group_threads(a.d, 2);
+  auto kernel = lanes == 16      ? norm_backward_kernel<SRC, DYT, 1, FULL, 16, kNarrowBwd>
+                : lanes == 32    ? norm_backward_kernel<SRC, DYT, 1, FULL, 32, kNarrowBwd>
+                : lanes == 64    ? norm_backward_kernel<SRC, DYT, 1, FULL, 64, kNarrowBwd>
+                : threads <= 512 ? norm_backward_kernel<SRC, DYT, 2, FULL, 0, 512>
+                                 : norm_backward_kernel<SRC, DYT, 2, FULL, 0, 1024>;
   kernel<<<grid, threads, 0, stream>>>(a);
 }
 
+template <int SRC, int DYT>
+void launch_norm_backward(const NormBwdArgs& a, int grid, hipStream_t stream) {
+  if (a.d % 8 == 0) launch_norm_backward_as<SRC, DYT, true>(a, grid, stream);
+  else launch_norm_backward_as<SRC, DYT, false>(a, grid, stream);
+}
+
 template <int XT, bool FULL>
-void launch_norm(const NormArgs& a, int rows, int nv, hipStream_t stream) {
-  auto kernel = nv == 1 ? norm_kernel<XT, 1, FULL> : nv == 2 ? norm_kernel<XT, 2, FULL> : norm_kernel<XT, 4, FULL>;
-  kernel<<<rows, group_threads(a.d, nv), 0, stream>>>(a);
+void launch_norm(const NormArgs& a, hipStream_t stream) {
+  if (const int lanes = narrow_lanes(a.d)) {
+    const int at_once = kNarrow / lanes, grid = (a.rows + at_once - 1) / at_once;
+    if (lanes == 16) norm_kernel<XT, 1, FULL, 16><<<grid, kNarrow, 0, stream>>>(a);
+    else if (lanes == 32) norm_kernel<XT, 1, FULL, 32><<<grid, kNarrow, 0, stream>>>(a);
+    else norm_kernel<XT, 1, FULL, 64><<<grid, kNarrow, 0, stream>>>(a);
+    return;
+  }
+  const int nv = norm_chunks_per_lane(a.rows, a.d);
+  auto kernel = nv == 1   ? norm_kernel<XT, 1, FULL, 0>
+                : nv == 2 ? norm_kernel<XT, 2, FULL, 0>
+                          : norm_kernel<XT, 4, FULL, 0>;
+  kernel<<<a.rows, group_threads(a.d, nv), 0, stream>>>(a);
 }
 
 bool row_dtype(int t) { return t == MOE_BF16 || t == MOE_F32; }
@@ -407,6 +476,7 @@ extern "C" moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const vo
               MOE_ERR_ALIGN, "moe_norm: pointers must be aligned to their elements");
   if (rows > 0) {
     NormArgs a;
+    a.rows = rows;
     a.x = x;
     a.ldx_b = ldx * row_esz(x_dtype);
     a.w = weight;
@@ -423,11 +493,11 @@ extern "C" moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const vo
     a.q = ck_q;
     a.q_scale = ck_scale;
     a.tiles = (d + 127) / 128;
-    const int nv = norm_chunks_per_lane(rows, d);
-    MOE_REQUIRE(rows <= kMaxLanes / group_threads(d, nv), MOE_ERR_SHAPE, "moe_norm: too many rows (%d)", rows);
+    const int lanes = narrow_lanes(d) ? narrow_lanes(d) : group_threads(d, norm_chunks_per_lane(rows, d));
+    MOE_REQUIRE(rows <= kMaxLanes / lanes, MOE_ERR_SHAPE, "moe_norm: too many rows (%d)", rows);
     const bool full = d % 8 == 0;
-    if (x_dtype == MOE_BF16) full ? launch_norm<ROW_BF16, true>(a, rows, nv, stream) : launch_norm<ROW_BF16, false>(a, rows, nv, stream);
-    else full ? launch_norm<ROW_F32, true>(a, rows, nv, stream) : launch_norm<ROW_F32, false>(a, rows, nv, stream);
+    if (x_dtype == MOE_BF16) full ? launch_norm<ROW_BF16, true>(a, stream) : launch_norm<ROW_BF16, false>(a, stream);
+    else full ? launch_norm<ROW_F32, true>(a, stream) : launch_norm<ROW_F32, false>(a, stream);
   }
   return check_launch("moe_norm");
 }
@@ -490,16 +560,15 @@ extern "C" moe_status moe_norm_backward(const void* dy, int dy_dtype, int64_t ld
     a.lddx_b = lddx * row_esz(dx_dtype);
     a.part_w = dweight ? (grid == 1 ? dweight : pw) : nullptr;
     a.part_b = dbias ? (grid == 1 ? dbias : pb) : nullptr;
-    const int nv = norm_bwd_chunks_per_lane(d), threads = group_threads(d, nv);
     if (ck_q) {
-      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_CKPT, ROW_BF16>(a, nv, grid, threads, stream);
-      else launch_norm_backward<SRC_CKPT, ROW_F32>(a, nv, grid, threads, stream);
+      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_CKPT, ROW_BF16>(a, grid, stream);
+      else launch_norm_backward<SRC_CKPT, ROW_F32>(a, grid, stream);
     } else if (x_dtype == MOE_BF16) {
-      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_BF16, ROW_BF16>(a, nv, grid, threads, stream);
-      else launch_norm_backward<SRC_BF16, ROW_F32>(a, nv, grid, threads, stream);
+      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_BF16, ROW_BF16>(a, grid, stream);
+      else launch_norm_backward<SRC_BF16, ROW_F32>(a, grid, stream);
     } else {
-      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_F32, ROW_BF16>(a, nv, grid, threads, stream);
-      else launch_norm_backward<SRC_F32, ROW_F32>(a, nv, grid, threads, stream);
+      if (dy_dtype == MOE_BF16) launch_norm_backward<SRC_F32, ROW_BF16>(a, grid, stream);
+      else launch_norm_backward<SRC_F32, ROW_F32>(a, grid, stream);
     }
   }
   if (grid != 1 && (dweight || dbias))  // with no rows the sums are zero

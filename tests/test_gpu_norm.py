@@ -127,7 +127,8 @@ def _ref_backward(dy, xhat, rstd, w, rms):
 def _check_backward(got, dy, xhat, rstd, w, rms, odt, T, slack):
     """slack: what xhat may be off by.  dx: two sums of at most 38 roundings, four products and differences; dw: a
     chain of the rows of one workgroup (256 workgroups or more once T is: T / 256 + 1 rows), then of the partial rows
-    (at most 256 for these T) in 16 strips, and of the strips."""
+    (at most 256 for these T) in 16 strips, and of the strips.  Rows of up to 512 columns: R = 64, 32 or 16 rows to a
+    workgroup, a lane's chain of T / (256 R) + 1 rows, then R sums, at most 256 partial rows and the strips."""
     dx, dw, db = got
     g, rdx, rdw, rdb = _ref_backward(dy, xhat, rstd, w, rms)
     s1 = np.abs(g).mean(1, keepdims=True)
@@ -135,8 +136,10 @@ def _check_backward(got, dy, xhat, rstd, w, rms, odt, T, slack):
     sx = (np.abs(g) * slack).mean(1, keepdims=True)
     tol = rstd[:, None] * (48 * U * (np.abs(g) + s1 + np.abs(xhat) * s2) + np.abs(xhat) * sx + slack * s2)
     assert np.all(np.abs(np64(dx) - rdx) <= tol + HALF[odt] * np.abs(rdx) + 1e-30)
-    assert T <= 4096
-    chain = (T / 256 + 1) + min(T, 256) / 16 + 1 + 16
+    d = dy.shape[1]
+    R = 64 if d <= 128 else 32 if d <= 256 else 16 if d <= 512 else 1
+    assert T <= 4096 or R > 1
+    chain = (T / (256 * R) + 1) + (R if R > 1 else 0) + min(T, 256) / 16 + 1 + 16
     assert np.all(np.abs(np64(dw) - rdw) <= chain * U * np.abs(dy * xhat).sum(0) + (np.abs(dy) * slack).sum(0) + 1e-30)
     if db is not None:
         assert np.all(np.abs(np64(db) - rdb) <= chain * U * np.abs(dy).sum(0) + 1e-30)
@@ -162,6 +165,35 @@ def test_norm_backward(d, rms):
         xhat = (np64(x) - m64[:, None]) * r64[:, None]
         slack = 2 * U * np.abs(xhat)  # the difference and the product
         _check_backward(got, np64(dy), xhat, r64, None if w is None else np64(w), rms, odt, T, slack)
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("T,d", [(1, 128), (15, 64), (65, 120), (64, 129), (33, 256), (31, 250), (17, 257), (16, 511), (20001, 100),
+                                 (16385, 128), (9000, 200), (8193, 256), (5000, 400), (4097, 512)])
+def test_norm_narrow(T, d, rms):
+    """Rows of up to 512 columns, several to a workgroup: short last workgroups, more rows than the backward's 256
+    workgroups take at once; the checkpoint is that of packing the f32 rows the norm gives without weights."""
+    say(f"norm narrow T={T} d={d} rms={rms}")
+    x = _rows(61, T, d, torch.bfloat16, 2)
+    dy = _rows(62, T, d, torch.float32, 0, offset=0.01)
+    w = _vec(63, d, torch.float32, 1.0)
+    b = _vec(64, d, torch.float32)
+    y, mean, rstd, _ = M().moe_norm(x, w, b, eps=1e-5, rms=rms, out_dtype=torch.float32, want_stats=True)
+    xhat32, _, _, ck = M().moe_norm(x, eps=1e-5, rms=rms, out_dtype=torch.float32, checkpoint=True)
+    x64, r64 = np64(x), np64(rstd)
+    m, r, xhat, ref = _ref_norm(x64, np64(w), np64(b), 1e-5, rms)
+    ax = np.abs(x64).mean(1)
+    tol = 100 * U * (np.abs(xhat) + (ax * r)[:, None]) * np.abs(np64(w)) + 3 * U * np.abs(ref)
+    assert np.all(np.abs(np64(y) - ref) <= tol + 1e-30)
+    assert np.all(np.abs(r64 - r) <= r * 100 * U * (1 + ax * r))
+    for got, want in zip(ck, M().fp8_ckpt_pack(xhat32)):
+        assert torch.equal(got, want)
+    got = M().moe_norm_backward(dy, x, mean, rstd, w, rms=rms, want_dbias=True)
+    xh = (x64 - (0.0 if rms else np64(mean)[:, None])) * r64[:, None]
+    _check_backward(got, np64(dy), xh, r64, np64(w), rms, torch.float32, T, 2 * U * np.abs(xh))
+    got = M().moe_norm_backward(dy, None, None, rstd, w, rms=rms, checkpoint=ck, want_dbias=True)
+    xh = np64(M().fp8_ckpt_unpack(*ck, out_dtype=torch.float32))
+    _check_backward(got, np64(dy), xh, r64, np64(w), rms, torch.float32, T, 0.0 * xh)
 
 
 @pytest.mark.parametrize("d", [1, 9, 130, 1024, 7168, 8200])
