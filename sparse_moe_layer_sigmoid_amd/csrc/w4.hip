@@ -464,9 +464,36 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
     fetch(d, pre, ahead < count);
     if (++ahead < count) advance(pre);
   }
-  for (int u = 0; u < count; u += D) {
+  // the waves' sums of tiles u .. u + n, in wave order.  D tiles' sums change hands at a time.  Two
+  // sets of buffers alternate: a wave writes a set again only after the barrier of the other, which
+  // the waves that read it have then passed.
+  auto join = [&](int u, int n) __attribute__((always_inline)) {
+    lds_barrier();
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      if (wave == ((u + i) & (NW - 1))) {
+        f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 2
+        for (int w = 0; w < NW; ++w) {
+          const f32x4 o = s_red[buf + i][w][lane];
 #pragma unroll
-    for (int d = 0; d < D; ++d) {  // past the last tile: zeros, not stored
+          for (int e = 0; e < 4; ++e) sum[e] += o[e];
+        }
+        store(sum, done);
+      }
+      if (u + i + 1 < count) advance(done);
+    }
+    buf ^= D;
+  };
+  // EARLY: leave after the last tile.  Else the ring's turn is finished with tiles that do not exist
+  // (zeros, not stored): with two tiles to a turn that costs at most one, and the exit between them
+  // costs more (gate/up of 256 tokens, 7168 inputs: 699 us, 733 us with it).  With four it is up to 20 KB
+  // of cold code that a short run does not execute (8 us calls of one to four tiles: 6 us).
+  constexpr bool EARLY = D > 2;
+  int u = 0, n = 0;
+  for (; EARLY || u < count; u += D) {
+#pragma unroll
+    for (int d = 0; d < D; ++d) {
       if (cur.g != xg || cur.rb() != xrb) {
         load_x(cur);
         xg = cur.g;
@@ -474,35 +501,18 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
       }
       const f32x4 v = tile(d, pre, ahead < count);
       if (++ahead < count) advance(pre);
-      if constexpr (NW > 1) {
-        s_red[buf + d][wave][lane] = v;
-      } else {
-        if (u + d < count) store(v, cur);
+      if constexpr (NW > 1) s_red[buf + d][wave][lane] = v;
+      else if (EARLY || u + d < count) store(v, cur);
+      if (EARLY && u + d + 1 >= count) {
+        n = d + 1;
+        break;
       }
-      if (u + d + 1 < count) advance(cur);
+      if (EARLY || u + d + 1 < count) advance(cur);
     }
-    if constexpr (NW > 1) {
-      // D tiles' sums change hands at a time.  Two sets of buffers alternate: a wave writes a set
-      // again only after the barrier of the other, which the waves that read it have then passed.
-      lds_barrier();
-      const int n = min(D, count - u);
-#pragma unroll 1
-      for (int i = 0; i < n; ++i) {
-        if (wave == ((u + i) & (NW - 1))) {  // the waves' sums, in wave order
-          f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll 2
-          for (int w = 0; w < NW; ++w) {
-            const f32x4 o = s_red[buf + i][w][lane];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) sum[e] += o[e];
-          }
-          store(sum, done);
-        }
-        if (u + i + 1 < count) advance(done);
-      }
-      buf ^= D;
-    }
+    if (EARLY && n > 0) break;
+    if constexpr (NW > 1) join(u, EARLY ? D : min(D, count - u));
   }
+  if constexpr (EARLY && NW > 1) join(u, n);
 }
 
 template <bool SWIGLU, int NT>
