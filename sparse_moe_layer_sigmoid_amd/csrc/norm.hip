@@ -25,7 +25,10 @@
 //  * Rows of up to 512 elements: 16, 32 or 64 lanes hold a row, so a workgroup takes several, their sums
 //    stay inside a wave, and the backward adds its 16 to 64 rows' dw and db through LDS before it writes
 //    one partial row.  65536 x 64 bf16: 7 us (24 us with a workgroup per row), x 256: 15 us (26 us);
-//    backward 65536 x 128 bf16: 15 us (37 us), 32768 x 512: 24 us (32 us).
+//    backward 65536 x 128 bf16: 15 us (37 us), 32768 x 512: 24 us (32 us).  The backward takes rows of up
+//    to 1024 that way, two chunks to a lane: 4096 x 768 bf16 14 us (29 us), 65536 x 640 f32 104 us (115
+//    us), but 16384 x 1024 42 us (39.5 us).  A short last chunk is read element by element: as the row's
+//    last 8 elements, shifted into place, the same kernels took 1.5 to 4 times as long.
 #include "abi_common.h"
 #include "device_common.h"
 #include "rows_common.h"
@@ -211,7 +214,7 @@ __global__ __launch_bounds__(LANES) void norm_backward_kernel(NormBwdArgs p) {
   constexpr int D = L ? L : 1;
   constexpr int ROWS = L ? LANES / D : 1;  // of a workgroup at a time
   __shared__ float red[2][2][16];
-  __shared__ float s_part[L ? ROWS : 1][L ? L * 8 + 1 : 1];
+  __shared__ float s_part[L ? ROWS : 1][L ? L * NV * 8 + 1 : 1];
   const int t = L ? threadIdx.x % D : threadIdx.x, G = L ? L : blockDim.x, nw = G >> 6;
   const float inv_d = 1.0f / (float)p.d;
   float w[NV][8], aw[NV][8], ab[NV][8];
@@ -325,7 +328,9 @@ __global__ __launch_bounds__(LANES) void norm_backward_kernel(NormBwdArgs p) {
       if (!part) continue;
       __syncthreads();
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s_part[threadIdx.x / D][t * 8 + e] = which ? ab[0][e] : aw[0][e];
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s_part[threadIdx.x / D][(t + i * L) * 8 + e] = which ? ab[i][e] : aw[i][e];
       __syncthreads();
       for (int c = threadIdx.x; c < p.d; c += LANES) {
         float v = 0.f;
@@ -394,7 +399,8 @@ int norm_chunks_per_lane(int rows, int d) {
 
 // Rows of up to 64 chunks take 16, 32 or 64 lanes of one chunk each, several rows to a workgroup.
 int narrow_lanes(int d) { return d <= 128 ? 16 : d <= 256 ? 32 : d <= 512 ? 64 : 0; }
-constexpr int kNarrowBwd = 1024;  // lanes of such a workgroup in the backward
+// The backward's workgroups of several rows: up to 1024 elements, with two chunks to a lane past 512.
+constexpr int kNarrowBwd = 1024, kNarrowBwd2 = 512;  // their lanes
 
 int group_threads(int d, int nv) {
   const int chunks = (d + 7) / 8;
@@ -402,26 +408,30 @@ int group_threads(int d, int nv) {
 }
 
 // Workgroups of the backward kernel.  Every one writes a partial row of dw and db that is read again,
-// so each should walk 16 rows or more, down to one workgroup per CU: 4096 rows of 7168, 256
-// workgroups 61 us, 512 70 us; 16384 rows, 256 143 us, 512 (32 rows each) 121 us.
+// so each should walk 16 rows or more, down to four waves per CU: 4096 rows of 7168 (7 waves), 256
+// workgroups 61 us, 512 70 us; 16384 rows, 256 143 us, 512 (32 rows each) 121 us; 4096 rows of 2048 (2
+// waves), 256 28 us, 512 22.5 us, 1024 27 us.
 int norm_bwd_grid(int rows, int d) {
-  if (const int lanes = narrow_lanes(d)) {
-    const int at_once = kNarrowBwd / lanes;
-    return rows < 256 * at_once ? (rows + at_once - 1) / at_once : 256;
+  if (d <= 1024) {
+    const int at_once = d <= 512 ? kNarrowBwd / narrow_lanes(d) : kNarrowBwd2 / 64, most = d <= 512 ? 256 : 512;
+    return rows < most * at_once ? (rows + at_once - 1) / at_once : most;
   }
   const int threads = group_threads(d, 2);
-  const int per_cu = threads >= 448 ? 2 : threads >= 256 ? 4 : threads >= 128 ? 8 : 16;
+  const int per_cu = threads >= 448 ? 2 : threads >= 256 ? 4 : 8;
   int n = rows / 16;
-  n = n < 256 ? 256 : n > 256 * per_cu ? 256 * per_cu : n;
+  const int least = threads < 256 ? 256 * 256 / threads : 256;
+  n = n < least ? least : n > 256 * per_cu ? 256 * per_cu : n;
   return rows < n ? rows : n;
 }
 
 template <int SRC, int DYT, bool FULL>
 void launch_norm_backward_as(const NormBwdArgs& a, int grid, hipStream_t stream) {
-  const int lanes = narrow_lanes(a.d), threads = lanes ? kNarrowBwd : group_threads(a.d, 2);
+  const int lanes = narrow_lanes(a.d);
+  const int threads = lanes ? kNarrowBwd : a.d <= 1024 ? kNarrowBwd2 : group_threads(a.d, 2);
   auto kernel = lanes == 16      ? norm_backward_kernel<SRC, DYT, 1, FULL, 16, kNarrowBwd>
                 : lanes == 32    ? norm_backward_kernel<SRC, DYT, 1, FULL, 32, kNarrowBwd>
                 : lanes == 64    ? norm_backward_kernel<SRC, DYT, 1, FULL, 64, kNarrowBwd>
+                : a.d <= 1024    ? norm_backward_kernel<SRC, DYT, 2, FULL, 64, kNarrowBwd2>
                 : threads <= 512 ? norm_backward_kernel<SRC, DYT, 2, FULL, 0, 512>
                                  : norm_backward_kernel<SRC, DYT, 2, FULL, 0, 1024>;
   kernel<<<grid, threads, 0, stream>>>(a);

@@ -127,8 +127,8 @@ def _ref_backward(dy, xhat, rstd, w, rms):
 def _check_backward(got, dy, xhat, rstd, w, rms, odt, T, slack):
     """slack: what xhat may be off by.  dx: two sums of at most 38 roundings, four products and differences; dw: a
     chain of the rows of one workgroup (256 workgroups or more once T is: T / 256 + 1 rows), then of the partial rows
-    (at most 256 for these T) in 16 strips, and of the strips.  Rows of up to 512 columns: R = 64, 32 or 16 rows to a
-    workgroup, a lane's chain of T / (256 R) + 1 rows, then R sums, at most 256 partial rows and the strips."""
+    (at most 512 for these T) in 16 strips, and of the strips.  Rows of up to 1024 columns: R = 64, 32, 16 or 8 rows to a
+    workgroup, a lane's chain of T / (256 R) + 1 rows, then R sums, at most 512 partial rows and the strips."""
     dx, dw, db = got
     g, rdx, rdw, rdb = _ref_backward(dy, xhat, rstd, w, rms)
     s1 = np.abs(g).mean(1, keepdims=True)
@@ -137,9 +137,9 @@ def _check_backward(got, dy, xhat, rstd, w, rms, odt, T, slack):
     tol = rstd[:, None] * (48 * U * (np.abs(g) + s1 + np.abs(xhat) * s2) + np.abs(xhat) * sx + slack * s2)
     assert np.all(np.abs(np64(dx) - rdx) <= tol + HALF[odt] * np.abs(rdx) + 1e-30)
     d = dy.shape[1]
-    R = 64 if d <= 128 else 32 if d <= 256 else 16 if d <= 512 else 1
+    R = 64 if d <= 128 else 32 if d <= 256 else 16 if d <= 512 else 8 if d <= 1024 else 1
     assert T <= 4096 or R > 1
-    chain = (T / (256 * R) + 1) + (R if R > 1 else 0) + min(T, 256) / 16 + 1 + 16
+    chain = (T / (256 * R) + 1) + (R if R > 1 else 0) + min(T, 512) / 16 + 1 + 16
     assert np.all(np.abs(np64(dw) - rdw) <= chain * U * np.abs(dy * xhat).sum(0) + (np.abs(dy) * slack).sum(0) + 1e-30)
     if db is not None:
         assert np.all(np.abs(np64(db) - rdb) <= chain * U * np.abs(dy).sum(0) + 1e-30)
@@ -169,10 +169,11 @@ def test_norm_backward(d, rms):
 
 @pytest.mark.parametrize("rms", [False, True])
 @pytest.mark.parametrize("T,d", [(1, 128), (15, 64), (65, 120), (64, 129), (33, 256), (31, 250), (17, 257), (16, 511), (20001, 100),
-                                 (16385, 128), (9000, 200), (8193, 256), (5000, 400), (4097, 512)])
+                                 (16385, 128), (9000, 200), (8193, 256), (5000, 400), (4097, 512), (1, 513), (9, 1024), (25, 1000), (4100, 640), (4097, 1024),
+                                 (4200, 1001)])
 def test_norm_narrow(T, d, rms):
-    """Rows of up to 512 columns, several to a workgroup: short last workgroups, more rows than the backward's 256
-    workgroups take at once; the checkpoint is that of packing the f32 rows the norm gives without weights."""
+    """Rows of up to 512 (backward: 1024) columns, several to a workgroup: short last workgroups, more rows than the
+    backward's workgroups take at once; the checkpoint is that of packing the f32 rows the norm gives without weights."""
     say(f"norm narrow T={T} d={d} rms={rms}")
     x = _rows(61, T, d, torch.bfloat16, 2)
     dy = _rows(62, T, d, torch.float32, 0, offset=0.01)
