@@ -465,7 +465,7 @@ moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const void* weight,
  *   dx      device bf16 or f32 [rows, d] out, leading dimension lddx
  *   dweight, dbias  device f32 [d] out (overwritten; zeros when rows == 0), each optional
  *   ws      device workspace of moe_norm_backward_workspace_size(rows, d) bytes, 16-byte aligned
- *           (needed for dweight or dbias); need not be initialised
+ *           (needed for dweight or dbias; 0 for few rows, and then NULL will do); need not be initialised
  * Limits: those of moe_norm. */
 size_t moe_norm_backward_workspace_size(int rows, int d);
 moe_status moe_norm_backward(const void* dy, int dy_dtype, int64_t lddy, const void* x, int x_dtype,

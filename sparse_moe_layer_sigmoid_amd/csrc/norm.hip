@@ -514,7 +514,8 @@ extern "C" moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const vo
 
 extern "C" size_t moe_norm_backward_workspace_size(int rows, int d) {
   if (rows <= 0 || d < 1 || d > moe::kMaxNormD) return 0;
-  return (size_t)2 * moe::norm_bwd_grid(rows, d) * d * sizeof(float);
+  const int grid = moe::norm_bwd_grid(rows, d);
+  return grid == 1 ? 0 : (size_t)2 * grid * d * sizeof(float);  // one workgroup's sums are the results
 }
 
 extern "C" moe_status moe_norm_backward(const void* dy, int dy_dtype, int64_t lddy, const void* x, int x_dtype,
@@ -543,14 +544,14 @@ extern "C" moe_status moe_norm_backward(const void* dy, int dy_dtype, int64_t ld
                   elem_aligned(mean, 4) && elem_aligned(rstd, 4) && elem_aligned(dweight, 4) && elem_aligned(dbias, 4),
               MOE_ERR_ALIGN, "moe_norm_backward: pointers must be aligned to their elements");
   const size_t need = moe_norm_backward_workspace_size(rows, d);
-  MOE_REQUIRE(!(dweight || dbias) || (ws && ws_bytes >= need && aligned16(ws)) || rows == 0, MOE_ERR_WORKSPACE,
+  MOE_REQUIRE(!(dweight || dbias) || need == 0 || (ws && ws_bytes >= need && aligned16(ws)), MOE_ERR_WORKSPACE,
               "moe_norm_backward: workspace %zu < %zu bytes (or NULL / unaligned)", ws_bytes, need);
   int grid = 0;
   float* pw = static_cast<float*>(ws);
   float* pb = nullptr;
   if (rows > 0) {
     grid = norm_bwd_grid(rows, d);
-    pb = pw + (size_t)grid * d;
+    if (pw) pb = pw + (size_t)grid * d;
     NormBwdArgs a;
     a.dy = dy;
     a.lddy_b = lddy * row_esz(dy_dtype);

@@ -55,8 +55,8 @@ def _norm_bwd(**kw):
     (dict(dy=None), 1), (dict(rstd=None), 1), (dict(dx=None), 1), (dict(x=None), 1), (dict(q=16), 1), (dict(q=16, s=16), 1),
     (dict(mean=None), 1), (dict(dyt=2), 3), (dict(xt=7), 3), (dict(dxt=2), 3), (dict(wt=2), 3), (dict(kind=-1), 3),
     (dict(rows=-2), 2), (dict(d=20000, lddy=20000, ldx=20000, lddx=20000), 2), (dict(lddy=60), 4), (dict(ldx=60), 4),
-    (dict(lddx=60), 4), (dict(dy=18), 4), (dict(x=17), 4), (dict(dw=18), 4), (dict(ws=None), 5), (dict(wsb=100), 5),
-    (dict(ws=8), 5),
+    (dict(lddx=60), 4), (dict(dy=18), 4), (dict(x=17), 4), (dict(dw=18), 4), (dict(rows=100, ws=None), 5),
+    (dict(rows=100, wsb=100), 5), (dict(rows=100, ws=8), 5),
 ])
 def test_norm_backward_rejects(kw, code):
     L = _lib()
@@ -67,7 +67,7 @@ def test_norm_backward_workspace_size():
     L = _lib()
     f = L.lib().moe_norm_backward_workspace_size
     assert f(0, 64) == 0 and f(-1, 64) == 0 and f(4, 0) == 0 and f(4, 16385) == 0
-    assert f(1, 64) == 2 * 64 * 4 and f(5, 2000) == 2 * 5 * 2000 * 4
+    assert f(1, 64) == 0 and f(1, 7168) == 0 and f(65, 64) == 2 * 2 * 64 * 4 and f(5, 2000) == 2 * 5 * 2000 * 4
     assert f(1 << 20, 7168) == f(1 << 21, 7168) > 0
 
 
