@@ -554,6 +554,14 @@ typedef struct {
  * left as they were. */
 moe_status moe_w4_gemm(const moe_w4_desc* desc, hipStream_t stream);
 
+/* moe_w4_gemm_bounded -- moe_w4_gemm for a caller that states how many rows its tensors hold, where the
+ * offsets are known on the device only: sorted_rows (entries of a_rows, or rows of a without it; sorted
+ * rows at or past it are not read), out_rows (of out) and tail_rows (of out_tail; not read without
+ * tail groups).  Sorted rows from the first one on that does not fit are left out, and the outputs'
+ * rows from there on are left as they were.  Counts >= 0; a tensor of no rows may be NULL. */
+moe_status moe_w4_gemm_bounded(const moe_w4_desc* desc, int64_t sorted_rows, int64_t out_rows,
+                               int64_t tail_rows, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -29,7 +29,7 @@ EXPORTS = (
     "moe_router_wgrad",
     "moe_norm", "moe_norm_backward_workspace_size", "moe_norm_backward",
     "fp8_ckpt_pack", "fp8_ckpt_unpack", "moe_swiglu_backward_ckpt", "moe_combine_backward_ckpt",
-    "w4_quant", "moe_w4_gemm",
+    "w4_quant", "moe_w4_gemm", "moe_w4_gemm_bounded",
 )
 
 _p = ctypes.c_void_p
@@ -138,6 +138,8 @@ def lib() -> ctypes.CDLL:
         L.w4_quant.argtypes = [_p, _i, _i, _i, _p, _p, _p]
         L.moe_w4_gemm.restype = _i
         L.moe_w4_gemm.argtypes = [ctypes.POINTER(MoeW4Desc), _p]
+        L.moe_w4_gemm_bounded.restype = _i
+        L.moe_w4_gemm_bounded.argtypes = [ctypes.POINTER(MoeW4Desc), _i64, _i64, _i64, _p]
         _LIB = L
     return _LIB
 
@@ -731,7 +733,8 @@ def moe_w4_gemm(a, w_q, w_scale, group_offsets, first_group: int, n_groups: int,
                 swiglu: bool = False, out_tail=None, tail_groups: int = 0):
     """moe_grouped_gemm with bf16 rows a [*, K] and 4-bit weights (w4_quant's codes [G, N, K/2] and scale
     codes [G, N, K/32]): out[r - off[first_group]] = epilogue(a[a_rows[r] or r] . W[g]^T), out bf16 or f32;
-    the last tail_groups groups write f32 rows to out_tail instead."""
+    the last tail_groups groups write f32 rows to out_tail instead.  The offsets are not read here: sorted rows from the
+    first one on that a_rows (or a), out or out_tail does not hold are left out, whatever the offsets say."""
     if not isinstance(a, torch.Tensor) or not a.is_cuda or a.dtype != torch.bfloat16:
         raise TypeError("a must be a bfloat16 GPU tensor")
     _dev(w_q, torch.uint8, "w_q")
@@ -757,7 +760,8 @@ def moe_w4_gemm(a, w_q, w_scale, group_offsets, first_group: int, n_groups: int,
         _rows(out_tail, "out_tail")
         if out_tail.dtype != torch.float32 or out_tail.shape[1] != cols:
             raise ValueError(f"out_tail must be float32 with {cols} columns")
-    if (a_rows.numel() if a_rows is not None else a.shape[0]) < m_total and first_group == 0:
+    sorted_rows = a_rows.numel() if a_rows is not None else a.shape[0]
+    if sorted_rows < m_total and first_group == 0:
         raise ValueError(f"{'a_rows' if a_rows is not None else 'a'} covers fewer than m_total={m_total} rows")
     if out.shape[0] + (out_tail.shape[0] if tail_groups else 0) < m_total:
         raise ValueError(f"the outputs hold fewer than m_total={m_total} rows")
@@ -771,5 +775,5 @@ def moe_w4_gemm(a, w_q, w_scale, group_offsets, first_group: int, n_groups: int,
         n_groups=n_groups, m_total=m_total, N=N, K=K, epilogue=MOE_EPI_SWIGLU if swiglu else MOE_EPI_NONE,
         out=out.data_ptr(), out_dtype=_ROW_DT[out.dtype], ldo=lead(out), tail_groups=tail_groups,
         out_tail=out_tail.data_ptr() if tail_groups else None, ldo_tail=lead(out_tail) if tail_groups else 0)
-    _launch(dev, "moe_w4_gemm", ctypes.byref(desc))
+    _launch(dev, "moe_w4_gemm_bounded", ctypes.byref(desc), sorted_rows, out.shape[0], out_tail.shape[0] if tail_groups else 0)
     return out

@@ -80,7 +80,11 @@ struct W4Args {
   const int32_t* offs;  // group_offsets + first_group
   int first_group;
   int n_groups;
-  int m_total;  // offsets past offs[0] + m_total count as that
+  // row counts, below 2^31 (an offset and a count add up in 32 bits): see row_limit
+  uint32_t m_total;
+  uint32_t sorted_rows;
+  uint32_t out_rows;
+  uint32_t tail_rows;
   int N;  // weight rows per group
   int K;
   int n_tiles;
@@ -104,22 +108,26 @@ __device__ __forceinline__ bf16x8_t decode_w4(uint32_t q, float scale) {
   return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
 }
 
-// Group offset i, held to the rows that the caller vouched for.
-__device__ __forceinline__ int group_offset(const W4Args& p, int i) {
-  const int first = p.offs[0];
-  return min(p.offs[i], (int)min((int64_t)first + p.m_total, (int64_t)INT32_MAX));
+// The sorted row from which nothing is read or written: the first one that the caller did not vouch for.  Where the
+// groups before the tail hold more rows than out does, that is the first row past out, and the tail is empty.
+__device__ __forceinline__ int row_limit(const W4Args& p) {
+  const uint32_t first = p.offs[0], tail = p.offs[p.tail_first];
+  const uint32_t room = tail - first > p.out_rows ? first + p.out_rows : tail + p.tail_rows;
+  return (int)min(min(first + p.m_total, p.sorted_rows), room);  // sorted_rows < 2^31
 }
+// Group offset i, held to that.
+__device__ __forceinline__ int group_offset(const W4Args& p, int limit, int i) { return min(p.offs[i], limit); }
 
 // Row blocks before each group (s_pre[g], of kMaxGroups + 1 entries) for row blocks of RB rows, built by a workgroup of THREADS lanes.
 template <int RB, int THREADS>
-__device__ __forceinline__ void row_block_prefix(const W4Args& p, int* s_pre, int* s_wsum) {
+__device__ __forceinline__ void row_block_prefix(const W4Args& p, int limit, int* s_pre, int* s_wsum) {
   constexpr int PER = kMaxGroups / THREADS;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int c[PER], sum = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int g = tid * PER + j;
-    const int len = g < p.n_groups ? group_offset(p, g + 1) - group_offset(p, g) : 0;
+    const int len = g < p.n_groups ? group_offset(p, limit, g + 1) - group_offset(p, limit, g) : 0;
     c[j] = (max(len, 0) + RB - 1) / RB;
     sum += c[j];
   }
@@ -154,11 +162,11 @@ __device__ __forceinline__ int find_group(const int* s_pre, int n_groups, int64_
 }
 
 // Stores four consecutive output columns (those below out_cols) of sorted row `row` of group g.
-__device__ __forceinline__ void store_columns(const W4Args& p, int g, int row, int base_row, int col, const f32x4& v) {
+__device__ __forceinline__ void store_columns(const W4Args& p, int limit, int g, int row, int base_row, int col, const f32x4& v) {
   const int left = p.out_cols - col;
   if (left <= 0) return;
   const bool tail = g >= p.tail_first;
-  uint8_t* orow = tail ? p.out_tail + (int64_t)(row - group_offset(p, p.tail_first)) * p.ldo_tail_b
+  uint8_t* orow = tail ? p.out_tail + (int64_t)(row - group_offset(p, limit, p.tail_first)) * p.ldo_tail_b
                        : p.out + (int64_t)(row - base_row) * p.ldo_b;
   if (tail || p.out_dtype == ROW_F32) {
     float* o = reinterpret_cast<float*>(orow) + col;
@@ -210,7 +218,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
-  const int G = p.n_groups, n_tiles = p.n_tiles;
+  const int G = p.n_groups, n_tiles = p.n_tiles, limit = row_limit(p);
 
   // prefix of the groups' row blocks, `per` consecutive groups to a lane; the lane whose groups hold
   // the workgroup's first unit says which one
@@ -218,9 +226,9 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   int step, count;  // units of this workgroup: u0, u0 + step, ...
   {
     const int per = (G + THREADS - 1) / THREADS, g0 = min(tid * per, G), g1 = min(g0 + per, G);
-    int sum = 0, o = group_offset(p, g0);
+    int sum = 0, o = group_offset(p, limit, g0);
     for (int g = g0; g < g1; ++g) {
-      const int next = group_offset(p, g + 1);
+      const int next = group_offset(p, limit, g + 1);
       s_off[g] = o;
       sum += (max(next - o, 0) + 15) >> 4;
       o = next;
@@ -525,7 +533,8 @@ __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4;
 
-  row_block_prefix<kRowBlock, 256>(p, s_pre, s_wsum);
+  const int limit = row_limit(p);
+  row_block_prefix<kRowBlock, 256>(p, limit, s_pre, s_wsum);
   const int64_t total = (int64_t)s_pre[kMaxGroups] * p.n_tiles;
   const int base_row = p.offs[0];
   const int kblocks = (p.K + 127) / 128;
@@ -536,8 +545,8 @@ __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
     const int blocks = s_pre[g + 1] - s_pre[g];
     const int local = (int)(L - (int64_t)s_pre[g] * p.n_tiles);
     const int nt = local / blocks, rb = local - nt * blocks;
-    const int row0 = group_offset(p, g) + rb * kRowBlock;
-    const int rows = min(kRowBlock, group_offset(p, g + 1) - row0);
+    const int row0 = group_offset(p, limit, g) + rb * kRowBlock;
+    const int rows = min(kRowBlock, group_offset(p, limit, g + 1) - row0);
 
     // weight rows of this lane (past N: the last one again, not stored)
     const int half = p.N / 2;
@@ -637,7 +646,7 @@ __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) v[e] = silu(v[e]) * u[e];
           }
-          store_columns(p, g, row0 + m * 16 + r, base_row, nt * OC + c4, v);
+          store_columns(p, limit, g, row0 + m * 16 + r, base_row, nt * OC + c4, v);
         }
       }
     };
@@ -690,10 +699,16 @@ extern "C" moe_status w4_quant(const uint16_t* w, int n_mats, int n, int k, uint
 }
 
 extern "C" moe_status moe_w4_gemm(const moe_w4_desc* d, hipStream_t stream) {
+  return moe_w4_gemm_bounded(d, INT64_MAX, INT64_MAX, INT64_MAX, stream);
+}
+
+extern "C" moe_status moe_w4_gemm_bounded(const moe_w4_desc* d, int64_t sorted_rows, int64_t out_rows, int64_t tail_rows,
+                                          hipStream_t stream) {
   using namespace moe;
   clear_error();
   MOE_REQUIRE(d != nullptr, MOE_ERR_NULL, "moe_w4_gemm: desc is NULL");
-  MOE_REQUIRE(d->w_q && d->w_scale && d->group_offsets && (d->m_total == 0 || (d->a && (d->out || d->tail_groups == d->n_groups))),
+  MOE_REQUIRE(d->w_q && d->w_scale && d->group_offsets && (d->m_total == 0 || sorted_rows == 0 ||
+                  (d->a && (d->out || out_rows == 0 || d->tail_groups == d->n_groups))),
               MOE_ERR_NULL, "moe_w4_gemm: a, w_q, w_scale, group_offsets and out are required");
   MOE_REQUIRE(d->epilogue == MOE_EPI_NONE || d->epilogue == MOE_EPI_SWIGLU, MOE_ERR_DTYPE,
               "moe_w4_gemm: unknown epilogue %d", d->epilogue);
@@ -704,6 +719,9 @@ extern "C" moe_status moe_w4_gemm(const moe_w4_desc* d, hipStream_t stream) {
               "moe_w4_gemm: n_groups=%d (1..%d) first_group=%d", d->n_groups, kMaxGroups, d->first_group);
   MOE_REQUIRE(d->m_total >= 0 && d->m_total < ((int64_t)1 << 31), MOE_ERR_SHAPE, "moe_w4_gemm: m_total=%lld",
               (long long)d->m_total);
+  MOE_REQUIRE(sorted_rows >= 0 && out_rows >= 0 && tail_rows >= 0, MOE_ERR_SHAPE,
+              "moe_w4_gemm: negative counts of rows (%lld sorted, %lld of out, %lld of out_tail)", (long long)sorted_rows,
+              (long long)out_rows, (long long)tail_rows);
   MOE_REQUIRE(d->K >= kGroup && d->K % kGroup == 0 && d->N >= 1 && (!swiglu || d->N % 2 == 0), MOE_ERR_SHAPE,
               "moe_w4_gemm: K=%d must be a positive multiple of %d, N=%d positive%s", d->K, kGroup, d->N,
               swiglu ? " and even" : "");
@@ -717,12 +735,12 @@ extern "C" moe_status moe_w4_gemm(const moe_w4_desc* d, hipStream_t stream) {
   MOE_REQUIRE(d->ldo >= out_cols && (reinterpret_cast<uintptr_t>(d->out) & (uintptr_t)(osz - 1)) == 0, MOE_ERR_ALIGN,
               "moe_w4_gemm: ldo=%lld must be >= %d and out aligned to its elements", (long long)d->ldo, out_cols);
   if (d->tail_groups > 0) {
-    MOE_REQUIRE(d->m_total == 0 || d->out_tail, MOE_ERR_NULL, "moe_w4_gemm: out_tail is NULL");
+    MOE_REQUIRE(d->m_total == 0 || sorted_rows == 0 || tail_rows == 0 || d->out_tail, MOE_ERR_NULL, "moe_w4_gemm: out_tail is NULL");
     MOE_REQUIRE(d->ldo_tail >= out_cols && (reinterpret_cast<uintptr_t>(d->out_tail) & 3u) == 0, MOE_ERR_ALIGN,
                 "moe_w4_gemm: ldo_tail=%lld must be >= %d and out_tail 4-byte aligned", (long long)d->ldo_tail, out_cols);
   }
   MOE_REQUIRE((int64_t)d->N * (d->K / 2) < ((int64_t)1 << 31), MOE_ERR_SHAPE, "moe_w4_gemm: one W[g] exceeds 2 GiB");
-  if (d->m_total == 0) return MOE_OK;
+  if (d->m_total == 0 || sorted_rows == 0) return MOE_OK;
   W4Args a;
   a.a = static_cast<const uint8_t*>(d->a);
   a.a_rows = d->a_rows;
@@ -732,7 +750,11 @@ extern "C" moe_status moe_w4_gemm(const moe_w4_desc* d, hipStream_t stream) {
   a.offs = d->group_offsets + d->first_group;
   a.first_group = d->first_group;
   a.n_groups = d->n_groups;
-  a.m_total = (int)d->m_total;
+  const auto count = [](int64_t n) { return (uint32_t)(n < INT32_MAX ? n : INT32_MAX); };  // no offset is larger
+  a.m_total = count(d->m_total);
+  a.sorted_rows = count(sorted_rows);
+  a.out_rows = count(out_rows);
+  a.tail_rows = d->tail_groups > 0 ? count(tail_rows) : INT32_MAX;
   a.N = d->N;
   a.K = d->K;
   a.out_cols = out_cols;

@@ -305,6 +305,41 @@ def test_w4_gemm_refuses_short_tensors():
                             tail_groups=c["tail_groups"], out_tail=c["out_tail"])
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("N", [48, 50])
+def test_w4_gemm_holds_to_its_tensors(N, swiglu):
+    """Rows that a_rows, a, out or out_tail does not hold are neither read nor written, whatever the offsets say
+    (streaming and general kernel): a sub-range of the groups with too few rows before it, and outputs that are long
+    enough together but not each.  Every tensor is the head of a longer one, whose rest has to stay as it was."""
+    lens, K = [4, 0, 21, 3, 40, 6], 192
+    offs = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    rows, G, cols = int(offs[-1]), len(lens), N // 2 if swiglu else N
+    q, s = _weights(590, G, N, K)
+    a = I.gen_normal(591, (rows, K), 1.0).to(DEV)
+    od, ident = torch.from_numpy(offs).to(DEV), torch.arange(rows, dtype=torch.int32, device=DEV)
+    want, tol = _reference(np64(a), decode(q, s), offs, np.arange(rows), swiglu)
+
+    def check(got, want, tol, n, half=0.0):
+        g = np64(got)
+        assert np.all(np.abs(g[:n] - want[:n]) <= (tol * 1.01 + half * np.abs(want))[:n] + 1e-30)
+        assert np.all(g[n:] == 9.0)
+
+    for have in (0, 3, 24, 27, 29, 69):  # sorted rows that are there; the range below is rows 4 to 68
+        for kw in (dict(a_rows=ident[:have]), dict()):
+            out = torch.full((64, cols), 9.0, device=DEV)
+            M().moe_w4_gemm(a if kw else a[:have], q, s, od, 2, 3, 64, out, swiglu=swiglu, **kw)
+            check(out, want[4:], tol[4:], min(max(have - 4, 0), 64))
+    for tails in (1, 2, 6):
+        t0 = int(offs[G - tails])
+        for main in sorted({0, 1, t0 // 2, max(t0 - 1, 0), t0, t0 + 1, rows}):
+            tail = rows - main
+            out = torch.full((rows + 8, cols), 9.0, dtype=torch.bfloat16, device=DEV)
+            rest = torch.full((rows + 8, cols), 9.0, device=DEV)
+            M().moe_w4_gemm(a, q, s, od, 0, G, rows, out[:main], out_tail=rest[:tail], tail_groups=tails, swiglu=swiglu)
+            check(out, want, tol, min(main, t0), 2.0 ** -8)
+            check(rest, want[t0:], tol[t0:], 0 if main < t0 else min(tail, rows - t0))
+
+
 def test_w4_gemm_two_streams_at_once():
     """Calls that run at the same time keep to themselves (the operator has no workspace)."""
     lens, N, K = [1, 0, 40, 3], 2048, 2048

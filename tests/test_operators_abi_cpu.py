@@ -125,6 +125,18 @@ def test_w4_gemm_rejects(kw, code):
     assert L.lib().moe_w4_gemm(None, None) == 1
 
 
+@pytest.mark.parametrize("counts", [(-1, 4, 4), (4, -1, 4), (4, 4, -1)])
+def test_w4_gemm_bounded_rejects(counts):
+    """Negative counts of rows; the descriptor's own refusals are moe_w4_gemm's."""
+    L = _lib()
+    d = L.MoeW4Desc(a=16, lda=64, w_q=16, w_scale=16, group_offsets=16, n_groups=4, m_total=10, N=32, K=64, out=16, ldo=32)
+    assert L.lib().moe_w4_gemm_bounded(ctypes.byref(d), *counts, None) == 2
+    assert "negative" in L.lib().moe_last_error().decode()
+    assert L.lib().moe_w4_gemm_bounded(None, 4, 4, 4, None) == 1
+    d.K = 48
+    assert L.lib().moe_w4_gemm_bounded(ctypes.byref(d), 4, 4, 4, None) == 2
+
+
 def test_more_threads_than_a_launch_has():
     """A launch counts its threads in 32 bits: calls with more chunks of 8 elements than that are refused (workgroups of
     256 chunks; for the norms 16 lanes a row or more, for the combine 64)."""
