@@ -525,6 +525,15 @@ def _launch(dev, fn: str, *args):
         _check(fn, st)
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _too_large(**sizes):
+    """The C calls take these sizes as int, and ctypes would drop their upper bits without a word."""
+    name, v = max(sizes.items(), key=lambda kv: kv[1])
+    raise ValueError(f"{name}={v} does not fit 32 bits")
+
+
 _ROW_DT = {torch.bfloat16: MOE_BF16, torch.float32: MOE_F32}
 
 
@@ -564,6 +573,8 @@ def _checkpoint(q, scale, name: str):
     if q.dim() != 2:
         raise ValueError(f"{name} codes must be two-dimensional")
     rows, cols = q.shape
+    if cols > _INT_MAX:
+        _too_large(cols=cols)
     _shape(scale, (rows, (cols + 127) // 128), f"{name} scales")
     return rows, cols
 
@@ -577,6 +588,8 @@ def moe_norm(x, weight=None, bias=None, eps: float = 1e-6, rms: bool = False, ou
     [T, ceil(d/128)]), from which the backward runs without x (it implies rstd)."""
     _rows(x, "x")
     T, d = x.shape
+    if T > _INT_MAX or d > _INT_MAX:
+        _too_large(T=T, d=d)
     dev = x.device
     wdt = _vectors(d, weight, bias)
     _same_device(dev, weight=weight, bias=bias)
@@ -600,6 +613,8 @@ def moe_norm_backward(dy, x, mean, rstd, weight=None, rms: bool = False, checkpo
     forward's checkpoint with rstd.  dx has out_dtype (default: dy's dtype)."""
     _rows(dy, "dy")
     T, d = dy.shape
+    if T > _INT_MAX or d > _INT_MAX:
+        _too_large(T=T, d=d)
     dev = dy.device
     wdt = _vectors(d, weight, None)
     _dev(rstd, torch.float32, "rstd")
@@ -642,6 +657,8 @@ def fp8_ckpt_pack(x):
     [rows, cols], E8M0 scale codes u8 [rows, ceil(cols/128)])."""
     _rows(x, "x")
     rows, cols = x.shape
+    if cols > _INT_MAX:
+        _too_large(cols=cols)
     q = torch.empty(rows, cols, dtype=torch.uint8, device=x.device)
     s = torch.empty(rows, (cols + 127) // 128, dtype=torch.uint8, device=x.device)
     _launch(x.device, "fp8_ckpt_pack", _addr(x), _ROW_DT[x.dtype], rows, cols, x.stride(0), _addr(q), _addr(s))
@@ -701,6 +718,8 @@ def moe_combine_backward_ckpt(d_out, y_q, y_scale, topk_idx, topk_gate, scores, 
     _shape(pair_pos, (T, K), "pair_pos")
     if scores.dim() != 2 or scores.shape[0] != T:
         raise ValueError("scores must be [T, n_experts]")
+    if max(T, K, scores.shape[1]) > _INT_MAX:
+        _too_large(T=T, top_k=K, n_experts=scores.shape[1])
     dev = d_out.device
     _same_device(dev, codes=y_q, scales=y_scale, topk_idx=topk_idx, topk_gate=topk_gate, scores=scores, pair_pos=pair_pos)
     dy = torch.empty(T * (K + 1), d, dtype=torch.bfloat16, device=dev)
@@ -722,6 +741,8 @@ def w4_quant(w):
     if w.dim() not in (2, 3):
         raise ValueError("w must be [n, k] or [n_mats, n, k]")
     k = w.shape[-1]
+    if max(w.shape) > _INT_MAX:
+        _too_large(n_mats=w.shape[0], n=w.shape[-2], k=k)
     q = torch.empty(*w.shape[:-1], k // 2, dtype=torch.uint8, device=w.device)
     s = torch.empty(*w.shape[:-1], k // 32, dtype=torch.uint8, device=w.device)
     mats = w.shape[0] if w.dim() == 3 else 1
@@ -744,11 +765,15 @@ def moe_w4_gemm(a, w_q, w_scale, group_offsets, first_group: int, n_groups: int,
     if w_q.dim() != 3 or a.dim() != 2:
         raise ValueError("w_q must be [G, N, K/2] and a two-dimensional")
     G, N, K = w_q.shape[0], w_q.shape[1], 2 * w_q.shape[2]
+    if G > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        _too_large(G=G, N=N, K=K)
     _shape(w_scale, (G, N, K // 32), "w_scale")
     if a.shape[1] != K or (K > 1 and a.stride(1) != 1):
         raise ValueError(f"a must have contiguous rows of {K} elements")
     if first_group < 0 or n_groups < 1 or first_group + n_groups > G:
         raise ValueError(f"groups [{first_group}, {first_group + n_groups}) are not among the {G} weights")
+    if tail_groups < 0 or tail_groups > n_groups:
+        raise ValueError(f"tail_groups={tail_groups} must be in [0, n_groups={n_groups}]")
     if group_offsets.numel() < first_group + n_groups + 1:
         raise ValueError("group_offsets needs first_group + n_groups + 1 entries")
     cols = N // 2 if swiglu else N

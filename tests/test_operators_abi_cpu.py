@@ -153,6 +153,48 @@ def test_more_threads_than_a_launch_has():
         _expect(L, fn, args, 2)
 
 
+class _Sized(torch.Tensor):
+    """A tensor of any size without memory, for the binding a GPU tensor."""
+    is_cuda = True
+
+
+def _sized(*shape, dtype=torch.float32):
+    return torch.empty(shape, dtype=dtype, device="meta").as_subclass(_Sized)
+
+
+def test_binding_refuses_sizes_past_32_bits():
+    """The C calls take widths and counts as int: a size of 2^32 + n is refused and does not arrive there as n."""
+    import sparse_moe_layer_sigmoid_amd as M
+    n, u8, i32, b16 = (1 << 32) + 16, torch.uint8, torch.int32, torch.bfloat16
+    many, wide = _sized(n, 8), _sized(1, n)
+    q, s = _sized(1, n, dtype=u8), _sized(1, (n + 127) // 128, dtype=u8)
+    offs, out = _sized(3, dtype=i32), _sized(4, 32)
+    for call in (
+            lambda: M.moe_norm(many), lambda: M.moe_norm(wide),
+            lambda: M.moe_norm_backward(many, many, _sized(n), _sized(n)),
+            lambda: M.moe_norm_backward(wide, wide, _sized(1), _sized(1)),
+            lambda: M.fp8_ckpt_pack(wide), lambda: M.fp8_ckpt_unpack(q, s),
+            lambda: M.moe_swiglu_backward_ckpt(q, s, _sized(1, n // 2)),
+            lambda: M.moe_combine_backward_ckpt(
+                _sized(n, 8, dtype=b16), _sized(n, 8, dtype=u8), _sized(n, 1, dtype=u8), _sized(n, 1, dtype=i32), _sized(n, 1),
+                _sized(n, 4), _sized(n, 1, dtype=i32)),
+            lambda: M.moe_combine_backward_ckpt(
+                _sized(1, 8, dtype=b16), _sized(1, 8, dtype=u8), _sized(1, 1, dtype=u8), _sized(1, 1, dtype=i32), _sized(1, 1),
+                _sized(1, n), _sized(1, 1, dtype=i32)),
+            lambda: M.w4_quant(_sized(n, 32, dtype=b16)), lambda: M.w4_quant(_sized(n, 1, 32, dtype=b16)),
+            lambda: M.w4_quant(_sized(1, n, dtype=b16)),
+            lambda: M.moe_w4_gemm(_sized(4, 32, dtype=b16), _sized(1, n, 16, dtype=u8), _sized(1, n, 1, dtype=u8), offs, 0, 1, 4,
+                                  _sized(4, n)),
+            lambda: M.moe_w4_gemm(_sized(4, n, dtype=b16), _sized(1, 32, n // 2, dtype=u8), _sized(1, 32, n // 32, dtype=u8), offs,
+                                  0, 1, 4, out)):
+        with pytest.raises(ValueError, match="does not fit 32 bits"):
+            call()
+    a, wq, ws = _sized(4, 32, dtype=b16), _sized(2, 32, 16, dtype=u8), _sized(2, 32, 1, dtype=u8)
+    for tails in (1 << 32, 3, -1):
+        with pytest.raises(ValueError, match="tail_groups"):
+            M.moe_w4_gemm(a, wq, ws, offs, 0, 2, 4, out, out_tail=out, tail_groups=tails)
+
+
 def test_binding_refuses_cpu_tensors():
     import sparse_moe_layer_sigmoid_amd as M
     x = torch.zeros((4, 128))
