@@ -447,7 +447,10 @@ moe_status moe_router_wgrad(const uint16_t* x, const int32_t* sorted_token,
  *   y       device bf16 (RNE) or f32 [rows, d] out, leading dimension ldy
  *   mean, rstd  device f32 [rows] out, each optional (NULL)
  *   ck_q, ck_scale  NULL, or the 8-bit checkpoint of xhat out: u8 [rows, d], u8 [rows, ceil(d/128)]
- * Limits: rows >= 0; 1 <= d <= 16384; 0 <= eps, finite; ldx, ldy >= d. */
+ * Rows of any magnitude: where the squares leave the float range, the row is taken times a power of two.
+ * mean and rstd are held as f32 (a row of subnormal numbers without eps has an infinite rstd, from which
+ * the backward cannot run, although its y is right).
+ * Limits: rows >= 0; 1 <= d <= 16384; 0 <= eps < 1e30; ldx, ldy >= d. */
 moe_status moe_norm(const void* x, int x_dtype, int64_t ldx, const void* weight, const void* bias,
                     int w_dtype, int rows, int d, float eps, int kind, void* y, int y_dtype,
                     int64_t ldy, float* mean, float* rstd, uint8_t* ck_q, uint8_t* ck_scale,

@@ -64,6 +64,18 @@ __device__ __forceinline__ float lanes_sum(float v) {
   return L == 16 ? v : v + __shfl_xor(v, 16, kWave);
 }
 
+// Largest v over the workgroup or, for L lanes, the row's lanes.
+template <int L>
+__device__ __forceinline__ uint32_t row_max(uint32_t v, uint32_t* red, int nwaves) {
+#pragma unroll
+  for (int o = (L ? L : kWave) / 2; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o, kWave));
+  if (L || nwaves == 1) return v;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = v;
+  __syncthreads();
+  for (int w = 0; w < nwaves; ++w) v = max(v, red[w]);
+  return v;
+}
+
 struct NormArgs {
   int rows;
   const void* x;
@@ -88,6 +100,7 @@ struct NormArgs {
 template <int XT, int NV, bool FULL, int L>
 __global__ __launch_bounds__(L ? kNarrow : 1024) void norm_kernel(NormArgs p) {
   __shared__ float red[2][16];
+  __shared__ uint32_t red_max[16];
   constexpr int D = L ? L : 1;
   const int64_t r = L ? (int64_t)blockIdx.x * (kNarrow / D) + threadIdx.x / D : blockIdx.x;
   const int t = L ? threadIdx.x % D : threadIdx.x, G = L ? L : blockDim.x, nw = G >> 6;
@@ -97,45 +110,79 @@ __global__ __launch_bounds__(L ? kNarrow : 1024) void norm_kernel(NormArgs p) {
     else return block_sum(v, red, nw);
   };
   const char* xr = static_cast<const char*>(p.x) + r * p.ldx_b;
-  float f[NV][8];
-#pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (t + i * G) * 8;
-    if (c < p.d) {
-      values8(load8<XT, FULL>(xr, c, p.d), f[i]);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
-    }
-  }
   // values and squares are summed times 2^-k >= 1/d > 2^-k-1 (exact products), so a sum overflows only
   // where its mean nearly does
   const int k = 31 - __clz(p.d);
   const float down = pow2f(-k), up = pow2f(k) / (float)p.d;
-  float mean = 0.f;
-  if (!p.rms) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) s = fmaf(f[i][e], down, s);
-    mean = row_sum(s, red[0]) * up;
+  float f[NV][8], mean = 0.f;
+  // loads the row times 2^-e, subtracts the mean and returns the variance, the same bits in every lane of the row
+  auto take_row = [&](int e) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
       const int c = (t + i * G) * 8;
+      if (c < p.d) {
+        values8(load8<XT, FULL>(xr, c, p.d), f[i]);
+      } else {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) f[i][e] = c + e < p.d ? f[i][e] - mean : 0.f;
+        for (int e = 0; e < 8; ++e) f[i][e] = 0.f;
+      }
+    }
+    if (e != 0) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[i][j] = ldexpf(f[i][j], -e);
+    }
+    if (!p.rms) {
+      float s = 0.f;
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s = fmaf(f[i][e], down, s);
+      mean = row_sum(s, red[0]) * up;
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (t + i * G) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) f[i][e] = c + e < p.d ? f[i][e] - mean : 0.f;
+      }
+    }
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) ss = fmaf(f[i][e] * down, f[i][e], ss);
+    return row_sum(ss, red[1]) * up;
+  };
+  const float var = take_row(0);
+  float rstd = 1.0f / sqrtf(var + p.eps);
+  // Squares leave the float range where the values do not: above 2^64 they overflow, and below about 2^-56
+  // their sum loses bits, which shows unless eps covers it (rows of 1e-21 and eps = 0: rstd off by 38%).
+  // A row whose variance comes out that way is taken again times 2^-e, with largest value or eps^1/2 in [1/2, 1).
+  int e = 0;
+  if (__builtin_expect(!(var <= 0x1p120f) || (var < 0x1p-96f && p.eps < 0x1p-70f), 0)) {
+    uint32_t top = 0;
+    int at = t;
+    asm volatile("" : "+v"(at));  // else its addresses are kept in registers from the loads above on
+#pragma nounroll
+    for (int c = at * 8; c < p.d; c += G * 8) {
+      float v[8];
+      values8(load8<XT, FULL>(xr, c, p.d), v);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(v[j]) & 0x7fffffffu);
+    }
+    top = row_max<L>(top, red_max, nw);
+    // a row with an infinity or NaN, and one of zeros without eps, keep what they have
+    if (top < 0x7f800000u && (top != 0 || p.eps > 0.f)) {
+      const int ex = top ? __builtin_amdgcn_frexp_expf(__uint_as_float(top)) : -1000;
+      const int ee = p.eps > 0.f ? (__builtin_amdgcn_frexp_expf(p.eps) + 1) >> 1 : -1000;
+      e = max(ex, ee);
+      rstd = 1.0f / sqrtf(take_row(e) + ldexpf(p.eps, -2 * e));
     }
   }
-  float ss = 0.f;
-#pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(f[i][e] * down, f[i][e], ss);
-  const float rstd = 1.0f / sqrtf(row_sum(ss, red[1]) * up + p.eps);
   if (t == 0) {
-    if (p.mean) p.mean[r] = mean;
-    if (p.rstd) p.rstd[r] = rstd;
+    if (p.mean) p.mean[r] = ldexpf(mean, e);
+    if (p.rstd) p.rstd[r] = ldexpf(rstd, -e);
   }
   char* yr = static_cast<char*>(p.y) + r * p.ldy_b;
 #pragma unroll

@@ -282,6 +282,89 @@ def test_norm_large_constant_rows():
         assert np.all(np.abs(np64(db) - g.sum(0)) <= 3 * U * np.abs(g).sum(0))
 
 
+@pytest.mark.parametrize("eps", [0.0, 1e-6, 2.0 ** -100, 1e20])
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("d", [4, 64, 129, 300, 512, 600, 1000, 1024, 2055, 7168, 16384])
+def test_norm_rows_of_any_magnitude(d, rms, eps):
+    """Rows of 2^e whose squares leave the float range, between ordinary ones: against float64 within the bounds above, to
+    which come half steps of the smallest subnormal, 2^-150, for each of at most 54 roundings of a sum (of x where the row
+    is taken as it is, of x / max|x| where it is scaled) and for the output.  rstd is held as f32, so a row of subnormals
+    without eps has an infinite one, although its y does not; a row that rounds to zeros, without eps, is 0 / 0.  The ordinary rows' bits do not depend on the others."""
+    exps = [-140, -127, -120, -100, -75, -70, -65, -60, -50, -45, -36, 30, 55, 59, 61, 63, 64, 66, 80, 100, 125]
+    base = torch.clamp(I.gen_normal(85, (2 * len(exps), d), 1.0, torch.float32), -3.9, 3.9) + 0.05
+    scale = torch.ones(2 * len(exps), dtype=torch.float64)
+    scale[1::2] = torch.exp2(torch.tensor(exps, dtype=torch.float64))
+    for times, xt in ((1, torch.float32), (1, torch.bfloat16), (7, torch.float32), (7, torch.bfloat16)):
+        say(f"norm magnitudes d={d} rms={rms} eps={eps} rows={2 * len(exps) * times} {xt}")
+        plain = base.repeat(times, 1).to(xt).to(DEV)
+        x = (base.double() * scale[:, None]).float().repeat(times, 1).to(xt).to(DEV)
+        y, mean, rstd, _ = M().moe_norm(x, eps=eps, rms=rms, out_dtype=torch.float32, want_stats=True)
+        q, s = M().moe_norm(x, eps=eps, rms=rms, out_dtype=torch.bfloat16, checkpoint=True)[3]
+        x64 = np64(x)
+        e32 = float(np.float32(eps))
+        with np.errstate(divide="ignore", invalid="ignore"):
+            m, r, xhat, _ = _ref_norm(x64, None, None, e32, rms)
+        ax, top = np.abs(x64).mean(1), np.abs(x64).max(1)
+        small = 2.0 ** -142
+        if not rms:
+            assert np.all(np.abs(np64(mean) - m) <= 56 * U * ax + small * np.maximum(top, 1.0))
+        r1, fine, held = np64(rstd), np.isfinite(r), r < 2.0 ** 127.9
+        assert np.all(np.abs(r1[held] - r[held]) <= r[held] * 100 * U * (1 + (ax * r)[held]) + 2.0 ** -149)
+        assert np.all(r1[~held] > 2.0 ** 127)
+        y64 = np64(y)
+        assert np.isnan(y64[~fine]).all() and not x64[~fine].any() and (~fine).sum() <= times
+        y64, xhat, r, ax, top = y64[fine], xhat[fine], r[fine], ax[fine], top[fine]
+        tol = 100 * U * (np.abs(xhat) + (ax * r)[:, None]) + (small * r * np.maximum(top, 1.0))[:, None] + 2.0 ** -148
+        assert np.all(np.abs(y64 - xhat) <= tol)
+        for got, want in zip((q, s), M().fp8_ckpt_pack(y)):
+            assert torch.equal(got, want)
+        y1, mean1, rstd1, _ = M().moe_norm(plain, eps=eps, rms=rms, out_dtype=torch.float32, want_stats=True)
+        assert torch.equal(y[::2], y1[::2]) and torch.equal(rstd[::2], rstd1[::2])
+        assert rms or torch.equal(mean[::2], mean1[::2])
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("d", [300, 1000, 2055])
+def test_norm_special_rows_without_eps(d, rms):
+    """eps = 0: a row of zeros is 0 times infinity; an infinity makes NaN of itself (layer norm: of its row), NaN of its
+    row; huge and tiny rows beside them are as by themselves."""
+    x = I.gen_normal(86, (6, d), 1.0, torch.float32)
+    x[1] = 0.0
+    x[2, 3] = float("inf")
+    x[3, d - 1] = float("nan")
+    x[4] *= 1e30
+    x[5] *= 1e-30
+    y, _, rstd, _ = M().moe_norm(x.to(DEV), eps=0.0, rms=rms, want_stats=True)
+    y, rstd = y.cpu(), rstd.cpu()
+    assert torch.isnan(y[1]).all() and rstd[1] == float("inf") and torch.isnan(y[3]).all()
+    if rms:
+        assert rstd[2] == 0 and torch.isnan(y[2, 3]) and not y[2][torch.arange(d) != 3].any()
+    else:
+        assert torch.isnan(y[2]).all()
+    rows = x[[0, 4, 5]]
+    m, r, xhat, _ = _ref_norm(np64(rows), None, None, 0.0, rms)
+    ax = np.abs(np64(rows)).mean(1)
+    assert np.all(np.abs(np64(y[[0, 4, 5]]) - xhat) <= 100 * U * (np.abs(xhat) + (ax * r)[:, None]))
+
+
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("e", [-100, -60, 61, 100])
+def test_norm_backward_of_any_magnitude(e, rms):
+    """The backward of such rows, from x and from the checkpoint (dw and db are of ordinary size; dx is about 2^-e)."""
+    T, d = 20, 1000
+    x = (I.gen_normal(87, (T, d), 1.0, torch.float32).double() * 2.0 ** e).float().to(DEV)
+    dy = _rows(88, T, d, torch.float32, 0, offset=0.01)
+    w = _vec(89, d, torch.float32, 1.0)
+    _, mean, rstd, ck = M().moe_norm(x, w, eps=0.0, rms=rms, want_stats=True, checkpoint=True)
+    r64 = np64(rstd)
+    xh = (np64(x) - (0.0 if rms else np64(mean)[:, None])) * r64[:, None]
+    got = M().moe_norm_backward(dy, x, mean, rstd, w, rms=rms, want_dbias=True)
+    _check_backward(got, np64(dy), xh, r64, np64(w), rms, torch.float32, T, 2 * U * np.abs(xh))
+    got = M().moe_norm_backward(dy, None, None, rstd, w, rms=rms, checkpoint=ck, want_dbias=True)
+    xh = np64(M().fp8_ckpt_unpack(*ck, out_dtype=torch.float32))
+    _check_backward(got, np64(dy), xh, r64, np64(w), rms, torch.float32, T, 0.0 * xh)
+
+
 def test_norm_one_row_of_any_stride():
     """One row has no row stride: a transposed column and a row of an expanded tensor are taken like any other."""
     d = 72
