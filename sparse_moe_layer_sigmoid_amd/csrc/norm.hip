@@ -398,13 +398,14 @@ __global__ __launch_bounds__(LANES) void norm_backward_kernel(NormBwdArgs p) {
   }
 }
 
-// out[c] = sum over the n partial rows in a fixed order: 1024 / COLS strips of rows, COLS columns
-// each, then the strips in order.
-template <int COLS>
+// out[c] = sum over the n partial rows in a fixed order: 16 strips of rows, 64 columns each, then the strips in order.
+// With 16 columns and 64 strips the backward of 16384 x 4096 (1024 partial rows) takes 93.7 us, not 89.0, of 8208 x
+// 2048 (513) 41.2, not 40.3, of 4096 x 7168 (256) 49.4, not 46.5; only many rows of few columns gain: 33000 x 1025
+// (2048) 66.0, not 66.9 (bf16, dw and db, whole calls).
 __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restrict__ part_w,
                                                            const float* __restrict__ part_b, int n, int d,
                                                            float* __restrict__ dw, float* __restrict__ db) {
-  constexpr int STRIPS = 1024 / COLS;
+  constexpr int COLS = 64, STRIPS = 1024 / COLS;
   __shared__ float red[STRIPS][COLS + 1];
   const float* part = blockIdx.y == 0 ? part_w : part_b;
   float* out = blockIdx.y == 0 ? dw : db;
@@ -426,13 +427,8 @@ __global__ __launch_bounds__(1024) void norm_reduce_kernel(const float* __restri
   }
 }
 
-// Many partial rows of few columns need more strips to fill the chip (2048 x 512: 8 us with 16
-// columns to a workgroup, 14 us with 64), few of many columns fewer workgroups (64 x 7168: 4 us
-// with 64 columns, 5.5 us with 16).
 void launch_reduce(const float* pw, const float* pb, int n, int d, float* dw, float* db, hipStream_t stream) {
-  const int two = db ? 2 : 1;
-  if (n > 512) norm_reduce_kernel<16><<<dim3((d + 15) / 16, two), 1024, 0, stream>>>(pw, pb, n, d, dw, db);
-  else norm_reduce_kernel<64><<<dim3((d + 63) / 64, two), 1024, 0, stream>>>(pw, pb, n, d, dw, db);
+  norm_reduce_kernel<<<dim3((d + 63) / 64, db ? 2 : 1), 1024, 0, stream>>>(pw, pb, n, d, dw, db);
 }
 
 // Forward: chunks per lane.  Few rows: one, so that a row's loads are all in flight together (one row

@@ -197,6 +197,40 @@ def test_norm_narrow(T, d, rms):
     _check_backward(got, np64(dy), xh, r64, np64(w), rms, torch.float32, T, 0.0 * xh)
 
 
+@pytest.mark.parametrize("rms", [False, True])
+@pytest.mark.parametrize("T,d", [(8208, 2048), (16384, 2048), (9001, 3001), (33000, 1025), (16400, 1500), (8192, 4100)])
+def test_norm_backward_many_partial_rows(T, d, rms):
+    """Rows wider than 1024 in batches whose workgroups walk 16 rows or more: up to 2048 partial rows of dw and db.  A
+    lane's chain of T / n + 1 rows, then n / 16 + 1 partial rows to a strip and 16 strips; from x and from the checkpoint,
+    against sums in float64 (of the stored statistics' xhat)."""
+    n = M().lib().moe_norm_backward_workspace_size(T, d) // (8 * d)
+    say(f"norm backward {T} x {d} rms={rms}: {n} partial rows")
+    assert n > 256
+    x = _rows(65, T, d, torch.bfloat16)
+    dy = _rows(66, T, d, torch.float32, 0, offset=0.01)
+    w = _vec(67, d, torch.float32, 1.0)
+    _, mean, rstd, ck = M().moe_norm(x, w, rms=rms, want_stats=True, checkpoint=True)
+    g64, r64, w64 = dy.double(), rstd.double()[:, None], w.double()
+    chain = T / n + 1 + n / 16 + 1 + 16
+    for kind in ("x", "checkpoint"):
+        if kind == "x":
+            got = M().moe_norm_backward(dy, x, mean, rstd, w, rms=rms, want_dbias=True)
+            xh = (x.double() - (0.0 if rms else mean.double()[:, None])) * r64
+            slack = 2 * U * xh.abs()  # the difference and the product
+        else:
+            got = M().moe_norm_backward(dy, None, None, rstd, w, rms=rms, checkpoint=ck, want_dbias=True)
+            xh = M().fp8_ckpt_unpack(*ck, out_dtype=torch.float32).double()
+            slack = 0.0 * xh
+        dx, dw, db = (t.double() for t in got)
+        assert bool(((dw - (g64 * xh).sum(0)).abs() <= chain * U * (g64 * xh).abs().sum(0) + (g64.abs() * slack).sum(0)).all())
+        assert bool(((db - g64.sum(0)).abs() <= chain * U * g64.abs().sum(0)).all())
+        g = g64 * w64
+        s1, s2, sx = g.abs().mean(1, keepdim=True), (g * xh).abs().mean(1, keepdim=True), (g.abs() * slack).mean(1, keepdim=True)
+        want = r64 * (g - (0.0 if rms else g.mean(1, keepdim=True)) - xh * (g * xh).mean(1, keepdim=True))
+        tol = r64 * (48 * U * (g.abs() + s1 + xh.abs() * s2) + xh.abs() * sx + slack * s2)
+        assert bool(((dx - want).abs() <= tol).all())
+
+
 @pytest.mark.parametrize("d", [1, 9, 130, 1024, 7168, 8200])
 @pytest.mark.parametrize("rms", [False, True])
 def test_norm_backward_from_checkpoint(d, rms):
