@@ -429,9 +429,10 @@ moe_status moe_router_wgrad(const uint16_t* x, const int32_t* sorted_token,
  * E8M0 scale code per 1x128 tile, u8 [rows, ceil(cols / 128)] (the last tile of a row may be
  * short), scale = 2^(code - 127) the least 2^k with max |v| <= 448 * 2^k, k in [-127, 127], 0 for
  * a tile of zeros: the rule of fp8_quant_1x128_e8m0.  The value of a code is E4M3(code) * scale,
- * exact in bf16 (2^128, to which f32 values from 248 * 2^120 on round, is infinite there and in
- * f32).  In a tile with infinities they saturate (a code of 448 at the largest scale an
- * f32 needs, whose value is again infinite) and NaN keeps a NaN code; NaN does not enter the scale.
+ * exact in f32 and, from k = -124 on, in bf16 (in tiles of smaller k values reach under bf16's smallest
+ * step 2^-133 and are rounded to it, RNE).  2^128, to which f32 values from 248 * 2^120 on round, is
+ * infinite in both.  In a tile with infinities they saturate (a code of 448 at the largest scale an f32
+ * needs, whose value is again infinite) and NaN keeps a NaN code; NaN does not enter the scale.
  *
  * In this section rows may have any width and start at any element (pointers and leading
  * dimensions need only the alignment of one element) unless a call says otherwise; outputs must

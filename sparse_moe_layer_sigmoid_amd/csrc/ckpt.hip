@@ -4,8 +4,8 @@
 //
 // Format: E4M3 codes [rows, cols] and one E8M0 scale code per 1x128 tile [rows, ceil(cols / 128)],
 // the scale the least 2^k with amax <= 448 * 2^k.  A power of two, so that packing rounds once
-// (the scaling is exact, whatever the input type), a value code * 2^k is exact in bf16 too, and a
-// scale costs one byte: 1.008 bytes per element against 4 (f32 gate | up products) or 2 (bf16).
+// (the scaling is exact, whatever the input type), a value code * 2^k is exact in bf16 too (from k =
+// -124 on; below, it can fall between bf16's subnormals and is rounded to them), and a scale costs one byte: 1.008 bytes per element against 4 (f32 gate | up products) or 2 (bf16).
 //
 //  * fp8_ckpt_pack / fp8_ckpt_unpack: streaming passes, 8 elements per lane, 16 lanes per tile, the
 //    tile's maximum by lane rotations.  36864 x 4096 f32 packed in 128 us (5.9 TB/s of 755 MB), bf16

@@ -91,6 +91,23 @@ def test_every_code_and_scale():
     assert np.array_equal(np.isnan(got), nan) and np.array_equal(got[~nan], want[~nan])
 
 
+def test_every_code_and_scale_in_bf16():
+    """The same in bf16: one rounding to nearest even of the f32 value, and none for scales of 2^-124 or more whose value
+    stays below 2^128."""
+    q = torch.arange(256, dtype=torch.uint8).repeat(255, 1)
+    s = torch.arange(255, dtype=torch.uint8)[:, None].repeat(1, 2)
+    got = M().fp8_ckpt_unpack(q.to(DEV), s.to(DEV)).cpu()
+    v = O.e4m3_decode(q.numpy().astype(np.uint8)) * np.exp2(np.arange(255.0) - 127)[:, None]
+    with np.errstate(over="ignore"):
+        want = torch.from_numpy(v.astype(np.float32)).to(torch.bfloat16)
+    nan = torch.from_numpy(np.isnan(v))
+    assert torch.equal(torch.isnan(got), nan)
+    assert torch.equal(got.view(torch.int16)[~nan], want.view(torch.int16)[~nan])
+    exact = (~np.isnan(v)) & (np.abs(v) < 2.0 ** 128) & (np.arange(255) >= 3)[:, None]
+    assert np.array_equal(got.double().numpy()[exact], v[exact])
+    assert not np.array_equal(got.double().numpy()[:3][~np.isnan(v[:3])], v[:3][~np.isnan(v[:3])])
+
+
 @pytest.mark.parametrize("cols", [1, 9, 128, 1001, 2048])
 def test_unpack_affine(cols):
     """v * w + b rounded once each in fp32: two half steps, then bf16's."""
