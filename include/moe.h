@@ -546,9 +546,9 @@ typedef struct {
   int N;                        /* weight rows of each group (2*I for SWIGLU) */
   int K;                        /* inputs, a positive multiple of 32 */
   int epilogue;                 /* MOE_EPI_NONE or MOE_EPI_SWIGLU (N even) */
-  void* out;                    /* device output, leading dimension ldo (elements, >= output columns) */
-  int out_dtype;                /* MOE_BF16 (RNE) or MOE_F32 */
-  int64_t ldo;
+  void* out;                    /* device output, leading dimension ldo (elements, >= output columns); */
+  int out_dtype;                /* MOE_BF16 (RNE) or MOE_F32; neither read nor written (NULL, 0) where */
+  int64_t ldo;                  /* all groups are tail groups */
   int tail_groups;              /* the last tail_groups groups write f32 rows to out_tail instead, */
   void* out_tail;               /* row r to r - off[first_group + n_groups - tail_groups]; 0: none */
   int64_t ldo_tail;

@@ -732,7 +732,7 @@ extern "C" moe_status moe_w4_gemm_bounded(const moe_w4_desc* d, int64_t sorted_r
   MOE_REQUIRE(d->lda >= d->K && d->lda % 8 == 0 && aligned16(d->a), MOE_ERR_ALIGN,
               "moe_w4_gemm: lda=%lld must be >= K, a multiple of 8, and a 16-byte aligned", (long long)d->lda);
   MOE_REQUIRE(aligned16(d->w_q), MOE_ERR_ALIGN, "moe_w4_gemm: w_q must be 16-byte aligned");
-  MOE_REQUIRE(d->ldo >= out_cols && (reinterpret_cast<uintptr_t>(d->out) & (uintptr_t)(osz - 1)) == 0, MOE_ERR_ALIGN,
+  MOE_REQUIRE((d->ldo >= out_cols || d->tail_groups == d->n_groups) && (reinterpret_cast<uintptr_t>(d->out) & (uintptr_t)(osz - 1)) == 0, MOE_ERR_ALIGN,
               "moe_w4_gemm: ldo=%lld must be >= %d and out aligned to its elements", (long long)d->ldo, out_cols);
   if (d->tail_groups > 0) {
     MOE_REQUIRE(d->m_total == 0 || sorted_rows == 0 || tail_rows == 0 || d->out_tail, MOE_ERR_NULL, "moe_w4_gemm: out_tail is NULL");

@@ -125,6 +125,16 @@ def test_w4_gemm_rejects(kw, code):
     assert L.lib().moe_w4_gemm(None, None) == 1
 
 
+def test_w4_gemm_needs_no_out_where_all_groups_are_tail_groups():
+    """Without rows the call returns before a launch, so its checks are all that runs."""
+    L = _lib()
+    d = L.MoeW4Desc(a=16, lda=64, w_q=16, w_scale=16, group_offsets=16, n_groups=4, m_total=0, N=32, K=64, out_dtype=1,
+                    tail_groups=4, out_tail=16, ldo_tail=32)
+    assert L.lib().moe_w4_gemm(ctypes.byref(d), None) == 0, L.lib().moe_last_error()
+    d.tail_groups = 3
+    assert L.lib().moe_w4_gemm(ctypes.byref(d), None) == 4
+
+
 @pytest.mark.parametrize("counts", [(-1, 4, 4), (4, -1, 4), (4, 4, -1)])
 def test_w4_gemm_bounded_rejects(counts):
     """Negative counts of rows; the descriptor's own refusals are moe_w4_gemm's."""
