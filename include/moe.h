@@ -448,6 +448,8 @@ moe_status moe_router_wgrad(const uint16_t* x, const int32_t* sorted_token,
  *   y       device bf16 (RNE) or f32 [rows, d] out, leading dimension ldy
  *   mean, rstd  device f32 [rows] out, each optional (NULL)
  *   ck_q, ck_scale  NULL, or the 8-bit checkpoint of xhat out: u8 [rows, d], u8 [rows, ceil(d/128)]
+ * For d > 512 a row's sums are cut differently up to 256 rows and above, so its last bits can depend on the
+ * number of rows (and a checkpoint code at a midpoint with them); the same call gives the same bits.
  * Rows of any magnitude: where the squares leave the float range, the row is taken times a power of two.
  * mean and rstd are held as f32 (a row of subnormal numbers without eps has an infinite rstd, from which
  * the backward cannot run, although its y is right).

@@ -14,7 +14,7 @@
 //    h = silu(a) c, which the down projection's weight gradient needs, so h is not kept at all.
 //    36864 x 2048: 153 us (5.9 TB/s; 156 us with ordinary stores, 160 us with 8-byte ones).
 //  * moe_combine_backward_ckpt: moe_combine_backward from the packed expert outputs.  4096 tokens of
-//    8 experts, 7168 columns: 177 us (4.65 TB/s, two thirds of it stores), alike with 256 lanes a
+//    8 experts, 7168 columns: 175-180 us (4.65 TB/s, two thirds of it stores), alike with 256 lanes a
 //    token or non-temporal stores, 273 us with 896 lanes.
 // All are bound by HBM: a 2 GiB copy on the same card runs at 4.9 TB/s, a read-only stream at 6.1.
 #include "abi_common.h"

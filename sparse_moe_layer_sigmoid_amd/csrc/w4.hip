@@ -14,10 +14,10 @@
 // row block, weight tile) come from the device-side offsets, as in moe_grouped_gemm: only experts
 // that hold rows are read.
 //
-//  * w4_stream_kernel (K up to 8192, N a multiple of 16): the weights stream at 5.5-6 TB/s.  Widths
-//    7168 -> 4096 (SwiGLU), 257 experts of 2048: one token 33 us (140 MB; about 9 us of that is the
-//    start of the launch and its first loads), 64 tokens 566 us (3.5 GB, 6.2 TB/s), 256 tokens 700
-//    us; the down projection of 16 tokens 142 us (806 MB, 5.7 TB/s).  An expert with more than 16
+//  * w4_stream_kernel (K up to 8192, N a multiple of 16): the weights stream at 5.0-6.2 TB/s.  Widths
+//    7168 -> 4096 (SwiGLU), 257 experts of 2048: one token 32-33 us (140 MB; about 9 us of that is the
+//    start of the launch and its first loads), 64 tokens 566 us (3.5 GB, 6.2 TB/s), 256 tokens 700-724
+//    us (3.6 GB, 5.0-5.2 TB/s); the down projection of 16 tokens 137-146 us (806 MB, 5.5-5.9 TB/s).  An expert with more than 16
 //    rows is read by several workgroups, at the same time and on one XCD (802 us when they followed
 //    each other); 256 tokens with skewed routing have 310 row blocks of 229 experts.  Sharing the
 //    XCDs' work out by what a set costs instead of by units gained 2% there and lost 3% elsewhere.
