@@ -568,6 +568,61 @@ moe_status moe_w4_gemm(const moe_w4_desc* desc, hipStream_t stream);
 moe_status moe_w4_gemm_bounded(const moe_w4_desc* desc, int64_t sorted_rows, int64_t out_rows,
                                int64_t tail_rows, hipStream_t stream);
 
+/* ====================================================================================
+ * Rows and experts in 8-bit integers, one f32 scale per row: per token for activations, per output
+ * channel for weights.
+ *
+ * Format: codes int8 [rows, cols] in [-127, 127] and scale f32 [rows]; value = code * scale.  For a row
+ * of x with A = max(max |x|, 127 * 2^-126): scale = fl32(A / 127), code = RNE(127 x / A).  A row that
+ * holds an infinity or NaN has the scale NaN and codes 0.
+ * ==================================================================================== */
+
+/* i8_quant -- x (device bf16 or f32 [rows, cols], leading dimension ldx) -> codes (contiguous) and
+ * scales; weights [n_mats, n, k] are n_mats * n rows of k.  Rows may have any width and start at any
+ * element.  Limits: 0 <= rows <= 2^22 - 1; 1 <= cols <= 2^24; ldx >= cols. */
+moe_status i8_quant(const void* x, int x_dtype, int64_t rows, int cols, int64_t ldx, int8_t* q,
+                    float* scale, hipStream_t stream);
+
+/* i8_dequant -- the values code * scale as bf16 (RNE) or f32 [rows, cols], leading dimension ldo.
+ * Limits: those of i8_quant; about 2^35 elements (rows count as whole chunks of 8). */
+moe_status i8_dequant(const int8_t* q, const float* scale, int64_t rows, int cols, void* out,
+                      int out_dtype, int64_t ldo, hipStream_t stream);
+
+/* moe_i8_gemm -- for every sorted row r of group g (groups and rows as in moe_grouped_gemm):
+ *   out[r - off[first_group]] = epilogue((A[i] . W[g]^T) * (a_scale[i] * w_scale[g])),  i = a_rows[r] or r
+ * The products of codes add up exactly in 32-bit integers; the sum becomes an f32 and meets the product
+ * of the two scales: a row's result depends on that row and the weights alone, bit for bit.  SWIGLU:
+ * W[g] holds N/2 gate rows, then N/2 up rows; out = silu(a) c. */
+typedef struct {
+  const int8_t* a;              /* device rows of codes (any int8), leading dimension lda (elements) */
+  const float* a_scale;         /* device f32, one per row of a */
+  const int32_t* a_rows;        /* device i32: row of A of each sorted row, or NULL: A row r */
+  int64_t lda;
+  const int8_t* w_q;            /* device codes [G, N, K] */
+  const float* w_scale;         /* device f32 [G, N] */
+  const int32_t* group_offsets; /* device i32, at least first_group + n_groups + 1 entries, non-decreasing */
+  int first_group;
+  int n_groups;                 /* 1..1024 */
+  int64_t m_total;              /* upper bound of the rows covered by the groups: offsets past
+                                   off[first_group] + m_total count as that */
+  int N;                        /* weight rows of each group (2*I for SWIGLU) */
+  int K;                        /* inputs, a positive multiple of 16 */
+  int epilogue;                 /* MOE_EPI_NONE or MOE_EPI_SWIGLU (N even) */
+  void* out;                    /* device output, leading dimension ldo (elements, >= output columns); */
+  int out_dtype;                /* MOE_BF16 (RNE) or MOE_F32; neither read nor written (NULL, 0) where */
+  int64_t ldo;                  /* all groups are tail groups */
+  int tail_groups;              /* the last tail_groups groups write f32 rows to out_tail instead, */
+  void* out_tail;               /* row r to r - off[first_group + n_groups - tail_groups]; 0: none */
+  int64_t ldo_tail;
+  int64_t sorted_rows;          /* rows that the tensors hold, as the offsets are known on the device only: */
+  int64_t out_rows;             /* entries of a_rows (rows of a without it), rows of out, of out_tail.  Sorted */
+  int64_t tail_rows;            /* rows from the first one on that does not fit are left out, and so are the */
+} moe_i8_desc;                  /* outputs' rows from there on */
+/* Limits: m_total in [0, 2^31); K < 131072; lda >= K and a multiple of 16; a and w_q 16-byte aligned, scales
+ * and outputs aligned to their elements; outputs do not overlap inputs; one W[g] < 2 GiB.  Rows of out past the groups'
+ * last row are left as they were. */
+moe_status moe_i8_gemm(const moe_i8_desc* desc, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

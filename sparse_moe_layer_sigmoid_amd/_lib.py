@@ -30,6 +30,7 @@ EXPORTS = (
     "moe_norm", "moe_norm_backward_workspace_size", "moe_norm_backward",
     "fp8_ckpt_pack", "fp8_ckpt_unpack", "moe_swiglu_backward_ckpt", "moe_combine_backward_ckpt",
     "w4_quant", "moe_w4_gemm", "moe_w4_gemm_bounded",
+    "i8_quant", "i8_dequant", "moe_i8_gemm",
 )
 
 _p = ctypes.c_void_p
@@ -55,6 +56,15 @@ class MoeW4Desc(ctypes.Structure):
         ("a", _p), ("a_rows", _p), ("lda", _i64), ("w_q", _p), ("w_scale", _p), ("group_offsets", _p),
         ("first_group", _i), ("n_groups", _i), ("m_total", _i64), ("N", _i), ("K", _i), ("epilogue", _i),
         ("out", _p), ("out_dtype", _i), ("ldo", _i64), ("tail_groups", _i), ("out_tail", _p), ("ldo_tail", _i64),
+    ]
+
+
+class MoeI8Desc(ctypes.Structure):
+    _fields_ = [
+        ("a", _p), ("a_scale", _p), ("a_rows", _p), ("lda", _i64), ("w_q", _p), ("w_scale", _p), ("group_offsets", _p),
+        ("first_group", _i), ("n_groups", _i), ("m_total", _i64), ("N", _i), ("K", _i), ("epilogue", _i),
+        ("out", _p), ("out_dtype", _i), ("ldo", _i64), ("tail_groups", _i), ("out_tail", _p), ("ldo_tail", _i64),
+        ("sorted_rows", _i64), ("out_rows", _i64), ("tail_rows", _i64),
     ]
 
 
@@ -140,6 +150,12 @@ def lib() -> ctypes.CDLL:
         L.moe_w4_gemm.argtypes = [ctypes.POINTER(MoeW4Desc), _p]
         L.moe_w4_gemm_bounded.restype = _i
         L.moe_w4_gemm_bounded.argtypes = [ctypes.POINTER(MoeW4Desc), _i64, _i64, _i64, _p]
+        L.i8_quant.restype = _i
+        L.i8_quant.argtypes = [_p, _i, _i64, _i, _i64, _p, _p, _p]
+        L.i8_dequant.restype = _i
+        L.i8_dequant.argtypes = [_p, _p, _i64, _i, _p, _i, _i64, _p]
+        L.moe_i8_gemm.restype = _i
+        L.moe_i8_gemm.argtypes = [ctypes.POINTER(MoeI8Desc), _p]
         _LIB = L
     return _LIB
 
@@ -801,4 +817,107 @@ def moe_w4_gemm(a, w_q, w_scale, group_offsets, first_group: int, n_groups: int,
         out=out.data_ptr(), out_dtype=_ROW_DT[out.dtype], ldo=lead(out), tail_groups=tail_groups,
         out_tail=out_tail.data_ptr() if tail_groups else None, ldo_tail=lead(out_tail) if tail_groups else 0)
     _launch(dev, "moe_w4_gemm_bounded", ctypes.byref(desc), sorted_rows, out.shape[0], out_tail.shape[0] if tail_groups else 0)
+    return out
+
+
+# ----------------------------------------------------------------------------- 8-bit integers
+
+
+def i8_quant(x):
+    """Rows in 8-bit integers: x [rows, cols] bf16 or f32 (row stride may exceed cols), or weights [n_mats, n, k]
+    (contiguous) -> (codes int8 like x, scale f32, one per row): value = code * scale."""
+    if not isinstance(x, torch.Tensor) or not x.is_cuda:
+        raise TypeError("x must be a GPU tensor")
+    if x.dim() == 3:
+        if x.dtype not in _ROW_DT:
+            raise TypeError(f"x must be torch.bfloat16 or torch.float32, got {x.dtype}")
+        if not x.is_contiguous():
+            raise ValueError("x must be contiguous")
+        rows, cols, ldx = x.shape[0] * x.shape[1], x.shape[2], x.shape[2]
+    else:
+        _rows(x, "x")
+        rows, cols = x.shape
+        ldx = x.stride(0) if rows > 1 else max(x.stride(0), cols)
+    if cols > _INT_MAX:
+        _too_large(cols=cols)
+    q = torch.empty(*x.shape, dtype=torch.int8, device=x.device)
+    s = torch.empty(*x.shape[:-1], dtype=torch.float32, device=x.device)
+    _launch(x.device, "i8_quant", _addr(x), _ROW_DT[x.dtype], rows, cols, ldx, _addr(q), _addr(s))
+    return q, s
+
+
+def i8_dequant(q, scale, out_dtype=torch.bfloat16):
+    """The values code * scale of 8-bit integer rows (q int8 [rows, cols], scale f32 [rows]; or weights [n_mats, n, k] and
+    [n_mats, n]) as bf16 or f32."""
+    _dev(q, torch.int8, "q")
+    _dev(scale, torch.float32, "scale")
+    if q.dim() not in (2, 3):
+        raise ValueError("q must be [rows, cols] or [n_mats, n, k]")
+    _shape(scale, q.shape[:-1], "scale")
+    _same_device(q.device, scale=scale)
+    if out_dtype not in _ROW_DT:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    cols = q.shape[-1]
+    if cols > _INT_MAX:
+        _too_large(cols=cols)
+    out = torch.empty(*q.shape, dtype=out_dtype, device=q.device)
+    _launch(q.device, "i8_dequant", _addr(q), _addr(scale), scale.numel(), cols, _addr(out), _ROW_DT[out_dtype], cols)
+    return out
+
+
+def moe_i8_gemm(a, a_scale, w_q, w_scale, group_offsets, first_group: int, n_groups: int, m_total: int, out, a_rows=None,
+                swiglu: bool = False, out_tail=None, tail_groups: int = 0):
+    """moe_grouped_gemm on 8-bit integers: rows a int8 [*, K] with a scale each (a_scale f32 [*]), weights w_q int8 [G, N, K]
+    with a scale per channel (w_scale f32 [G, N]): out[r - off[first_group]] = epilogue(a[i] . W[g]^T * a_scale[i] *
+    w_scale[g]), i = a_rows[r] or r; out bf16 or f32; the last tail_groups groups write f32 rows to out_tail instead.  The
+    offsets are not read here: sorted rows from the first one on that a_rows (or a), out or out_tail does not hold are left
+    out, whatever the offsets say."""
+    _dev(a, torch.int8, "a", contiguous=False)
+    _dev(a_scale, torch.float32, "a_scale")
+    _dev(w_q, torch.int8, "w_q")
+    _dev(w_scale, torch.float32, "w_scale")
+    _dev(group_offsets, torch.int32, "group_offsets")
+    _rows(out, "out")
+    if w_q.dim() != 3 or a.dim() != 2:
+        raise ValueError("w_q must be [G, N, K] and a two-dimensional")
+    G, N, K = w_q.shape
+    if G > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+        _too_large(G=G, N=N, K=K)
+    _shape(w_scale, (G, N), "w_scale")
+    if a.shape[1] != K or (K > 1 and a.stride(1) != 1):
+        raise ValueError(f"a must have contiguous rows of {K} elements")
+    _shape(a_scale, (a.shape[0],), "a_scale")
+    if first_group < 0 or n_groups < 1 or first_group + n_groups > G:
+        raise ValueError(f"groups [{first_group}, {first_group + n_groups}) are not among the {G} weights")
+    if tail_groups < 0 or tail_groups > n_groups:
+        raise ValueError(f"tail_groups={tail_groups} must be in [0, n_groups={n_groups}]")
+    if group_offsets.numel() < first_group + n_groups + 1:
+        raise ValueError("group_offsets needs first_group + n_groups + 1 entries")
+    cols = N // 2 if swiglu else N
+    if out.shape[1] != cols:
+        raise ValueError(f"out must have {cols} columns, got {out.shape[1]}")
+    if a_rows is not None:
+        _dev(a_rows, torch.int32, "a_rows")
+    if tail_groups:
+        _rows(out_tail, "out_tail")
+        if out_tail.dtype != torch.float32 or out_tail.shape[1] != cols:
+            raise ValueError(f"out_tail must be float32 with {cols} columns")
+    sorted_rows = a_rows.numel() if a_rows is not None else a.shape[0]
+    if sorted_rows < m_total and first_group == 0:
+        raise ValueError(f"{'a_rows' if a_rows is not None else 'a'} covers fewer than m_total={m_total} rows")
+    if out.shape[0] + (out_tail.shape[0] if tail_groups else 0) < m_total:
+        raise ValueError(f"the outputs hold fewer than m_total={m_total} rows")
+    dev = a.device
+    _same_device(dev, a_scale=a_scale, w_q=w_q, w_scale=w_scale, group_offsets=group_offsets, out=out, a_rows=a_rows,
+                 out_tail=out_tail if tail_groups else None)
+    lead = lambda t: t.stride(0) if t.shape[0] > 1 else max(t.stride(0), t.shape[1])  # noqa: E731
+    desc = MoeI8Desc(
+        a=a.data_ptr(), a_scale=a_scale.data_ptr(), a_rows=a_rows.data_ptr() if a_rows is not None else None,
+        lda=lead(a) if a.shape[0] > 1 else K, w_q=w_q.data_ptr(), w_scale=w_scale.data_ptr(),
+        group_offsets=group_offsets.data_ptr(), first_group=first_group, n_groups=n_groups, m_total=m_total, N=N, K=K,
+        epilogue=MOE_EPI_SWIGLU if swiglu else MOE_EPI_NONE, out=out.data_ptr(), out_dtype=_ROW_DT[out.dtype], ldo=lead(out),
+        tail_groups=tail_groups, out_tail=out_tail.data_ptr() if tail_groups else None,
+        ldo_tail=lead(out_tail) if tail_groups else 0, sorted_rows=sorted_rows, out_rows=out.shape[0],
+        tail_rows=out_tail.shape[0] if tail_groups else 0)
+    _launch(dev, "moe_i8_gemm", ctypes.byref(desc))
     return out

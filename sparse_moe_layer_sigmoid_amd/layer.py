@@ -7,7 +7,8 @@ in libmoe's kernels:
           -> down grouped GEMM (routed experts to bf16 rows, the shared expert to fp32 rows)
           -> combine -> [bias update]
 
-With 4-bit weights (w4=True, for decode batches) the two GEMMs are moe_w4_gemm.
+With 4-bit weights (w4=True, for decode batches) the two GEMMs are moe_w4_gemm, with 8-bit integer ones (i8=True)
+moe_i8_gemm, each behind i8_quant of its rows.
 
 Layer definition: "DeepSeek-V3 Technical Report" (wiki summary), "DeepSeekMoE と補助損失
 なしの負荷分散" (1 shared + N routed experts, top-K by sigmoid affinity + bias, gates from
@@ -24,13 +25,14 @@ from . import _lib as L
 class MoELayer:
     def __init__(self, w_router, W13, W2, bias, top_k: int, n_group: int = 1, topk_group: int = 1,
                  fp8: bool = False, fp8_scales: str = "f32", w4: bool = False, norm: str | None = None,
-                 norm_weight=None, norm_bias=None, norm_eps: float = 1e-6):
+                 norm_weight=None, norm_bias=None, norm_eps: float = 1e-6, i8: bool = False):
         """w_router [N, d] bf16; W13 [N+1, 2I, d] bf16 (rows [0,I) gate, [I,2I) up; expert N is
         the shared one); W2 [N+1, d, I] bf16; bias [N] f32.  With fp8=True the weights are
         block-quantised once (128x128, E4M3) and the layer runs the FP8 path, with f32 tile
         scales (fp8_scales="f32") or power-of-two ones stored as E8M0 codes ("e8m0").  With w4=True
-        they are quantised once to 4 bits (E2M1, a power of two per 32 inputs) and the layer runs
-        forward only.  norm="layer" or "rms" normalises the layer's input rows first (norm_weight,
+        they are quantised once to 4 bits (E2M1, a power of two per 32 inputs), with i8=True to 8-bit
+        integers (a scale per output channel; the rows x and h get a scale each on the way, h from its
+        f32 values), and the layer runs forward only.  norm="layer" or "rms" normalises the layer's input rows first (norm_weight,
         norm_bias [d], bf16 or f32, optional): the input may then be f32 as well as bf16."""
         if fp8_scales not in ("f32", "e8m0"):
             raise ValueError(f"fp8_scales must be 'f32' or 'e8m0', got {fp8_scales!r}")
@@ -38,9 +40,10 @@ class MoELayer:
             raise ValueError(f"norm must be None, 'layer' or 'rms', got {norm!r}")
         if norm is None and (norm_weight is not None or norm_bias is not None):
             raise ValueError("norm_weight and norm_bias need norm='layer' or 'rms'")
-        if fp8 and w4:
-            raise ValueError("the experts' weights are either E4M3 (fp8) or 4-bit (w4)")
+        if fp8 + w4 + i8 > 1:
+            raise ValueError("the experts' weights are either E4M3 (fp8), 4-bit (w4) or 8-bit integers (i8)")
         self.w4 = w4
+        self.i8 = i8
         self.norm = norm
         self.norm_weight, self.norm_bias, self.norm_eps = norm_weight, norm_bias, norm_eps
         self.w_router = w_router
@@ -62,6 +65,9 @@ class MoELayer:
         elif w4:
             self.W13, self.W13_s = L.w4_quant(W13)
             self.W2, self.W2_s = L.w4_quant(W2)
+        elif i8:
+            self.W13, self.W13_s = L.i8_quant(W13)
+            self.W2, self.W2_s = L.i8_quant(W2)
         else:
             self.W13, self.W13_s = W13, None
             self.W2, self.W2_s = W2, None
@@ -78,7 +84,7 @@ class MoELayer:
         same; the gradients carry the checkpoints' rounding."""
         train = train or checkpoint
         if train:
-            if self.e8m0 or self.w4:
+            if self.e8m0 or self.w4 or self.i8:
                 raise NotImplementedError("the backward pass runs on the bf16 and the f32-scale FP8 paths")
             keep = True
         x_in, norm_buf = x, None
@@ -107,9 +113,13 @@ class MoELayer:
                                w_scale=self.W13_s, swiglu=True, out_scale=hs, out_preact=ac)
         else:
             xq = xs = hs = None
-            h = torch.empty((rows, I), dtype=torch.bfloat16, device=dev)
+            h = torch.empty((rows, I), dtype=torch.float32 if self.i8 else torch.bfloat16, device=dev)
             if self.w4:
                 L.moe_w4_gemm(x, self.W13, self.W13_s, offs, 0, N + 1, rows, h, a_rows=sorted_token, swiglu=True)
+            elif self.i8:
+                xq, xs = L.i8_quant(x)
+                L.moe_i8_gemm(xq, xs, self.W13, self.W13_s, offs, 0, N + 1, rows, h, a_rows=sorted_token, swiglu=True)
+                h, hs = L.i8_quant(h)
             else:
                 L.moe_grouped_gemm(x, self.W13, offs, 0, N + 1, rows, h, a_rows=sorted_token, swiglu=True,
                                    out_preact=ac)
@@ -123,6 +133,8 @@ class MoELayer:
         # expert's rows (the last group) to ysh (f32)
         if self.w4:
             L.moe_w4_gemm(h, self.W2, self.W2_s, offs, 0, N + 1, rows, y, out_tail=ysh, tail_groups=1)
+        elif self.i8:
+            L.moe_i8_gemm(h, hs, self.W2, self.W2_s, offs, 0, N + 1, rows, y, out_tail=ysh, tail_groups=1)
         else:
             L.moe_grouped_gemm(h, self.W2, offs, 0, N + 1, rows, y, a_scale=hs, w_scale=self.W2_s, out_tail=ysh,
                                tail_groups=1)
@@ -154,7 +166,7 @@ class MoELayer:
         the FP8 path E4M3 with 128x128 block scales (the blocks of W^T are those of W,
         transposed, so these are the forward's codes and scales in transposed order)."""
         if getattr(self, "_WT", None) is None:
-            if self.e8m0 or self.w4:
+            if self.e8m0 or self.w4 or self.i8:
                 raise NotImplementedError("the backward pass runs on the bf16 and the f32-scale FP8 paths")
             W13, W2 = self._src if self.fp8 else (self.W13, self.W2)
             G, I2, d = W13.shape
