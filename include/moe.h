@@ -55,7 +55,7 @@ enum {
   MOE_ERR_HIP = 6        /* a HIP launch reported an error */
 };
 
-enum { MOE_BF16 = 0, MOE_F32 = 1, MOE_FP8_E4M3 = 2 };
+enum { MOE_BF16 = 0, MOE_F32 = 1, MOE_FP8_E4M3 = 2, MOE_I8 = 3, MOE_FP4_E2M1 = 4 };
 enum { MOE_EPI_NONE = 0, MOE_EPI_SWIGLU = 1 };
 /* Scale formats of FP8 tensors: float32 scales, or E8M0 codes (uint8, value 2^(code-127)). */
 enum { MOE_SCALE_F32 = 0, MOE_SCALE_E8M0 = 1 };
@@ -622,6 +622,67 @@ typedef struct {
  * and outputs aligned to their elements; outputs do not overlap inputs; one W[g] < 2 GiB.  Rows of out past the groups'
  * last row are left as they were. */
 moe_status moe_i8_gemm(const moe_i8_desc* desc, hipStream_t stream);
+
+/* ====================================================================================
+ * moe_decode -- the whole layer for a few tokens (1..16), in two launches: where a token reaches its
+ * experts' weights once, the time is those weights' bytes, and what lies between the calls above (launches,
+ * rows sorted by expert, products written and read back) is most of what else there is.
+ *
+ *   xn  = bf16(norm(x)) (moe_norm's definition), or x without a norm
+ *   idx, gate = moe_route's selection on xn, all in fp64 (sums, sigmoid, selection, gates)
+ *   out = sum_k gate_k W2[idx_k] h_k + W2[N] h_N,   h_e = silu(W1[e] xn) * (W3[e] xn)
+ *
+ * with expert N the shared one (n_shared = 1; without it that term is missing).  Weights are the values
+ * that their codes and scales stand for, and xn meets them unquantised; h is held in f32 (as two bf16 parts
+ * in the products), sums are f32 in a fixed order: a token's result depends neither on the other tokens nor
+ * on timing.
+ * ==================================================================================== */
+enum { MOE_NORM_NONE = -1 };
+typedef struct {
+  const void* x;                /* device [T, d], leading dimension ldx (elements): bf16, or f32 with a norm */
+  int x_dtype;
+  int64_t ldx;
+  int T;                        /* 0..16 */
+  int d;                        /* inputs */
+  int inter;                    /* width of an expert */
+  int n_experts;                /* routed experts: 4..256, a multiple of 4 */
+  int n_shared;                 /* 0 or 1 */
+  int top_k;                    /* 1..32 */
+  int n_group, topk_group;      /* as in moe_route */
+  int norm;                     /* MOE_NORM_NONE, MOE_NORM_LAYER or MOE_NORM_RMS */
+  const void* norm_weight;      /* device [d] or NULL (ones), */
+  const void* norm_bias;        /* device [d] or NULL (zeros), */
+  int norm_dtype;               /* both bf16 or f32 */
+  float norm_eps;
+  const uint16_t* w_router;     /* device bf16 [n_experts, d] */
+  const float* bias;            /* device f32 [n_experts] */
+  int w_dtype;                  /* the experts' weights (G = n_experts + n_shared):
+                                   MOE_BF16       bf16 [G, 2*inter, d], [G, d, inter]
+                                   MOE_FP8_E4M3   the same as E4M3, scales per 128x128 block per scale_fmt
+                                   MOE_I8         the same as int8, scales f32 [G, 2*inter], [G, d]
+                                   MOE_FP4_E2M1   w4_quant's codes and scale codes */
+  int scale_fmt;                /* E4M3 only: MOE_SCALE_F32 or MOE_SCALE_E8M0 */
+  const void* w13;              /* device: inter gate rows, then inter up rows of each expert */
+  const void* w13_scale;        /* (NULL for bf16) */
+  const void* w2;
+  const void* w2_scale;
+  void* out;                    /* device [T, d] out, leading dimension ldo: MOE_BF16 (RNE) or MOE_F32 */
+  int out_dtype;
+  int64_t ldo;
+  int32_t* topk_idx;            /* device i32 [T, top_k] out, or NULL */
+  float* topk_gate;             /* device f32 [T, top_k] out, or NULL */
+  int32_t* expert_counts;       /* device i32 [n_experts] out, or NULL */
+  void* ws;                     /* device workspace of moe_decode_workspace_size() bytes, 16-byte aligned; need */
+  size_t ws_bytes;              /* not be initialised; calls that may overlap in time need distinct ones */
+} moe_decode_desc;
+/* Limits: those of moe_route on T, d, n_experts and the groups; d <= 8192; d and inter multiples of 64 (bf16)
+ * or 128 (E4M3, int8, 4 bits; E4M3 with power-of-two scales: d and inter multiples of 512); w13, w2,
+ * w_router 16-byte aligned, the rest aligned to its elements (4-bit scale codes to 4 bytes); ldx >= d, and without a norm a multiple of 8 with x
+ * 16-byte aligned; ldo >= d; one expert's w13 or w2 < 2 GiB.  T = 0 writes zero counts only.  Rows of out past T are not touched.
+ * The second launch's workgroups wait for each other's parts of h; none waits for a workgroup that has not
+ * started, and the wait ends by itself after seconds (NaN rows) should the workspace be overwritten meanwhile. */
+size_t moe_decode_workspace_size(int T, int d, int inter, int n_experts, int n_shared, int top_k);
+moe_status moe_decode(const moe_decode_desc* desc, hipStream_t stream);
 
 #ifdef __cplusplus
 }

@@ -14,10 +14,10 @@ import torch
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libmoe.so")
 
 MOE_OK, MOE_ERR_NULL, MOE_ERR_SHAPE, MOE_ERR_DTYPE, MOE_ERR_ALIGN, MOE_ERR_WORKSPACE, MOE_ERR_HIP = range(7)
-MOE_BF16, MOE_F32, MOE_FP8_E4M3 = 0, 1, 2
+MOE_BF16, MOE_F32, MOE_FP8_E4M3, MOE_I8, MOE_FP4_E2M1 = range(5)
 MOE_EPI_NONE, MOE_EPI_SWIGLU = 0, 1
 MOE_SCALE_F32, MOE_SCALE_E8M0 = 0, 1
-MOE_NORM_LAYER, MOE_NORM_RMS = 0, 1
+MOE_NORM_LAYER, MOE_NORM_RMS, MOE_NORM_NONE = 0, 1, -1
 
 EXPORTS = (
     "moe_status_str", "moe_last_error", "moe_abi_version",
@@ -30,7 +30,7 @@ EXPORTS = (
     "moe_norm", "moe_norm_backward_workspace_size", "moe_norm_backward",
     "fp8_ckpt_pack", "fp8_ckpt_unpack", "moe_swiglu_backward_ckpt", "moe_combine_backward_ckpt",
     "w4_quant", "moe_w4_gemm", "moe_w4_gemm_bounded",
-    "i8_quant", "i8_dequant", "moe_i8_gemm",
+    "i8_quant", "i8_dequant", "moe_i8_gemm", "moe_decode_workspace_size", "moe_decode",
 )
 
 _p = ctypes.c_void_p
@@ -65,6 +65,16 @@ class MoeI8Desc(ctypes.Structure):
         ("first_group", _i), ("n_groups", _i), ("m_total", _i64), ("N", _i), ("K", _i), ("epilogue", _i),
         ("out", _p), ("out_dtype", _i), ("ldo", _i64), ("tail_groups", _i), ("out_tail", _p), ("ldo_tail", _i64),
         ("sorted_rows", _i64), ("out_rows", _i64), ("tail_rows", _i64),
+    ]
+
+
+class MoeDecodeDesc(ctypes.Structure):
+    _fields_ = [
+        ("x", _p), ("x_dtype", _i), ("ldx", _i64), ("T", _i), ("d", _i), ("inter", _i), ("n_experts", _i), ("n_shared", _i),
+        ("top_k", _i), ("n_group", _i), ("topk_group", _i), ("norm", _i), ("norm_weight", _p), ("norm_bias", _p),
+        ("norm_dtype", _i), ("norm_eps", _f), ("w_router", _p), ("bias", _p), ("w_dtype", _i), ("scale_fmt", _i),
+        ("w13", _p), ("w13_scale", _p), ("w2", _p), ("w2_scale", _p), ("out", _p), ("out_dtype", _i), ("ldo", _i64),
+        ("topk_idx", _p), ("topk_gate", _p), ("expert_counts", _p), ("ws", _p), ("ws_bytes", _sz),
     ]
 
 
@@ -156,6 +166,10 @@ def lib() -> ctypes.CDLL:
         L.i8_dequant.argtypes = [_p, _p, _i64, _i, _p, _i, _i64, _p]
         L.moe_i8_gemm.restype = _i
         L.moe_i8_gemm.argtypes = [ctypes.POINTER(MoeI8Desc), _p]
+        L.moe_decode_workspace_size.restype = _sz
+        L.moe_decode_workspace_size.argtypes = [_i, _i, _i, _i, _i, _i]
+        L.moe_decode.restype = _i
+        L.moe_decode.argtypes = [ctypes.POINTER(MoeDecodeDesc), _p]
         _LIB = L
     return _LIB
 
@@ -921,3 +935,90 @@ def moe_i8_gemm(a, a_scale, w_q, w_scale, group_offsets, first_group: int, n_gro
         tail_rows=out_tail.shape[0] if tail_groups else 0)
     _launch(dev, "moe_i8_gemm", ctypes.byref(desc))
     return out
+
+
+# ----------------------------------------------------------------------------- the whole layer for a few tokens
+
+_NORMS = {None: MOE_NORM_NONE, "layer": MOE_NORM_LAYER, "rms": MOE_NORM_RMS}
+
+
+def _expert_weights(W, scale, n: int, k: int, G: int, name: str):
+    """(w_dtype, scale_fmt) of one of the experts' weight tensors, from its types and shapes."""
+    if not isinstance(W, torch.Tensor) or not W.is_cuda:
+        raise TypeError(f"{name} must be a GPU tensor")
+    if not W.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if W.dim() != 3 or tuple(W.shape[:2]) != (G, n):
+        raise ValueError(f"{name} must be [{G}, {n}, *], got {tuple(W.shape)}")
+    if W.dtype == torch.bfloat16:
+        if scale is not None:
+            raise ValueError(f"{name} in bfloat16 has no scales")
+        _shape(W, (G, n, k), name)
+        return MOE_BF16, MOE_SCALE_F32
+    if scale is None:
+        raise ValueError(f"{name} in {W.dtype} needs scales")
+    if W.dtype == torch.int8:
+        _shape(W, (G, n, k), name)
+        _shape(_dev(scale, torch.float32, f"{name} scales"), (G, n), f"{name} scales")
+        return MOE_I8, MOE_SCALE_F32
+    if W.dtype != torch.uint8:
+        raise TypeError(f"{name} must be bfloat16, int8, or uint8 (E4M3 or 4-bit codes), got {W.dtype}")
+    if W.shape[2] == k:
+        e8 = isinstance(scale, torch.Tensor) and scale.dtype == torch.uint8
+        _dev(scale, torch.uint8 if e8 else torch.float32, f"{name} scales")
+        _shape(scale, (G, n // 128, k // 128), f"{name} scales")
+        return MOE_FP8_E4M3, MOE_SCALE_E8M0 if e8 else MOE_SCALE_F32
+    _shape(W, (G, n, k // 2), name)
+    _shape(_dev(scale, torch.uint8, f"{name} scales"), (G, n, k // 32), f"{name} scales")
+    return MOE_FP4_E2M1, MOE_SCALE_F32
+
+
+def moe_decode(x, w_router, bias, W13, W2, top_k: int, n_group: int = 1, topk_group: int = 1, W13_scale=None, W2_scale=None,
+               norm: str | None = None, norm_weight=None, norm_bias=None, norm_eps: float = 1e-6, out_dtype=torch.bfloat16):
+    """The whole layer for up to 16 tokens in two launches: [norm,] routing, experts and their weighted sum.  x [T, d] bf16,
+    or f32 with a norm (row stride may exceed d); w_router [N, d] bf16; bias [N] f32; W13 [G, 2I, d] (I gate rows, then I up
+    rows), W2 [G, d, I], G = N + 1 with a shared expert (the last) or N without one, in bf16, as E4M3 codes (uint8) with
+    128x128 block scales (f32, or E8M0 codes in uint8), as int8 with a scale per row, or as w4_quant's 4-bit codes; the products
+    take the values that codes and scales stand for.  Returns (out [T, d] bf16 or f32, topk_idx [T, K] int32,
+    topk_gate [T, K] f32, expert_counts [N] int32)."""
+    _rows(x, "x")
+    _dev(w_router, torch.bfloat16, "w_router")
+    _dev(bias, torch.float32, "bias")
+    if norm not in _NORMS:
+        raise ValueError(f"norm must be None, 'layer' or 'rms', got {norm!r}")
+    if norm is None and (norm_weight is not None or norm_bias is not None):
+        raise ValueError("norm_weight and norm_bias need norm='layer' or 'rms'")
+    if out_dtype not in _ROW_DT:
+        raise TypeError(f"out_dtype must be torch.bfloat16 or torch.float32, got {out_dtype}")
+    T, d = x.shape
+    if w_router.dim() != 2 or w_router.shape[1] != d:
+        raise ValueError(f"w_router must be [N, {d}], got {tuple(w_router.shape)}")
+    N = w_router.shape[0]
+    if max(T, d, N, top_k, n_group, topk_group) > _INT_MAX:
+        _too_large(T=T, d=d, N=N, top_k=top_k, n_group=n_group, topk_group=topk_group)
+    _shape(bias, (N,), "bias")
+    if not isinstance(W13, torch.Tensor) or W13.dim() != 3 or W13.shape[1] % 2 or W13.shape[0] not in (N, N + 1):
+        raise ValueError(f"W13 must be [G, 2I, *] of G = {N} or {N + 1} experts")
+    G, I = W13.shape[0], W13.shape[1] // 2
+    if I > _INT_MAX // 2:
+        _too_large(I=I)
+    fmt = _expert_weights(W13, W13_scale, 2 * I, d, G, "W13")
+    if _expert_weights(W2, W2_scale, d, I, G, "W2") != fmt:
+        raise TypeError("W13 and W2 must be in the same format")
+    ndt = _vectors(d, norm_weight, norm_bias)
+    dev = x.device
+    _same_device(dev, w_router=w_router, bias=bias, W13=W13, W2=W2, W13_scale=W13_scale, W2_scale=W2_scale,
+                 norm_weight=norm_weight, norm_bias=norm_bias)
+    out = torch.empty(T, d, dtype=out_dtype, device=dev)
+    idx = torch.empty(T, max(top_k, 0), dtype=torch.int32, device=dev)
+    gate = torch.empty(T, max(top_k, 0), dtype=torch.float32, device=dev)
+    counts = torch.empty(N, dtype=torch.int32, device=dev)
+    wsb = lib().moe_decode_workspace_size(T, d, I, N, G - N, top_k)
+    ws = torch.empty(max(wsb, 16), dtype=torch.uint8, device=dev)
+    desc = MoeDecodeDesc(
+        x.data_ptr(), _ROW_DT[x.dtype], x.stride(0) if T > 1 else max(x.stride(0), d), T, d, I, N, G - N, top_k, n_group,
+        topk_group, _NORMS[norm], _addr(norm_weight), _addr(norm_bias), ndt, norm_eps, w_router.data_ptr(), bias.data_ptr(),
+        fmt[0], fmt[1], W13.data_ptr(), _addr(W13_scale), W2.data_ptr(), _addr(W2_scale), out.data_ptr(), _ROW_DT[out_dtype],
+        d, idx.data_ptr(), gate.data_ptr(), counts.data_ptr(), ws.data_ptr(), wsb)
+    _launch(dev, "moe_decode", ctypes.byref(desc))
+    return out, idx, gate, counts

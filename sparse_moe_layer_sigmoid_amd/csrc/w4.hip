@@ -28,11 +28,10 @@
 #include "abi_common.h"
 #include "device_common.h"
 #include "rows_common.h"
+#include "weights.h"
 
 namespace moe {
 namespace {
-
-typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
 
 constexpr int kMaxGroups = 1024;
 constexpr int kGroup = 32;      // inputs per scale
@@ -98,15 +97,6 @@ struct W4Args {
 };
 
 __device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
-
-// 8 codes -> 8 bf16 weights (code * scale, exact unless it overflows).
-__device__ __forceinline__ bf16x8_t decode_w4(uint32_t q, float scale) {
-  const bf16x2_t a = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 0);
-  const bf16x2_t b = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 1);
-  const bf16x2_t c = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 2);
-  const bf16x2_t d = __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(q, scale, 3);
-  return bf16x8_t{a[0], a[1], b[0], b[1], c[0], c[1], d[0], d[1]};
-}
 
 // The sorted row from which nothing is read or written: the first one that the caller did not vouch for.  Where the
 // groups before the tail hold more rows than out does, that is the first row past out, and the tail is empty.

@@ -159,6 +159,17 @@ class MoELayer:
                          "y_ckpt": y_ckpt}
         return out
 
+    def decode(self, x, out_dtype=torch.bfloat16, update_bias: bool = False, gamma: float = 0.001):
+        """The forward for up to 16 tokens in two launches (moe_decode): x [T, d] bf16 (or f32 with a norm) -> out
+        [T, d].  The same layer as forward on the same weights; its inner rows are not rounded on the way (forward
+        rounds h to bf16, and quantises x and h on the E4M3 and 8-bit integer paths)."""
+        out, _, _, counts = L.moe_decode(x, self.w_router, self.bias, self.W13, self.W2, self.top_k, self.n_group,
+                                         self.topk_group, self.W13_s, self.W2_s, self.norm, self.norm_weight, self.norm_bias,
+                                         self.norm_eps, out_dtype)
+        if update_bias:
+            L.moe_bias_update(self.bias, counts, x.shape[0] * self.top_k, gamma)
+        return out
+
     # ------------------------------------------------------------------ backward (bf16 path)
 
     def _transposed_weights(self):

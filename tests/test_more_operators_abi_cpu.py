@@ -72,3 +72,41 @@ def test_binding_refuses_cpu_tensors():
                                        z(2, dtype=torch.int32), 0, 1, 2, z(2, 4))):
         with pytest.raises(TypeError):
             call()
+
+
+def _decode(**kw):
+    a = dict(x=16, x_dtype=0, ldx=256, T=2, d=256, inter=128, n_experts=8, n_shared=1, top_k=2, n_group=1, topk_group=1, norm=-1,
+             norm_dtype=1, norm_eps=1e-6, w_router=16, bias=16, w_dtype=0, scale_fmt=0, w13=16, w2=16, out=16, out_dtype=0, ldo=256,
+             ws=256, ws_bytes=1 << 30)
+    a.update(kw)
+    return a
+
+
+@pytest.mark.parametrize("kw,code", [
+    (dict(x=None), 1), (dict(w_router=None), 1), (dict(bias=None), 1), (dict(w13=None), 1), (dict(w2=None), 1), (dict(out=None), 1),
+    (dict(w_dtype=3), 1), (dict(w_dtype=3, w13_scale=16), 1), (dict(T=-1), 2), (dict(T=17), 2), (dict(n_experts=6), 2),
+    (dict(n_experts=260), 2), (dict(n_shared=2), 2), (dict(n_shared=-1), 2), (dict(top_k=0), 2), (dict(top_k=9), 2),
+    (dict(n_experts=64, top_k=33), 2), (dict(n_group=3), 2), (dict(n_group=0), 2), (dict(n_group=4), 2), (dict(topk_group=2), 2),
+    (dict(n_experts=16, n_group=4, top_k=5), 2), (dict(w_dtype=1), 3), (dict(w_dtype=5), 3), (dict(scale_fmt=1), 3),
+    (dict(norm=2), 3), (dict(norm=-2), 3), (dict(x_dtype=1), 3), (dict(x_dtype=2), 3), (dict(out_dtype=2), 3),
+    (dict(norm=0, norm_dtype=2), 3), (dict(norm=0, norm_eps=-1.0), 2), (dict(norm=0, norm_eps=float("nan")), 2),
+    (dict(d=96, ldx=96), 2), (dict(d=0), 2), (dict(d=8256, ldx=8256, ldo=8256), 2), (dict(inter=32), 2), (dict(inter=0), 2),
+    (dict(w_dtype=3, d=320, ldx=320, ldo=320, w13_scale=16, w2_scale=16), 2), (dict(w_dtype=4, inter=192, w13_scale=16, w2_scale=16), 2),
+    (dict(w_dtype=2, scale_fmt=1, w13_scale=16, w2_scale=16), 2), (dict(inter=1 << 17, d=8192, ldx=8192, ldo=8192), 2),
+    (dict(ldx=255), 4), (dict(ldx=260), 4), (dict(x=8), 4), (dict(ldo=255), 4), (dict(out=17), 4), (dict(out=18, out_dtype=1), 4),
+    (dict(w_router=8), 4), (dict(w13=8), 4), (dict(w2=8), 4), (dict(bias=18), 4), (dict(w_dtype=4, w13_scale=18, w2_scale=16), 4),
+    (dict(norm=0, x=17), 4), (dict(norm=0, norm_weight=18), 4), (dict(topk_idx=18), 4), (dict(ws=None), 5), (dict(ws_bytes=100), 5),
+    (dict(ws=8), 5),
+])
+def test_decode_rejects(kw, code):
+    L = _lib()
+    _expect(L, "moe_decode", (ctypes.byref(L.MoeDecodeDesc(**_decode(**kw))), None), code)
+
+
+def test_decode_null_desc_workspace_size():
+    L = _lib()
+    _expect(L, "moe_decode", (None, None), 1)
+    f = L.lib().moe_decode_workspace_size
+    assert f(-1, 256, 128, 8, 1, 2) == 0 and f(17, 256, 128, 8, 1, 2) == 0 and f(1, 8200, 128, 8, 1, 2) == 0
+    assert f(1, 256, 128, 8, 2, 2) == 0 and f(1, 256, 128, 8, 1, 33) == 0
+    assert f(16, 256, 128, 8, 1, 2) - f(16, 256, 128, 8, 0, 2) == 16 * 128 * 4 and f(0, 256, 128, 8, 1, 2) > 0
