@@ -42,19 +42,19 @@ constexpr int kMaxTopK = 32;
 constexpr int kMaxD = 8192;       // inputs a workgroup's waves hold in registers
 constexpr int kNW = 8;            // waves of a workgroup
 constexpr int kMaxActive = 257;
-constexpr int kRowThreads = 512;
+constexpr int kRowThreads = 1024;
 constexpr uint64_t kWaitTicks = 500000000ull;  // 5 s of the 100 MHz clock: bound of the wait for h
 
-// Workspace: counters, logits, normalised rows, h.
-constexpr size_t kCounterBytes = 512;  // the next list, the next block of columns, finished lists: 128 bytes apart
-constexpr size_t kLogitBytes = (size_t)kMaxT * 256 * sizeof(double);
+// Workspace: counters, affinities, normalised rows, h.
+constexpr size_t kCounterBytes = 512;  // the next tile, finished tiles, started workgroups: 128 bytes apart
+constexpr size_t kScoreBytes = (size_t)kMaxT * 256 * sizeof(double);
 struct DecodeWs {
-  size_t logits, xn, h, total;
+  size_t scores, xn, h, total;
 };
 DecodeWs decode_ws(int T, int d, int inter, int n_shared, int top_k) {
   DecodeWs w;
-  w.logits = kCounterBytes;
-  w.xn = w.logits + kLogitBytes;
+  w.scores = kCounterBytes;
+  w.xn = w.scores + kScoreBytes;
   w.h = w.xn + (((size_t)T * d * 2 + 255) & ~(size_t)255);
   w.total = w.h + (size_t)T * (top_k + n_shared) * inter * 4;
   return w;
@@ -74,100 +74,135 @@ struct RowsArgs {
   double eps;
   const uint16_t* wr;
   uint32_t* counters;
-  double* logits;  // [T][256]
+  double* scores;  // affinities, [T][256]
   uint16_t* xn;
 };
 
+// v's sum over the wave by DPP moves (no LDS), in every lane.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double dpp_or_zero(double v) {
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xf, false),
+                                          (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xf, false)});
+}
 __device__ __forceinline__ double wave_sum64(double v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o, kWave);
-  return v;
+  v += dpp_or_zero<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8: lane 15 of each row of 16 has the row's sum
+  v += dpp_or_zero<0x112, 0xf>(v);
+  v += dpp_or_zero<0x114, 0xf>(v);
+  v += dpp_or_zero<0x118, 0xf>(v);
+  v += dpp_or_zero<0x142, 0xa>(v);  // lane 15 to the second row of each half, lane 31 to the upper half
+  v += dpp_or_zero<0x143, 0xc>(v);
+  const u32x2 w = __builtin_bit_cast(u32x2, v);
+  return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)w[0], 63),
+                                          (uint32_t)__builtin_amdgcn_readlane((int)w[1], 63)});
 }
 
+// A workgroup per routed expert and four tokens: one chunk of 8 inputs to a lane.
+template <bool NORM>
 __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(RowsArgs p) {
-  constexpr int CH = kMaxD / 8 / kRowThreads;  // chunks of 8 inputs per lane
-  __shared__ double s_mean[kMaxT], s_rstd[kMaxT], s_red[kRowThreads / 64][kMaxT];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int e = blockIdx.x, chunks = p.d / 8;
-  if (e == 0 && tid < 3) p.counters[tid * 32] = 0;
-  u32x4 wv[CH];
+  constexpr int G = 4;
+  static_assert(kMaxD <= 8 * kRowThreads, "one chunk per lane");
+  constexpr int W = kRowThreads / 64;
+  __shared__ double s_sums[NORM ? 2 : 1][W][NORM ? 2 * G : G];
+  __shared__ double s_stat[NORM ? G : 1][2];
+  const int tid = threadIdx.x, c = tid * 8;
+  const int e = blockIdx.x, t0 = blockIdx.y * G, nt = min(G, p.T - t0);
+  const bool in = c < p.d;
+  if (e == 0 && t0 == 0 && tid < 3) p.counters[tid * 32] = 0;
+  u32x4 wv = {0u, 0u, 0u, 0u};
+  if (in && e < p.N) wv = *(const u32x4*)(p.wr + (int64_t)e * p.d + c);
+  float f[G][8];
 #pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    wv[j] = u32x4{0u, 0u, 0u, 0u};
-    const int c = tid + j * kRowThreads;
-    if (c < chunks && e < p.N) wv[j] = *(const u32x4*)(p.wr + (int64_t)e * p.d + c * 8);
+  for (int i = 0; i < G; ++i) {
+#pragma unroll
+    for (int q = 0; q < 8; ++q) f[i][q] = 0.f;
+    if (in && i < nt) load8_any<true>(p.x_dtype, p.x + (t0 + i) * p.ldx_b, c, p.d, f[i]);
   }
-  if (p.norm != MOE_NORM_NONE) {
-    // statistics in fp64, of x minus the row's first element: no range to leave, and a mean far from zero cancels nothing
-    for (int t = wave; t < p.T; t += kRowThreads / 64) {
-      const uint8_t* row = p.x + t * p.ldx_b;
-      float f[8];
-      double pivot = 0.0, s1 = 0.0, s2 = 0.0;
-      if (p.norm == MOE_NORM_LAYER)
-        pivot = p.x_dtype == ROW_F32 ? (double)*(const float*)row : (double)bf16_to_f32(*(const uint16_t*)row);
-      for (int c = lane; c < chunks; c += 64) {
-        load8_any<true>(p.x_dtype, row, c * 8, p.d, f);
+  if constexpr (NORM) {
+    float g[8], b[8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const double v = (double)f[i] - pivot;
-          s1 += v;
-          s2 += v * v;
-        }
+    for (int q = 0; q < 8; ++q) {
+      g[q] = 1.f;
+      b[q] = 0.f;
+    }
+    if (p.weight && in) load8_any<true>(p.w_dtype, p.weight, c, p.d, g);
+    if (p.bias && in) load8_any<true>(p.w_dtype, p.bias, c, p.d, b);
+    // In fp64, statistics of x minus the row's first element: there is no range to leave, a mean far from zero cancels
+    // nothing, and the rounding to bf16 is that of the exact value but for one in 2^20 or so.
+    double pivot[G], sum[2 * G];
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const uint8_t* row = p.x + (t0 + min(i, nt - 1)) * p.ldx_b;
+      pivot[i] = p.norm != MOE_NORM_LAYER ? 0.0
+                 : p.x_dtype == ROW_F32   ? (double)*(const float*)row
+                                          : (double)bf16_to_f32(*(const uint16_t*)row);
+      sum[2 * i] = sum[2 * i + 1] = 0.0;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        const double v = in ? (double)f[i][q] - pivot[i] : 0.0;
+        sum[2 * i] += v;
+        sum[2 * i + 1] = fma(v, v, sum[2 * i + 1]);
       }
-      s1 = wave_sum64(s1) / p.d;
-      s2 = wave_sum64(s2) / p.d;
-      if (lane == 0) {
-        const bool layer = p.norm == MOE_NORM_LAYER;
-        s_mean[t] = layer ? pivot + s1 : 0.0;
-        s_rstd[t] = 1.0 / sqrt(fmax(layer ? s2 - s1 * s1 : s2, s2 - s2) + p.eps);
-      }
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * G; ++i) sum[i] = wave_sum64(sum[i]);
+    if ((tid & 63) == 0) {
+#pragma unroll
+      for (int i = 0; i < 2 * G; ++i) s_sums[0][tid >> 6][i] = sum[i];
     }
     __syncthreads();
-  }
-  float g[CH][8], b[CH][8];
+    if (tid < G) {
+      double s1 = 0.0, s2 = 0.0, piv = pivot[0];
 #pragma unroll
-  for (int j = 0; j < CH; ++j) {
-    const int c = tid + j * kRowThreads;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      g[j][i] = 1.f;
-      b[j][i] = 0.f;
-    }
-    if (p.norm != MOE_NORM_NONE && c < chunks) {
-      if (p.weight) load8_any<true>(p.w_dtype, p.weight, c * 8, p.d, g[j]);
-      if (p.bias) load8_any<true>(p.w_dtype, p.bias, c * 8, p.d, b[j]);
-    }
-  }
-  for (int t = 0; t < p.T; ++t) {
-    const uint8_t* row = p.x + t * p.ldx_b;
-    double acc = 0.0;
-#pragma unroll
-    for (int j = 0; j < CH; ++j) {
-      const int c = tid + j * kRowThreads;
-      if (c >= chunks) continue;
-      float f[8], w[8];
-      load8_any<true>(p.x_dtype, row, c * 8, p.d, f);
-      if (p.norm != MOE_NORM_NONE) {
-        const double mean = s_mean[t], rstd = s_rstd[t];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) f[i] = (float)(((double)f[i] - mean) * rstd * (double)g[j][i] + (double)b[j][i]);
-        const u32x4 o = pack_bf16x8(f);
-        if (t % gridDim.x == e) *(u32x4*)(p.xn + (int64_t)t * p.d + c * 8) = o;
-        unpack_bf16x8(o, f);
+      for (int i = 1; i < G; ++i) piv = tid == i ? pivot[i] : piv;
+      for (int w = 0; w < W; ++w) {
+        s1 += s_sums[0][w][2 * tid];
+        s2 += s_sums[0][w][2 * tid + 1];
       }
-      unpack_bf16x8(wv[j], w);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) acc += (double)(f[i] * w[i]);
+      double mean = 0.0, var = s2 / p.d;
+      if (p.norm == MOE_NORM_LAYER) {
+        const double m1 = s1 / p.d;
+        mean = piv + m1;
+        var -= m1 * m1;
+        if (var < 0.0) var = 0.0;
+      }
+      s_stat[tid][0] = mean;
+      s_stat[tid][1] = 1.0 / sqrt(var + p.eps);
     }
-    acc = wave_sum64(acc);
-    if (lane == 0) s_red[wave][t] = acc;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < G; ++i) {
+      const double mean = s_stat[i][0], rstd = s_stat[i][1];
+      float y[8];
+#pragma unroll
+      for (int q = 0; q < 8; ++q) y[q] = (float)fma(((double)f[i][q] - mean) * rstd, (double)g[q], (double)b[q]);
+      const u32x4 o = pack_bf16x8(y);
+      const int t = t0 + i;
+      if (in && i < nt && t % gridDim.x == e) *(u32x4*)(p.xn + (int64_t)t * p.d + c) = o;
+      unpack_bf16x8(o, f[i]);
+    }
+  }
+  double acc[G];
+  float w[8];
+  unpack_bf16x8(wv, w);
+#pragma unroll
+  for (int i = 0; i < G; ++i) {
+    acc[i] = 0.0;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) acc[i] += in ? (double)(f[i][q] * w[q]) : 0.0;  // bf16 products are exact in fp32
+  }
+  double(*const part)[NORM ? 2 * G : G] = s_sums[NORM ? 1 : 0];
+#pragma unroll
+  for (int i = 0; i < G; ++i) acc[i] = wave_sum64(acc[i]);
+  if ((tid & 63) == 0) {
+#pragma unroll
+    for (int i = 0; i < G; ++i) part[tid >> 6][i] = acc[i];
   }
   __syncthreads();
-  if (tid < p.T && e < p.N) {
-    double sum = 0.0;
-#pragma unroll
-    for (int w = 0; w < kRowThreads / 64; ++w) sum += s_red[w][tid];
-    p.logits[tid * 256 + e] = sum;
+  if (tid < nt && e < p.N) {
+    double u = 0.0;
+    for (int w = 0; w < W; ++w) u += part[w][tid];
+    p.scores[(t0 + tid) * 256 + e] = sigmoid_v<double>(u);
   }
 }
 
@@ -182,9 +217,10 @@ struct ExpertArgs {
   int64_t ldxn;
   int T, d, inter, N, n_shared, K, n_group, topk_group;
   const float* bias;
-  const double* logits;
+  const double* scores;
   uint32_t* counters;
-  float* h;  // [T][K + n_shared][inter]
+  uint16_t* h;  // [T][K + n_shared][inter], upper and lower parts one after the other
+  int ahead;    // tiles a workgroup holds: the one at work and those that its ring reaches into
   const uint8_t* w13;
   const uint8_t* s13;
   const uint8_t* w2;
@@ -211,17 +247,17 @@ __device__ __forceinline__ void lds_barrier() {
   asm volatile("" ::: "memory");
 }
 
-// 16 or 4 bytes per lane from base + v + off (v per lane, base and off uniform; `bytes` from base on may be read) to LDS at
-// dst, lane after lane.  (The host pass does not know the builtin.)
-__device__ __forceinline__ void load16_to_lds(const uint8_t* base, uint32_t bytes, uint32_t v, uint32_t off, uint8_t* dst) {
+// 16 or 4 bytes per lane from base + v + off (v per lane, base and off uniform) to LDS at dst, lane after lane.  (The host
+// pass does not know the builtin.)
+__device__ __forceinline__ void load16_to_lds(const uint8_t* base, uint32_t v, uint32_t off, uint8_t* dst) {
 #ifdef __HIP_DEVICE_COMPILE__
-  const auto r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
+  const auto r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0xffffffffu, 0x00020000);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 16, v, off, 0, 0);
 #endif
 }
-__device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t bytes, uint32_t v, uint32_t off, uint8_t* dst) {
+__device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t v, uint32_t off, uint8_t* dst) {
 #ifdef __HIP_DEVICE_COMPILE__
-  const auto r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
+  const auto r = __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, 0xffffffffu, 0x00020000);
   __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void*)dst, 4, v, off, 0, 0);
 #endif
 }
@@ -253,33 +289,19 @@ __device__ __forceinline__ bf16x8_t operand(const u32x4& q, int s, float scale) 
   else return decode_e4m3(q[2 * s], q[2 * s + 1]);
 }
 
-// h in two bf16 parts: the upper half of the float and what is left, rounded (2^-16 of h at most is lost).
-__device__ __forceinline__ void split8(const f32x4& a, const f32x4& b, bf16x8_t& hi, bf16x8_t& lo) {
-  u32x4 h, l;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float v0 = i < 2 ? a[2 * i] : b[2 * i - 4], v1 = i < 2 ? a[2 * i + 1] : b[2 * i - 3];
-    const uint32_t u0 = __float_as_uint(v0), u1 = __float_as_uint(v1);
-    h[i] = __builtin_amdgcn_perm(u1, u0, 0x07060302u);
-    const float r0 = v0 - __uint_as_float(u0 & 0xffff0000u), r1 = v1 - __uint_as_float(u1 & 0xffff0000u);
-    const float l0 = fabsf(v0) < INFINITY ? r0 : 0.f, l1 = fabsf(v1) < INFINITY ? r1 : 0.f;
-    l[i] = f32_to_bf16_rne(l0) | (f32_to_bf16_rne(l1) << 16);
-  }
-  hi = __builtin_bit_cast(bf16x8_t, h);
-  lo = __builtin_bit_cast(bf16x8_t, l);
-}
-
 template <int FMT>
 __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs p) {
   using F = Fmt<FMT>;
   constexpr int D = F::kDepth, SLOT = F::kSlot;
+  constexpr int U = 2 * F::kUnit;  // steps of a unit of the down projection: (expert, slice of the inner width)
+  static_assert(D % U == 0 && F::kSteps >= D / 2, "the ring holds whole units, and at most two tiles ahead");
   __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kNW * D * SLOT];
   __shared__ __attribute__((aligned(16))) f32x4 s_red[2][kNW][64];
   __shared__ float s_gate[kMaxT * (kMaxTopK + 1)];  // gate of slot t (K + n_shared) + k
   __shared__ __attribute__((aligned(16))) uint8_t s_k[kMaxActive][kMaxT];  // k of a token's active expert, 255: not chosen
   __shared__ uint16_t s_exp[kMaxActive];            // active experts, the shared one first
   __shared__ uint8_t s_first[kMaxActive];           // a token that chose it
-  __shared__ int s_ctl[4];                          // list, block of columns, active experts, gave up waiting
+  __shared__ int s_ctl[5];                          // tiles taken (two in turn), gave up waiting, first tile, number
   // of the selection, before the sums need the space
   uint32_t* const s_mask = reinterpret_cast<uint32_t*>(&s_red[0][0][0]);
   int32_t* const s_idx = reinterpret_cast<int32_t*>(&s_red[0][4][0]);
@@ -290,26 +312,105 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
   const int T = p.T, K = p.K, KS = p.K + p.n_shared;
-  uint32_t* const list_ticket = p.counters;
-  uint32_t* const block_ticket = p.counters + 32;
-  uint32_t* const done = p.counters + 64;
-  auto take = [](uint32_t* c) {
-    return (int)__hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  uint32_t* const next_tile = p.counters;
+  uint32_t* const done = p.counters + 32;
+  uint32_t in_vgpr = 0;  // of a uniform address the compiler combines the wave's additions, and waits for the sum at once
+  asm volatile("" : "+v"(in_vgpr));
+  auto take = [&](uint32_t* counter) __attribute__((always_inline)) {
+    return (int)__hip_atomic_fetch_add(counter + in_vgpr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
-  int first_list = 0;
-  if (tid == 0) first_list = take(list_ticket);
+  int number_taken = 0;
+  if (tid == 0) {
+    s_ctl[3] = (int)__hip_atomic_fetch_add(next_tile + in_vgpr, (uint32_t)p.ahead, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    number_taken = take(p.counters + 64);
+  }
 
-  // ---- this wave's inputs of all tokens (columns past T hold the last token again and are never stored) ----
-  const int nb1 = (p.d + F::kBlock - 1) / F::kBlock;        // blocks of a gate/up row
-  const int steps1 = (nb1 + kNW - 1) / kNW;
-  bf16x8_t x[F::kSteps][2][F::kVec];
+  // ---- what is needed of the weights' layout ----
+  const int nt = p.inter / 8;                                // tiles of an expert
+  const int nb1 = (p.d + F::kBlock - 1) / F::kBlock;         // blocks of a gate/up row
+  const int nb2 = (p.inter + F::kBlock - 1) / F::kBlock;     // blocks of a down row
+  // steps of a tile; as many at least as leave the ring no more than two tiles ahead (a block that a wave does not have
+  // is another one of the row again, unused)
+  const int steps = max((nb1 + kNW - 1) / kNW, D / 2);
+  const uint32_t row1_b = p.d / F::kBlock * 128 + p.d % F::kBlock * 128 / F::kBlock;
+  const uint32_t row2_b = p.inter / F::kBlock * 128 + p.inter % F::kBlock * 128 / F::kBlock;
+  const int lrow = lane >> 3;
+  const int chunk = (lane & 7) ^ lrow;                       // 16-byte piece of a block that this lane loads
+  const int srow = FMT == W_FP4 ? (lane >> 1) & 15 : lr;     // row of a step whose scale this lane loads
+  constexpr int kScaleLanes = FMT == W_FP4 ? 32 : 16;
+  // offset of row q's scales from row 0's (k inputs, nb blocks to a row)
+  auto scale_row = [&](uint32_t q, uint32_t nb, uint32_t k) __attribute__((always_inline)) {
+    if constexpr (FMT == W_FP4) return q * (k / 32);
+    else if constexpr (FMT == W_E4M3) return q / 128 * nb * 4;
+    else if constexpr (FMT == W_E4M3_E8M0) return q / 128 * nb;
+    else return q * 4;
+  };
+  // bytes of one expert's scales (n rows)
+  auto scale_bytes = [&](int64_t n, int64_t nb, int64_t k) __attribute__((always_inline)) {
+    if constexpr (FMT == W_FP4) return n * (k / 32);
+    else if constexpr (FMT == W_E4M3) return n / 128 * nb * 4;
+    else if constexpr (FMT == W_E4M3_E8M0) return n / 128 * nb;
+    else return n * 4;
+  };
+  uint8_t* const ring = s_ring + wave * (D * SLOT);
+  // A step: 16 rows x 128 bytes (block b of rows of row_b bytes) and their scales.  This lane's pieces are at v0 and v1 + off1 of
+  // w, its scales at vs of sc.
+  struct Place {
+    const uint8_t *w, *sc;
+  };
+  struct Source {
+    Place at;
+    uint32_t row_b, b, v0, v1, off1, vs;
+  };
+  // Buffer loads: for the compiler global loads into LDS are flat ones, behind which it waits for everything in flight before it
+  // uses a register that a load of h fills.
+  auto load_step = [&](int slot, const Source& q) __attribute__((always_inline)) {
+    uint8_t* dst = ring + slot * SLOT;
+    const bool half = FMT == W_FP4 && q.b * 128 + 128 > q.row_b;  // a last block of 64 bytes: its first half twice
+    const uint32_t back = half && (chunk & 4) ? 64 : 0;
+    load16_to_lds(q.at.w, q.v0 - back, q.b * 128, dst);
+    load16_to_lds(q.at.w, q.v1 - back, q.b * 128 + q.off1, dst + 1024);
+    if constexpr (F::kScaled) {
+      const uint32_t off = FMT == W_FP4 ? q.b * 8 : FMT == W_E4M3 ? q.b * 4 : FMT == W_E4M3_E8M0 ? q.b & ~3u : 0u;
+      uint32_t v = q.vs;
+      if constexpr (FMT == W_FP4) v += half ? 0 : (lane & 1) * 4;
+      if (lane < kScaleLanes) load4_to_lds(q.at.sc, v, off, dst + 2048);
+    }
+  };
+  // Wave w's i-th block of a row is in the i-th eight blocks, rotated by i and (down) the expert: with the same place in every
+  // eight, a wave would meet the same memory channels all along.
+  auto own_block = [&](int i, int e) __attribute__((always_inline)) { return i * kNW + ((wave + i + e) & (kNW - 1)); };
+  auto block_of = [&](int i, int e, int nb) __attribute__((always_inline)) {
+    const int b = own_block(i, e);
+    return (uint32_t)(b < nb ? b : min(wave, nb - 1));
+  };
+  // gate/up: tile `tile` of expert e is 8 gate rows and their 8 up rows
+  auto up_place = [&](int64_t e, int tile) __attribute__((always_inline)) {
+    Place q;
+    q.w = p.w13 + (e * 2 * p.inter + tile * 8) * row1_b;
+    q.sc = p.s13 + e * scale_bytes(2 * p.inter, nb1, p.d) + scale_row(tile * 8, nb1, p.d);
+    return q;
+  };
+  const uint32_t up_v = lrow * row1_b + chunk * 16, up_off = p.inter * row1_b;
+  uint32_t up_vs;  // tiles start at multiples of 8 rows: none crosses a block of 128
+  if constexpr (FMT == W_E4M3 || FMT == W_E4M3_E8M0) up_vs = srow < 8 ? 0 : scale_row(p.inter, nb1, p.d);
+  else up_vs = scale_row((srow & 7) + (srow < 8 ? 0 : p.inter), nb1, p.d);
+  auto up_step = [&](const Place& q, int s) __attribute__((always_inline)) {
+    return Source{q, row1_b, block_of(s, 0, nb1), up_v, up_v, up_off, up_vs};
+  };
+
+  // ---- the tokens' affinities and inputs, in flight before any weights ----
+  double u[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) u[r] = wave < T && lane * 4 + r < p.N ? p.scores[wave * 256 + lane * 4 + r] : 0.0;
+  bf16x8_t x[F::kSteps][2][F::kVec];  // this wave's blocks of all tokens (columns past T hold the last token again)
   {
     const uint16_t* xr = p.xn + (int64_t)min(lr, T - 1) * p.ldxn;
 #pragma unroll
     for (int j = 0; j < F::kSteps; ++j)
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
-        const int k0 = (wave + j * kNW) * F::kBlock + hf * (F::kBlock / 2);
+        const int k0 = own_block(j, 0) * F::kBlock + hf * (F::kBlock / 2);
 #pragma unroll
         for (int s = 0; s < F::kVec; ++s) {
           u32x4 v = {0u, 0u, 0u, 0u};
@@ -318,27 +419,47 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
         }
       }
   }
-
-  // ---- selection ----
   for (int i = tid; i < 256; i += kNW * 64) s_mask[i] = 0;
-  for (int t = wave; t < T; t += kNW) {
-    double u[4];
-#pragma unroll
-    for (int r = 0; r < 4; ++r) u[r] = lane * 4 + r < p.N ? p.logits[t * 256 + lane * 4 + r] : 0.0;
-    float* const gate = s_gate + t * (KS - K);  // select_token writes at t * K + k; rows here are KS apart
-    select_token<double>(u, p.bias, p.N, K, p.n_group, p.topk_group, t, true, s_idx, gate, nullptr);
-    if (lane == 0 && p.n_shared) s_gate[t * KS + K] = 1.0f;
-  }
-  if (tid == 0) s_ctl[0] = first_list;
-  __syncthreads();
-  for (int i = tid; i < T * K; i += kNW * 64) atomicOr(&s_mask[s_idx[i]], 1u << (i / K));
   for (int i = tid; i < kMaxActive * kMaxT / 4; i += kNW * 64) reinterpret_cast<uint32_t*>(&s_k[0][0])[i] = 0xffffffffu;
   __syncthreads();
+  // Tickets name tiles: the first p.ahead * gridDim.x tickets are taken p.ahead at a time (one workgroup's tiles at work and ahead)
+  // and name tiles a gridDim.x apart, so that everyone starts with the shared expert's.
+  auto tile_of = [&](int ticket) __attribute__((always_inline)) {
+    if (ticket >= p.ahead * (int)gridDim.x) return ticket;
+    const int v = (int)((uint32_t)ticket / (uint32_t)p.ahead);
+    return (ticket - v * p.ahead) * (int)gridDim.x + v;
+  };
+  const int ticket = __builtin_amdgcn_readfirstlane(s_ctl[3]);
+  const int first = tile_of(ticket);
+
+  // the shared expert's tiles come first: their weights are on the way while the routed ones are being chosen
+  int loaded = 0;
+  if (p.n_shared && first < nt) {
+    const Place q = up_place(p.N, first);
+    loaded = min(D, steps);
+#pragma unroll 1
+    for (int s = 0; s < loaded; ++s) load_step(s, up_step(q, s));
+  }
+
+  // ---- selection ----
+#pragma unroll 1
+  for (int t = wave; t < T; t += kNW) {
+    if (t >= kNW) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) u[r] = lane * 4 + r < p.N ? p.scores[t * 256 + lane * 4 + r] : 0.0;
+    }
+    float* const gate = s_gate + t * (KS - K);  // select_token writes at t * K + k; rows here are KS apart
+    select_token<double, true>(u, p.bias, p.N, K, p.n_group, p.topk_group, t, true, s_idx, gate, nullptr);
+    if (lane == 0 && p.n_shared) s_gate[t * KS + K] = 1.0f;
+  }
+  lds_barrier();
+  for (int i = tid; i < T * K; i += kNW * 64) atomicOr(&s_mask[s_idx[i]], 1u << (i / K));
+  lds_barrier();
   {
     const uint32_t mask = tid < p.N ? s_mask[tid] : 0u;
     const uint64_t any = __ballot(mask != 0);
     if (lane == 0 && wave < 4) s_cnt[wave] = (uint32_t)__popcll(any);
-    __syncthreads();
+    lds_barrier();
     int at = p.n_shared;
     for (int w = 0; w < 4 && w < wave; ++w) at += (int)s_cnt[w];
     at += __popcll(any & ((1ull << lane) - 1));
@@ -352,10 +473,10 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
         s_exp[0] = (uint16_t)p.N;
         s_first[0] = 0;
       }
-      s_ctl[2] = p.n_shared + (int)(s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3]);
-      s_ctl[3] = 0;
+      s_ctl[2] = 0;
+      s_ctl[4] = number_taken;
     }
-    if (s_ctl[0] == 0) {  // the first workgroup reports the routing
+    if (ticket == 0) {  // the first workgroup reports the routing
       if (p.counts && tid < p.N) p.counts[tid] = __popc(mask);
       for (int i = tid; i < T * K; i += kNW * 64) {
         if (p.topk_idx) p.topk_idx[i] = s_idx[i];
@@ -363,137 +484,52 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       }
     }
   }
-  __syncthreads();
+  const int A = __builtin_amdgcn_readfirstlane(p.n_shared + (int)(s_cnt[0] + s_cnt[1] + s_cnt[2] + s_cnt[3]));
+  const int tiles = A * nt;
+  lds_barrier();
   for (int i = tid; i < T * K; i += kNW * 64) s_k[s_pos[s_idx[i]]][i / K] = (uint8_t)(i % K);
   if (p.n_shared && tid < T) s_k[0][tid] = (uint8_t)K;
-  __syncthreads();
-  const int A = __builtin_amdgcn_readfirstlane(s_ctl[2]);
 
-  // ---- the work: lists of gate/up tiles, then blocks of output columns ----
-  const int nt = p.inter / 8;                                // tiles of an expert
-  const int tiles = A * nt;
-  const int lists = min((int)gridDim.x, tiles);              // list v: tiles v, v + lists, ...
-  const int R = min(32, (((p.d + (int)gridDim.x - 1) / (int)gridDim.x) + 3) & ~3);  // columns of a block
+  const int number = __builtin_amdgcn_readfirstlane(s_ctl[4]);  // of this workgroup, in the order they started
+
+  // ---- down: blocks of R output columns, block `number` for this workgroup (and, were there more blocks than workgroups,
+  // every gridDim.x-th from there): no other workgroup needs them, so they may wait for one that starts late ----
+  const int R = min(32, (((p.d + (int)gridDim.x - 1) / (int)gridDim.x) + 3) & ~3);
   const int blocks = (p.d + R - 1) / R;
-  const int nb2 = (p.inter + F::kBlock - 1) / F::kBlock;     // blocks of a down row
   const int slices = (nb2 + kNW * F::kUnit - 1) / (kNW * F::kUnit);
-  constexpr int U = 2 * F::kUnit;                            // steps of a unit (expert, slice)
-  const uint32_t row1_b = p.d / F::kBlock * 128 + p.d % F::kBlock * 128 / F::kBlock;
-  const uint32_t row2_b = p.inter / F::kBlock * 128 + p.inter % F::kBlock * 128 / F::kBlock;
-
-  const int lrow = lane >> 3;
-  const int chunk = (lane & 7) ^ lrow;  // 16-byte piece of a block that this lane loads
-
-  // Where the next step is loaded from: `w` and `sc` are one expert's weights and scales; this lane's rows of them are at
-  // v[0], v[1] (down: v[2], v[3] in the second 16 rows of the block), its scales at vs[0] (vs[1]).  Buffer loads: for
-  // the compiler global loads into LDS are flat ones, behind which it waits for everything in flight before it uses a register
-  // that a load of h fills.
-  enum { UP, DOWN, NOTHING };
-  struct Cursor {
-    int kind, a, tile, id, j, sl, steps;
-    uint32_t row_b, nb;
-    const uint8_t *w, *sc;
-    uint32_t w_bytes, sc_bytes;
-    uint32_t v[4], vs[2];
-  } cu;
-  const uint8_t* ring = s_ring + wave * (D * SLOT);
-  const int srow = FMT == W_FP4 ? (lane >> 1) & 15 : lr;  // row of a step whose scale this lane loads
-  const uint32_t half_back = FMT == W_FP4 && (chunk & 4) ? 64 : 0;
-  int next_kind = NOTHING, next_id = 0;  // what is loaded after the list's last step
-  // offset of row q's scales within its expert's (k inputs to a row)
-  auto scale_row = [&](uint32_t q, uint32_t nb, uint32_t k) __attribute__((always_inline)) {
-    if constexpr (FMT == W_FP4) return q * (k / 32) + (lane & 1) * 4;
-    else if constexpr (FMT == W_E4M3) return q / 128 * nb * 4;
-    else if constexpr (FMT == W_E4M3_E8M0) return q / 128 * nb;
-    else return q * 4;
-  };
-  auto set_expert = [&]() __attribute__((always_inline)) {
-    const int64_t e = __builtin_amdgcn_readfirstlane(s_exp[cu.a]);
-    const bool up = cu.kind == UP;
-    const int64_t n = up ? 2 * p.inter : p.d;
-    cu.w = (up ? p.w13 : p.w2) + e * n * cu.row_b;
-    cu.w_bytes = (uint32_t)n * cu.row_b;
-    const uint32_t k = up ? p.d : p.inter;
-    const int64_t sn = FMT == W_FP4 ? n * (k / 32) : FMT == W_I8 ? n * 4 : n / 128 * cu.nb * (FMT == W_E4M3 ? 4 : 1);
-    cu.sc = (up ? p.s13 : p.s2) + e * sn;
-    cu.sc_bytes = (uint32_t)sn;
-  };
-  auto set_tile = [&]() __attribute__((always_inline)) {
-    const uint32_t q = cu.tile * 8 + lrow;
-    cu.v[0] = q * cu.row_b + chunk * 16;
-    cu.v[1] = cu.v[0] + p.inter * cu.row_b;
-    cu.vs[0] = scale_row(cu.tile * 8 + (srow & 7) + (srow < 8 ? 0 : p.inter), cu.nb, p.d);
-  };
-  auto start = [&](int kind, int id) __attribute__((always_inline)) {
-    cu.kind = kind;
-    cu.j = 0;
-    cu.sl = 0;
-    cu.id = id;
-    cu.a = 0;
-    if (kind == UP) {
-      cu.a = (int)((uint32_t)id / (uint32_t)nt);
-      cu.tile = id - cu.a * nt;
-      cu.steps = steps1;
-      cu.row_b = row1_b;
-      cu.nb = nb1;
-      set_expert();
-      set_tile();
-    } else {
-      const int c0 = kind == DOWN ? id * R : 0, last = min(c0 + R, p.d) - 1;
-      cu.steps = U;
-      cu.row_b = row2_b;
-      cu.nb = nb2;
-      set_expert();
+  const int units = A * slices;
+  uint32_t dn_v[4], dn_vs[2];  // this lane's rows of a block, two times 16
+  auto set_block = [&](int block) __attribute__((always_inline)) {
+    const int c0 = block * R, last = min(c0 + R, p.d) - 1;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) cu.v[i] = (uint32_t)min(c0 + i * 8 + lrow, last) * row2_b + chunk * 16;
+    for (int i = 0; i < 4; ++i) dn_v[i] = (uint32_t)min(c0 + i * 8 + lrow, last) * row2_b + chunk * 16;
 #pragma unroll
-      for (int i = 0; i < 2; ++i) cu.vs[i] = scale_row(min(c0 + i * 16 + srow, last), nb2, p.inter);
-    }
+    for (int i = 0; i < 2; ++i) dn_vs[i] = scale_row(min(c0 + i * 16 + srow, last), nb2, p.inter);
   };
-  auto advance = [&]() __attribute__((always_inline)) {  // to the step after a tile's or a unit's last one
-    cu.j = 0;
-    if (cu.kind == UP) {
-      cu.id += lists;
-      if (cu.id >= tiles) {
-        start(next_kind, next_id);
-      } else {
-        cu.tile += lists;
-        while (cu.tile >= nt) {
-          cu.tile -= nt;
-          ++cu.a;
-        }
-        set_expert();
-        set_tile();
-      }
-    } else if (cu.kind == DOWN && ++cu.sl == slices) {
-      cu.sl = 0;
-      if (++cu.a == A) {  // past the end the first steps again, so that the number of loads in flight stays
-        cu.a = 0;
-        cu.kind = NOTHING;
-      }
-      set_expert();
-    }
+  auto expert = [&](int a) __attribute__((always_inline)) { return __builtin_amdgcn_readfirstlane(s_exp[a]); };
+  auto down_place = [&](int64_t e) __attribute__((always_inline)) {
+    Place q;
+    q.w = p.w2 + e * p.d * row2_b;
+    q.sc = p.s2 + e * scale_bytes(p.d, nb2, p.inter);
+    return q;
   };
-  // Load the next step, 16 weight rows x 128 bytes and its scales, into `slot`.
-  auto issue = [&](int slot) __attribute__((always_inline)) {
-    uint8_t* dst = const_cast<uint8_t*>(ring) + slot * SLOT;
-    const bool up = cu.kind == UP, second = !up && (cu.j & 1);
-    uint32_t b = up ? wave + cu.j * kNW : (cu.sl * F::kUnit + (cu.j >> 1)) * kNW + wave;
-    b = b < cu.nb ? b : min((uint32_t)wave, cu.nb - 1);  // a wave without a block of its own here loads another, unused
-    const uint32_t off = b * 128;
-    const uint32_t back = FMT == W_FP4 && off + 128 > cu.row_b ? half_back : 0;  // a last block of 64 bytes
-    load16_to_lds(cu.w, cu.w_bytes, (second ? cu.v[2] : cu.v[0]) - back, off, dst);
-    load16_to_lds(cu.w, cu.w_bytes, (second ? cu.v[3] : cu.v[1]) - back, off, dst + 1024);
-    if constexpr (F::kScaled) {
-      const uint32_t vs = second ? cu.vs[1] : cu.vs[0];
-      if (lane < (FMT == W_FP4 ? 32 : 16)) {
-        uint32_t at = FMT == W_FP4 ? b * 8 : FMT == W_E4M3 ? b * 4 : FMT == W_E4M3_E8M0 ? b & ~3u : 0u;
-        if constexpr (FMT == W_FP4) at -= off + 128 > cu.row_b ? (lane & 1) * 4 : 0;
-        load4_to_lds(cu.sc, cu.sc_bytes, vs + at, 0, dst + 2048);
-      }
+  auto down_step = [&](const Place& q, int e, int sl, int i) __attribute__((always_inline)) {  // step i of slice sl
+    Source r = {q, row2_b, block_of(sl * F::kUnit + (i >> 1), e, nb2), dn_v[0], dn_v[1], 0, dn_vs[0]};
+    if (i & 1) {
+      r.v0 = dn_v[2];
+      r.v1 = dn_v[3];
+      r.vs = dn_vs[1];
     }
-    if (++cu.j == cu.steps) advance();
+    return r;
   };
+  auto down_step_at = [&](int c) __attribute__((always_inline)) {  // step c of the block (past its end: step 0's, unused)
+    int un = c / U;
+    un = un < units ? un : 0;
+    const int a = slices == 1 ? un : (int)((uint32_t)un / (uint32_t)slices);
+    const int e = expert(a);
+    return down_step(down_place(e), e, un - a * slices, c % U);
+  };
+  set_block(number < blocks ? number : 0);
 
   // A step's operands from its slot: this lane's two 16-byte pieces of row lr and its scales.  The reads and their wait
   // are one block: the compiler does not order them against the loads into LDS, the waits on those do.
@@ -538,7 +574,6 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       return __uint_as_float(s.sc[r]);
     }
   };
-
   // The 8 waves' partial sums of one value, in wave order: 1 KB apart from byte address `at` on.
   auto join8 = [](uint32_t at) __attribute__((always_inline)) {
     float v[8];
@@ -559,195 +594,224 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   int slot = 0;
   auto next_slot = [&]() __attribute__((always_inline)) { slot = slot + 1 == D ? 0 : slot + 1; };
 
-  // ---- gate/up ----
-  // A list's successor has to be known when its last steps are being loaded, D steps ahead of its last tile's end: it is taken
-  // `early` tiles before the last one (a short list's at its start).  Taking it sooner would keep lists from workgroups
-  // that have yet to start.
-  const int early = 1 + (D - 1) / steps1;
-  // Lists so short that the ring holds all of one do not run on into each other: the one after next would have to be known.
-  const bool chained = tiles / max(lists, 1) * steps1 > D;
-  int list = __builtin_amdgcn_readfirstlane(s_ctl[0]);
-  int next_list = lists, column_block = blocks;
-  bool prefilled = false;
-  auto take_next = [&]() __attribute__((always_inline)) {  // one lane: what follows
-    const int v = take(list_ticket);
-    if (v < lists) {
-      s_ctl[0] = v;
-    } else {
-      s_ctl[0] = lists;
-      s_ctl[1] = take(block_ticket);
-    }
+  // ---- gate/up: tile q0 at work, q1 (deep: and q2) taken; those >= tiles do not exist ----
+  auto place_of = [&](int id) __attribute__((always_inline)) {
+    if (id >= tiles) return Place{p.w13, p.s13};
+    const int a = (int)((uint32_t)id / (uint32_t)nt);
+    return up_place(expert(a), id - a * nt);
   };
-  auto read_next = [&]() __attribute__((always_inline)) {
-    const int v = __builtin_amdgcn_readfirstlane(s_ctl[0]);
-    next_list = v;
-    if (v < lists) {
-      next_kind = chained ? UP : NOTHING;
-      next_id = v;
-    } else {
-      column_block = __builtin_amdgcn_readfirstlane(s_ctl[1]);
-      next_kind = column_block < blocks ? DOWN : NOTHING;
-      next_id = column_block;
-    }
-  };
-  __syncthreads();  // every lane has read the first list
-  if (list >= lists) {
-    if (tid == 0) s_ctl[1] = take(block_ticket);
-    __syncthreads();
-    column_block = __builtin_amdgcn_readfirstlane(s_ctl[1]);
+  const bool deep = p.ahead > 2;  // the ring reaches into the tile after next
+  int q0 = first, q1 = tile_of(ticket + 1), q2 = deep ? tile_of(ticket + 2) : tiles;
+  if (q1 >= tiles) {  // those that exist come first
+    q1 = q2;
+    q2 = tiles;
   }
-  wait_vm<0>();  // the inputs are here: below, waits count the ring's loads alone
-  int buf = 0;
-  while (list < lists) {
-    const int n = (tiles - list + lists - 1) / lists;
-    const int when = n - 1 - early;  // tile before which the successor is taken
-    if (when < 1) {
-      if (tid == 0) take_next();
-      __syncthreads();
-      read_next();
+  if (q0 >= tiles) {
+    q0 = q1;
+    q1 = q2;
+    q2 = tiles;
+  }
+  int last = ticket + p.ahead - 1;                               // the latest ticket
+  const int no_more = max(tiles, p.ahead * (int)gridDim.x);      // from here on tickets name no tile
+  Place p0 = place_of(q0), p1 = place_of(q1), p2 = place_of(q2);
+  // the step `ahead` of tile q0's first one: in a taken tile, or past the last one of those in the down projection
+  auto load_ahead = [&](int slot, int ahead) __attribute__((always_inline)) {
+    const int k = (ahead >= steps) + (ahead >= 2 * steps);
+    int id = q2;
+    Place q = p2;
+    if (k == 0) {
+      id = q0;
+      q = p0;
+    } else if (k == 1) {
+      id = q1;
+      q = p1;
     }
-    if (!prefilled) {
-      start(UP, list);
-      for (int s = 0; s < D; ++s) issue(s);
-      prefilled = true;
+    // (one load_step behind both ways, so that the compiler can count its loads)
+    Source r;
+    if (id < tiles) {
+      r = up_step(q, ahead - k * steps);
+    } else {
+      const int have = (q0 < tiles) + (q1 < tiles) + (q2 < tiles);  // they are taken in order
+      r = down_step_at(ahead - have * steps);
     }
-    int a = (int)((uint32_t)list / (uint32_t)nt), tile = list - a * nt;
-    for (int i = 0; i < n; ++i) {
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-      u32x4 sc = {0u, 0u, 0u, 0u};
-#pragma unroll
-      for (int j = 0; j < F::kSteps; ++j) {
-        if (j < steps1) {
-          wait_vm<F::kWaitUp>();
-          const Step s = read_step(slot);
-          issue(slot);
-          next_slot();
-          const int b = wave + j * kNW;
-          if (b < nb1) {
-            f32x4 part = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (FMT != W_E4M3 && FMT != W_E4M3_E8M0) part = acc;
-            const float s0 = __uint_as_float(s.sc[0] << 23), s1 = __uint_as_float(s.sc[1] << 23);
-#pragma unroll
-            for (int v = 0; v < F::kVec; ++v) part = mfma_bf16(operand<FMT>(s.lo, v, s0), x[j][0][v], part);
-            if (FMT != W_FP4 || b * F::kBlock + F::kBlock / 2 < p.d) {
-#pragma unroll
-              for (int v = 0; v < F::kVec; ++v) part = mfma_bf16(operand<FMT>(s.hi, v, s1), x[j][1][v], part);
-            }
-            if constexpr (FMT == W_E4M3 || FMT == W_E4M3_E8M0) {
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[r] = fmaf(part[r], row_scale(s, b, r), acc[r]);
-            } else {
-              acc = part;
-            }
-          }
-          if constexpr (FMT == W_I8) sc = s.sc;
-        }
-      }
-      if constexpr (FMT == W_I8) {
-#pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] *= __uint_as_float(sc[r]);
-      }
-      s_red[buf][wave][lane] = acc;
-      if (when >= 1 && i + 1 == when && tid == 0) take_next();
+    load_step(slot, r);
+  };
+  __syncthreads();  // s_k; and the inputs are here: below, waits count the ring's loads alone
+  wait_vm<0>();
+#pragma unroll 1
+  for (; loaded < D; ++loaded) load_ahead(loaded, loaded);
+
+  int buf = 0, mine = 0;
+  for (;;) {
+    if (q0 >= tiles) {
+      // Nothing left of what was taken.  Unless the latest ticket was past the end there may be tiles of workgroups that have
+      // not started, which may not start before this one ends: take them, one at a time.
+      if (last >= no_more) break;
+      if (tid == 0) s_ctl[3] = take(next_tile);
       lds_barrier();
-      if (when >= 1 && i + 1 == when) read_next();
-      if (tid < 128) {  // the waves' sums in wave order, SwiGLU, h
-        const int t = tid >> 3, c = tid & 7;
-        const uint32_t at = red_at + buf * (kNW * 1024) + (t + 16 * (c >> 2)) * 16 + (c & 3) * 4;
-        const float g = join8(at), u = join8(at + 512);
-        const int k = s_k[a][t];
-        if (k != 255) p.h[(int64_t)(t * KS + k) * p.inter + tile * 8 + c] = silu(g) * u;
-      }
-      buf ^= 1;
-      tile += lists;
-      while (tile >= nt) {
-        tile -= nt;
-        ++a;
-      }
-    }
-    // this list's h is in memory, for every XCD to see, before it is counted
-    if (tid < 128) __builtin_amdgcn_fence(__ATOMIC_RELEASE, "agent");
-    __syncthreads();
-    if (tid == 0) __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    list = next_list;
-    if (list < lists && !chained) {
+      last = __builtin_amdgcn_readfirstlane(s_ctl[3]);
+      lds_barrier();
+      q0 = last < no_more ? tile_of(last) : tiles;
+      if (q0 >= tiles) continue;
+      p0 = place_of(q0);
+      q1 = q2 = tiles;
       wait_vm<0>();  // start over with an empty ring
       slot = 0;
-      prefilled = false;
+#pragma unroll 1
+      for (int s = 0; s < D; ++s) load_ahead(s, s);
     }
+    const int a = (int)((uint32_t)q0 / (uint32_t)nt), tile = q0 - a * nt;
+    const bool ask = (deep ? q2 : q1) < tiles && last < no_more;
+    int taken = 0;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    u32x4 sc = {0u, 0u, 0u, 0u};
+#pragma unroll
+    for (int j = 0; j < F::kSteps; ++j) {
+      if (j < D / 2 || j < steps) {
+        // The next tile's number is asked for at the start of this one and looked at D / 2 steps on (those are unconditional, so
+        // the compiler can count the loads behind it)
+        if (j == 0 && ask && tid == 0) taken = take(next_tile);
+        if (j == D / 2 - 1 && tid == 0) s_ctl[buf] = taken;
+        wait_vm<F::kWaitUp>();
+        const Step s = read_step(slot);
+        load_ahead(slot, j + D);
+        next_slot();
+        const int b = own_block(j, 0);
+        if (b < nb1) {
+          f32x4 part = {0.f, 0.f, 0.f, 0.f};
+          if constexpr (FMT != W_E4M3 && FMT != W_E4M3_E8M0) part = acc;
+          const float s0 = __uint_as_float(s.sc[0] << 23), s1 = __uint_as_float(s.sc[1] << 23);
+#pragma unroll
+          for (int v = 0; v < F::kVec; ++v) part = mfma_bf16(operand<FMT>(s.lo, v, s0), x[j][0][v], part);
+          if (FMT != W_FP4 || b * F::kBlock + F::kBlock / 2 < p.d) {
+#pragma unroll
+            for (int v = 0; v < F::kVec; ++v) part = mfma_bf16(operand<FMT>(s.hi, v, s1), x[j][1][v], part);
+          }
+          if constexpr (FMT == W_E4M3 || FMT == W_E4M3_E8M0) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) acc[r] = fmaf(part[r], row_scale(s, b, r), acc[r]);
+          } else {
+            acc = part;
+          }
+        }
+        if constexpr (FMT == W_I8) sc = s.sc;
+      }
+    }
+    if constexpr (FMT == W_I8) {
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[r] *= __uint_as_float(sc[r]);
+    }
+    s_red[buf][wave][lane] = acc;
+    lds_barrier();
+    if (tid < 128) {  // the waves' sums in wave order, SwiGLU, h
+      const int t = tid >> 3, c = tid & 7;
+      const uint32_t at = red_at + buf * (kNW * 1024) + (t + 16 * (c >> 2)) * 16 + (c & 3) * 4;
+      const float g = join8(at), up = join8(at + 512);
+      const int k = s_k[a][t];
+      if (k != 255) {
+        // h in two bf16 parts: the float's upper half and what is left of it, rounded (2^-16 of h at most is lost).  An even lane
+        // stores its own and its neighbour's upper parts, an odd one the lower ones, through to memory.
+        const float h = silu(g) * up;
+        const uint32_t w = __float_as_uint(h);
+        const float rest = fabsf(h) < INFINITY ? h - __uint_as_float(w & 0xffff0000u) : 0.f;
+        const uint32_t both = (w >> 16) | (f32_to_bf16_rne(rest) << 16);
+        const uint32_t next = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)both, 0xb1, 0xf, 0xf, false);  // quad_perm 1, 0, 3, 2
+        const uint32_t pair = c & 1 ? (next >> 16) | (both & 0xffff0000u) : (both & 0xffffu) | (next << 16);
+        uint16_t* o = p.h + (int64_t)(t * KS + k) * 2 * p.inter + (c & 1 ? p.inter : 0) + tile * 8 + (c & ~1);
+        __hip_atomic_store(reinterpret_cast<uint32_t*>(o), pair, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+    }
+    if (ask) last = __builtin_amdgcn_readfirstlane(s_ctl[buf]);
+    const int next = ask && last < no_more ? tile_of(last) : tiles;
+    q0 = q1;
+    p0 = p1;
+    q1 = deep ? q2 : next;
+    p1 = deep ? p2 : place_of(next);
+    if (deep) {
+      q2 = next;
+      p2 = place_of(next);
+    }
+    buf ^= 1;
+    ++mine;
+  }
+  if (mine > 0) {
+    // This workgroup's h is in memory, past the XCD's L2, before it is counted: its stores went through and are waited for.
+    // (A release fence would write the whole L2 back, one workgroup after the other: 13 us.)
+    wait_vm<0>();
+    __syncthreads();
+    if (tid == 0) __hip_atomic_fetch_add(done, (uint32_t)mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   }
 
   // ---- down ----
-  bool waited = false;
-  while (column_block < blocks) {
-    const int c0 = column_block * R, cols = min(R, p.d - c0);
-    if (!prefilled || waited) {
-      start(DOWN, column_block);
-      for (int s = 0; s < D; ++s) issue(s);
-      slot = 0;
-      prefilled = true;
-    }
-    if (!waited) {
+  for (int block = number; block < blocks; block += gridDim.x) {
+    const int c0 = block * R, cols = min(R, p.d - c0);
+    if (block == number) {
       if (tid == 0) {
         const uint64_t t0 = wall_clock64();
-        while (__hip_atomic_load(done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < (uint32_t)lists) {
-          __builtin_amdgcn_s_sleep(1);
+        while (__hip_atomic_load(done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < (uint32_t)tiles) {
+          __builtin_amdgcn_s_sleep(8);
           if (wall_clock64() - t0 > kWaitTicks) {
-            s_ctl[3] = 1;
+            s_ctl[2] = 1;
             break;
           }
         }
       }
+      // one wave's acquire clears what L1 and L2 hold for the others too (by all waves of all workgroups: 13 us)
+      if (wave == 0) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
       __syncthreads();
-      __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      waited = true;
+    } else {
+      set_block(block);
+      slot = 0;
+#pragma unroll 1
+      for (int s = 0; s < D; ++s) load_step(s, down_step_at(s));
     }
-    const int units = A * slices;
     f32x4 total[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     // this lane's h of a unit: token lr's, or for a token that did not choose the expert one that did (not used)
-    f32x4 raw[F::kUnit][2][F::kVec][2];
-    auto load_h = [&](int a, int sl) __attribute__((always_inline)) {
+    u32x4 raw[F::kUnit][2][F::kVec][2];
+    auto load_h = [&](int a, int e, int sl) __attribute__((always_inline)) {
       const int t = s_k[a][lr] != 255 ? lr : s_first[a];
-      const float* hr = p.h + (int64_t)(t * KS + s_k[a][t]) * p.inter;
+      const uint16_t* hr = p.h + (int64_t)(t * KS + s_k[a][t]) * 2 * p.inter;
 #pragma unroll
       for (int u = 0; u < F::kUnit; ++u) {
-        int b = (sl * F::kUnit + u) * kNW + wave;
-        b = b < nb2 ? b : min(wave, nb2 - 1);
+        const int k1 = block_of(sl * F::kUnit + u, e, nb2) * F::kBlock;
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf) {
-          const int k0 = b * F::kBlock + (FMT == W_FP4 && b * F::kBlock + F::kBlock / 2 >= p.inter ? 0 : hf * (F::kBlock / 2));
+          const int k0 = k1 + (FMT == W_FP4 && k1 + F::kBlock / 2 >= p.inter ? 0 : hf * (F::kBlock / 2)) + lg * (F::kBlock / 8);
 #pragma unroll
           for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) raw[u][hf][v][q] = *(const f32x4*)(hr + k0 + lg * (F::kBlock / 8) + v * 8 + q * 4);
+            for (int q = 0; q < 2; ++q) raw[u][hf][v][q] = *(const u32x4*)(hr + q * p.inter + k0 + v * 8);
         }
       }
     };
-    int a = 0, sl = 0;
-    load_h(0, 0);
+    int a = 0, e = expert(0), sl = 0;  // the unit at work, and the one D steps ahead
+    int la = (D / U) / slices, ls = (D / U) - la * slices;
+    load_h(0, e, 0);
     wait_vm<0>();  // the compiler then counts the next unit's loads against the ring's instead of waiting for all
+#pragma unroll 1
     for (int un = 0; un < units; ++un) {
-      bf16x8_t hh[F::kUnit][2][F::kVec], hl[F::kUnit][2][F::kVec];
+      bf16x8_t h[F::kUnit][2][F::kVec][2];
 #pragma unroll
       for (int u = 0; u < F::kUnit; ++u)
 #pragma unroll
         for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-          for (int v = 0; v < F::kVec; ++v) split8(raw[u][hf][v][0], raw[u][hf][v][1], hh[u][hf][v], hl[u][hf][v]);
-      // the conversion waits for h here, not among the loads below
+          for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
-      for (int u = 0; u < F::kUnit; ++u)
-#pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
-#pragma unroll
-          for (int v = 0; v < F::kVec; ++v) asm volatile("" : "+v"(hh[u][hf][v]), "+v"(hl[u][hf][v]));
-      const int kk = s_k[a][lr], first = sl * F::kUnit * kNW + wave;
+            for (int q = 0; q < 2; ++q) {
+              h[u][hf][v][q] = __builtin_bit_cast(bf16x8_t, raw[u][hf][v][q]);
+              asm volatile("" : "+v"(h[u][hf][v][q]));  // the wait for h is here, not among the loads below
+            }
+      const int kk = s_k[a][lr], i0 = sl * F::kUnit, e0 = e;
       const float gate = kk != 255 ? s_gate[lr * KS + kk] : 0.f;
       if (++sl == slices) {
         sl = 0;
         a = a + 1 < A ? a + 1 : 0;
+        e = expert(a);
       }
-      load_h(a, sl);  // the next unit's (after the last one: the first one's again, not used)
+      load_h(a, e, sl);  // the next unit's (after the last one: the first one's again, not used)
+      const int le = expert(la < A ? la : 0);
+      const Place lp = down_place(le);
       f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
       for (int u = 0; u < F::kUnit; ++u)
@@ -755,9 +819,9 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
         for (int r = 0; r < 2; ++r) {
           wait_vm<F::kWaitDown>();
           const Step s = read_step(slot);
-          issue(slot);
+          load_step(slot, down_step(lp, le, ls, u * 2 + r));
           next_slot();
-          const int b = first + u * kNW;
+          const int b = own_block(i0 + u, e0);
           if (b < nb2) {
             f32x4 part = {0.f, 0.f, 0.f, 0.f};
             if constexpr (FMT != W_E4M3 && FMT != W_E4M3_E8M0) part = acc[r];
@@ -765,15 +829,15 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
 #pragma unroll
             for (int v = 0; v < F::kVec; ++v) {
               const bf16x8_t w = operand<FMT>(s.lo, v, s0);
-              part = mfma_bf16(w, hh[u][0][v], part);
-              part = mfma_bf16(w, hl[u][0][v], part);
+              part = mfma_bf16(w, h[u][0][v][0], part);
+              part = mfma_bf16(w, h[u][0][v][1], part);
             }
             if (FMT != W_FP4 || b * F::kBlock + F::kBlock / 2 < p.inter) {
 #pragma unroll
               for (int v = 0; v < F::kVec; ++v) {
                 const bf16x8_t w = operand<FMT>(s.hi, v, s1);
-                part = mfma_bf16(w, hh[u][1][v], part);
-                part = mfma_bf16(w, hl[u][1][v], part);
+                part = mfma_bf16(w, h[u][1][v][0], part);
+                part = mfma_bf16(w, h[u][1][v][1], part);
               }
             }
             if constexpr (FMT == W_E4M3 || FMT == W_E4M3_E8M0) {
@@ -790,6 +854,10 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
             }
           }
         }
+      if (++ls == slices) {
+        ls = 0;
+        ++la;
+      }
 #pragma unroll
       for (int r = 0; r < 2; ++r)
 #pragma unroll
@@ -798,18 +866,14 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     lds_barrier();  // the sums' space is free
     s_red[0][wave][lane] = total[0];
     s_red[1][wave][lane] = total[1];
-    if (tid == 0) s_ctl[1] = take(block_ticket);
     lds_barrier();
-    {
-      const int t = tid >> 5, c = tid & 31;
-      float v = join8(red_at + (c >> 4) * (kNW * 1024) + (t + 16 * ((c & 15) >> 2)) * 16 + (c & 3) * 4);
-      if (s_ctl[3]) v = __uint_as_float(0x7fc00000u);  // h was never complete
-      if (t < T && c < cols) {
-        uint8_t* o = p.out + t * p.ldo_b;
-        if (p.out_dtype == ROW_F32) reinterpret_cast<float*>(o)[c0 + c] = v;
-        else reinterpret_cast<uint16_t*>(o)[c0 + c] = (uint16_t)f32_to_bf16_rne(v);
-      }
-      column_block = __builtin_amdgcn_readfirstlane(s_ctl[1]);
+    const int t = tid >> 5, c = tid & 31;
+    float v = join8(red_at + (c >> 4) * (kNW * 1024) + (t + 16 * ((c & 15) >> 2)) * 16 + (c & 3) * 4);
+    if (s_ctl[2]) v = __uint_as_float(0x7fc00000u);  // h was never complete
+    if (t < T && c < cols) {
+      uint8_t* o = p.out + t * p.ldo_b;
+      if (p.out_dtype == ROW_F32) reinterpret_cast<float*>(o)[c0 + c] = v;
+      else reinterpret_cast<uint16_t*>(o)[c0 + c] = (uint16_t)f32_to_bf16_rne(v);
     }
     wait_vm<0>();  // the ring is empty again
     lds_barrier();
@@ -924,9 +988,10 @@ extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
   r.eps = q->norm_eps;
   r.wr = q->w_router;
   r.counters = reinterpret_cast<uint32_t*>(ws);
-  r.logits = reinterpret_cast<double*>(ws + L.logits);
+  r.scores = reinterpret_cast<double*>(ws + L.scores);
   r.xn = reinterpret_cast<uint16_t*>(ws + L.xn);
-  decode_rows_kernel<<<q->n_experts, kRowThreads, 0, stream>>>(r);
+  if (norm) decode_rows_kernel<true><<<dim3(q->n_experts, (q->T + 3) / 4), kRowThreads, 0, stream>>>(r);
+  else decode_rows_kernel<false><<<dim3(q->n_experts, (q->T + 3) / 4), kRowThreads, 0, stream>>>(r);
   ExpertArgs a;
   a.xn = norm ? r.xn : static_cast<const uint16_t*>(q->x);
   a.ldxn = norm ? q->d : q->ldx;
@@ -939,9 +1004,9 @@ extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
   a.n_group = q->n_group;
   a.topk_group = q->topk_group;
   a.bias = q->bias;
-  a.logits = r.logits;
+  a.scores = r.scores;
   a.counters = r.counters;
-  a.h = reinterpret_cast<float*>(ws + L.h);
+  a.h = reinterpret_cast<uint16_t*>(ws + L.h);
   a.w13 = static_cast<const uint8_t*>(q->w13);
   a.s13 = static_cast<const uint8_t*>(q->w13_scale);
   a.w2 = static_cast<const uint8_t*>(q->w2);
@@ -952,6 +1017,9 @@ extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
   a.topk_idx = q->topk_idx;
   a.topk_gate = q->topk_gate;
   a.counts = q->expert_counts;
+  const int block = fmt == W_BF16 ? 64 : fmt == W_FP4 ? 256 : 128, depth = fmt == W_FP4 ? Fmt<W_FP4>::kDepth : Fmt<W_BF16>::kDepth;
+  const int per_wave = ((q->d + block - 1) / block + kNW - 1) / kNW;
+  a.ahead = per_wave < depth ? 3 : 2;
   const int grid = compute_units(), threads = kNW * 64;
   switch (fmt) {
     case W_BF16: decode_experts_kernel<W_BF16><<<grid, threads, 0, stream>>>(a); break;
