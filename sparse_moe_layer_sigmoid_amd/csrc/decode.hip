@@ -26,6 +26,8 @@
 // The hand-over: gate/up tiles are dealt out in lists, one per workgroup, by a ticket; a workgroup that has finished its list
 // takes further lists while there are any, so that every list is in the hands of a running workgroup before any workgroup
 // waits for the count of finished lists.  None waits for one that has not started: calls may overlap on the device.
+#include <type_traits>
+
 #include "abi_common.h"
 #include "device_common.h"
 #include "rows_common.h"
@@ -72,45 +74,50 @@ struct RowsArgs {
   const void* bias;
   int w_dtype;
   double eps;
+  int experts;  // per workgroup
   const uint16_t* wr;
   uint32_t* counters;
   double* scores;  // affinities, [T][256]
   uint16_t* xn;
 };
 
-// v's sum over the wave by DPP moves (no LDS), in every lane.
+// Sums by DPP moves (no LDS): over rows of 16 lanes, in lane 15 of each; over the wave, in every lane.
 template <int CTRL, int ROWS>
 __device__ __forceinline__ double dpp_or_zero(double v) {
   const u32x2 w = __builtin_bit_cast(u32x2, v);
   return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[0], CTRL, ROWS, 0xf, false),
                                           (uint32_t)__builtin_amdgcn_update_dpp(0, (int)w[1], CTRL, ROWS, 0xf, false)});
 }
-__device__ __forceinline__ double wave_sum64(double v) {
-  v += dpp_or_zero<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8: lane 15 of each row of 16 has the row's sum
+__device__ __forceinline__ double row_sum64(double v) {
+  v += dpp_or_zero<0x111, 0xf>(v);  // row_shr 1, 2, 4, 8
   v += dpp_or_zero<0x112, 0xf>(v);
   v += dpp_or_zero<0x114, 0xf>(v);
-  v += dpp_or_zero<0x118, 0xf>(v);
+  return v + dpp_or_zero<0x118, 0xf>(v);
+}
+__device__ __forceinline__ double wave_sum64(double v) {
+  v = row_sum64(v);
   v += dpp_or_zero<0x142, 0xa>(v);  // lane 15 to the second row of each half, lane 31 to the upper half
   v += dpp_or_zero<0x143, 0xc>(v);
-  const u32x2 w = __builtin_bit_cast(u32x2, v);
-  return __builtin_bit_cast(double, u32x2{(uint32_t)__builtin_amdgcn_readlane((int)w[0], 63),
-                                          (uint32_t)__builtin_amdgcn_readlane((int)w[1], 63)});
+  return lane_value(v, 63);
 }
 
-// A workgroup per routed expert and four tokens: one chunk of 8 inputs to a lane.
+// A workgroup takes up to four tokens, one chunk of 8 inputs to a lane, and p.experts routed experts, so that the rows are
+// normalised 256 times whatever their number (they come from L2).
 template <bool NORM>
 __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(RowsArgs p) {
-  constexpr int G = 4;
+  constexpr int G = 4, W = kRowThreads / 64;
   static_assert(kMaxD <= 8 * kRowThreads, "one chunk per lane");
-  constexpr int W = kRowThreads / 64;
-  __shared__ double s_sums[NORM ? 2 : 1][W][NORM ? 2 * G : G];
+  static_assert(W == 16, "a row of lanes adds the waves' sums");
+  __shared__ double s_sums[NORM ? W : 1][2 * G];
   __shared__ double s_stat[NORM ? G : 1][2];
-  const int tid = threadIdx.x, c = tid * 8;
-  const int e = blockIdx.x, t0 = blockIdx.y * G, nt = min(G, p.T - t0);
+  __shared__ double s_part[2][W][G];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = tid * 8;
+  const int e0 = blockIdx.x * p.experts, e1 = min(e0 + p.experts, p.N);
+  const int t0 = blockIdx.y * G, nt = min(G, p.T - t0);
   const bool in = c < p.d;
-  if (e == 0 && t0 == 0 && tid < 3) p.counters[tid * 32] = 0;
+  if (e0 == 0 && t0 == 0 && tid < 3) p.counters[tid * 32] = 0;
   u32x4 wv = {0u, 0u, 0u, 0u};
-  if (in && e < p.N) wv = *(const u32x4*)(p.wr + (int64_t)e * p.d + c);
+  if (in) wv = *(const u32x4*)(p.wr + (int64_t)e0 * p.d + c);
   float f[G][8];
 #pragma unroll
   for (int i = 0; i < G; ++i) {
@@ -129,80 +136,77 @@ __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(RowsArgs p) {
     if (p.bias && in) load8_any<true>(p.w_dtype, p.bias, c, p.d, b);
     // In fp64, statistics of x minus the row's first element: there is no range to leave, a mean far from zero cancels
     // nothing, and the rounding to bf16 is that of the exact value but for one in 2^20 or so.
-    double pivot[G], sum[2 * G];
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      const uint8_t* row = p.x + (t0 + min(i, nt - 1)) * p.ldx_b;
-      pivot[i] = p.norm != MOE_NORM_LAYER ? 0.0
-                 : p.x_dtype == ROW_F32   ? (double)*(const float*)row
-                                          : (double)bf16_to_f32(*(const uint16_t*)row);
-      sum[2 * i] = sum[2 * i + 1] = 0.0;
+      if (i >= nt) break;
+      const uint8_t* row = p.x + (t0 + i) * p.ldx_b;
+      const double pivot = p.norm != MOE_NORM_LAYER ? 0.0
+                           : p.x_dtype == ROW_F32   ? (double)*(const float*)row
+                                                    : (double)bf16_to_f32(*(const uint16_t*)row);
+      double s1 = 0.0, s2 = 0.0;
 #pragma unroll
       for (int q = 0; q < 8; ++q) {
-        const double v = in ? (double)f[i][q] - pivot[i] : 0.0;
-        sum[2 * i] += v;
-        sum[2 * i + 1] = fma(v, v, sum[2 * i + 1]);
+        const double v = in ? (double)f[i][q] - pivot : 0.0;
+        s1 += v;
+        s2 = fma(v, v, s2);
       }
-    }
-#pragma unroll
-    for (int i = 0; i < 2 * G; ++i) sum[i] = wave_sum64(sum[i]);
-    if ((tid & 63) == 0) {
-#pragma unroll
-      for (int i = 0; i < 2 * G; ++i) s_sums[0][tid >> 6][i] = sum[i];
+      if (p.norm == MOE_NORM_LAYER) s1 = wave_sum64(s1);
+      s2 = wave_sum64(s2);
+      if (lane == 0) {
+        s_sums[wave][2 * i] = s1;
+        s_sums[wave][2 * i + 1] = s2;
+        if (wave == 0) s_stat[i][0] = pivot;
+      }
     }
     __syncthreads();
-    if (tid < G) {
-      double s1 = 0.0, s2 = 0.0, piv = pivot[0];
-#pragma unroll
-      for (int i = 1; i < G; ++i) piv = tid == i ? pivot[i] : piv;
-      for (int w = 0; w < W; ++w) {
-        s1 += s_sums[0][w][2 * tid];
-        s2 += s_sums[0][w][2 * tid + 1];
+    if (tid < 2 * G * W) {  // row of lanes v: the waves' sums of value v (token v / 2: sum, sum of squares)
+      const int v = tid >> 4, i = v >> 1;
+      const double sum = row_sum64(s_sums[tid & 15][v]);
+      const double s1 = __shfl(sum, (lane & 32) + 15, kWave);
+      if ((tid & 31) == 31 && i < nt) {
+        double mean = 0.0, var = sum / p.d;
+        if (p.norm == MOE_NORM_LAYER) {
+          const double m1 = s1 / p.d;
+          mean = s_stat[i][0] + m1;
+          var -= m1 * m1;
+          if (var < 0.0) var = 0.0;
+        }
+        s_stat[i][0] = mean;
+        s_stat[i][1] = 1.0 / sqrt(var + p.eps);
       }
-      double mean = 0.0, var = s2 / p.d;
-      if (p.norm == MOE_NORM_LAYER) {
-        const double m1 = s1 / p.d;
-        mean = piv + m1;
-        var -= m1 * m1;
-        if (var < 0.0) var = 0.0;
-      }
-      s_stat[tid][0] = mean;
-      s_stat[tid][1] = 1.0 / sqrt(var + p.eps);
     }
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < G; ++i) {
+      if (i >= nt) break;
       const double mean = s_stat[i][0], rstd = s_stat[i][1];
       float y[8];
 #pragma unroll
       for (int q = 0; q < 8; ++q) y[q] = (float)fma(((double)f[i][q] - mean) * rstd, (double)g[q], (double)b[q]);
       const u32x4 o = pack_bf16x8(y);
-      const int t = t0 + i;
-      if (in && i < nt && t % gridDim.x == e) *(u32x4*)(p.xn + (int64_t)t * p.d + c) = o;
+      if (in && (t0 + i) % gridDim.x == blockIdx.x) *(u32x4*)(p.xn + (int64_t)(t0 + i) * p.d + c) = o;
       unpack_bf16x8(o, f[i]);
     }
   }
-  double acc[G];
-  float w[8];
-  unpack_bf16x8(wv, w);
+  for (int e = e0; e < e1; ++e) {
+    float w[8];
+    unpack_bf16x8(wv, w);
+    if (in && e + 1 < e1) wv = *(const u32x4*)(p.wr + (int64_t)(e + 1) * p.d + c);
+    double(*const part)[G] = s_part[e & 1];  // two in turn: a barrier lies between a sum's last reader and its next writer
 #pragma unroll
-  for (int i = 0; i < G; ++i) {
-    acc[i] = 0.0;
+    for (int i = 0; i < G; ++i) {
+      if (i >= nt) break;
+      double acc = 0.0;
 #pragma unroll
-    for (int q = 0; q < 8; ++q) acc[i] += in ? (double)(f[i][q] * w[q]) : 0.0;  // bf16 products are exact in fp32
-  }
-  double(*const part)[NORM ? 2 * G : G] = s_sums[NORM ? 1 : 0];
-#pragma unroll
-  for (int i = 0; i < G; ++i) acc[i] = wave_sum64(acc[i]);
-  if ((tid & 63) == 0) {
-#pragma unroll
-    for (int i = 0; i < G; ++i) part[tid >> 6][i] = acc[i];
-  }
-  __syncthreads();
-  if (tid < nt && e < p.N) {
-    double u = 0.0;
-    for (int w = 0; w < W; ++w) u += part[w][tid];
-    p.scores[(t0 + tid) * 256 + e] = sigmoid_v<double>(u);
+      for (int q = 0; q < 8; ++q) acc += in ? (double)(f[i][q] * w[q]) : 0.0;  // bf16 products are exact in fp32
+      acc = wave_sum64(acc);
+      if (lane == 0) part[wave][i] = acc;
+    }
+    __syncthreads();
+    if (wave == (e & 15)) {
+      const double u = row_sum64(part[lane & 15][lane >> 4]);
+      if ((lane & 15) == 15 && (lane >> 4) < nt) p.scores[(t0 + (lane >> 4)) * 256 + e] = sigmoid_v<double>(u);
+    }
   }
 }
 
@@ -319,11 +323,8 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   auto take = [&](uint32_t* counter) __attribute__((always_inline)) {
     return (int)__hip_atomic_fetch_add(counter + in_vgpr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
-  int number_taken = 0;
-  if (tid == 0) {
+  if (tid == 0)
     s_ctl[3] = (int)__hip_atomic_fetch_add(next_tile + in_vgpr, (uint32_t)p.ahead, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    number_taken = take(p.counters + 64);
-  }
 
   // ---- what is needed of the weights' layout ----
   const int nt = p.inter / 8;                                // tiles of an expert
@@ -431,6 +432,8 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   };
   const int ticket = __builtin_amdgcn_readfirstlane(s_ctl[3]);
   const int first = tile_of(ticket);
+  int number_taken = 0;  // looked at after the selection
+  if (tid == 0) number_taken = take(p.counters + 64);
 
   // the shared expert's tiles come first: their weights are on the way while the routed ones are being chosen
   int loaded = 0;
@@ -767,8 +770,9 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     }
     f32x4 total[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
     // this lane's h of a unit: token lr's, or for a token that did not choose the expert one that did (not used)
-    u32x4 raw[F::kUnit][2][F::kVec][2];
-    auto load_h = [&](int a, int e, int sl) __attribute__((always_inline)) {
+    u32x4 raw[2][F::kUnit][2][F::kVec][2];  // of the next two units
+    auto load_h = [&](auto set_c, int a, int e, int sl) __attribute__((always_inline)) {
+      constexpr int S = decltype(set_c)::value;
       const int t = s_k[a][lr] != 255 ? lr : s_first[a];
       const uint16_t* hr = p.h + (int64_t)(t * KS + s_k[a][t]) * 2 * p.inter;
 #pragma unroll
@@ -780,16 +784,28 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
 #pragma unroll
           for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
-            for (int q = 0; q < 2; ++q) raw[u][hf][v][q] = *(const u32x4*)(hr + q * p.inter + k0 + v * 8);
+            for (int q = 0; q < 2; ++q) raw[S][u][hf][v][q] = *(const u32x4*)(hr + q * p.inter + k0 + v * 8);
         }
       }
     };
-    int a = 0, e = expert(0), sl = 0;  // the unit at work, and the one D steps ahead
+    int a = 0, e = expert(0), sl = 0;  // the unit at work; (na, ne, ns) the one whose h is loaded next; (la, ls) D steps ahead
+    int na = 0, ne = e, ns = 0;
     int la = (D / U) / slices, ls = (D / U) - la * slices;
-    load_h(0, e, 0);
-    wait_vm<0>();  // the compiler then counts the next unit's loads against the ring's instead of waiting for all
-#pragma unroll 1
-    for (int un = 0; un < units; ++un) {
+    auto next_h = [&]() __attribute__((always_inline)) {  // past the end the first units' again, not used
+      if (++ns == slices) {
+        ns = 0;
+        na = na + 1 < A ? na + 1 : 0;
+        ne = expert(na);
+      }
+    };
+    load_h(std::integral_constant<int, 0>(), na, ne, ns);
+    next_h();
+    load_h(std::integral_constant<int, 1>(), na, ne, ns);
+    next_h();
+    wait_vm<0>();  // the compiler then counts the next units' loads against the ring's instead of waiting for all
+    auto unit = [&](auto set_c, auto ends_c) __attribute__((always_inline)) {
+      constexpr int S = decltype(set_c)::value;
+      constexpr bool kEnds = decltype(ends_c)::value;  // the last unit: nothing loads h any more, and no wait may count on it
       bf16x8_t h[F::kUnit][2][F::kVec][2];
 #pragma unroll
       for (int u = 0; u < F::kUnit; ++u)
@@ -799,7 +815,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
           for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
             for (int q = 0; q < 2; ++q) {
-              h[u][hf][v][q] = __builtin_bit_cast(bf16x8_t, raw[u][hf][v][q]);
+              h[u][hf][v][q] = __builtin_bit_cast(bf16x8_t, raw[S][u][hf][v][q]);
               asm volatile("" : "+v"(h[u][hf][v][q]));  // the wait for h is here, not among the loads below
             }
       const int kk = s_k[a][lr], i0 = sl * F::kUnit, e0 = e;
@@ -809,7 +825,10 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
         a = a + 1 < A ? a + 1 : 0;
         e = expert(a);
       }
-      load_h(a, e, sl);  // the next unit's (after the last one: the first one's again, not used)
+      if constexpr (!kEnds) {
+        load_h(set_c, na, ne, ns);
+        next_h();
+      }
       const int le = expert(la < A ? la : 0);
       const Place lp = down_place(le);
       f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
@@ -817,7 +836,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       for (int u = 0; u < F::kUnit; ++u)
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
-          wait_vm<F::kWaitDown>();
+          wait_vm<kEnds ? F::kWaitDown - 16 : F::kWaitDown>();
           const Step s = read_step(slot);
           load_step(slot, down_step(lp, le, ls, u * 2 + r));
           next_slot();
@@ -862,7 +881,13 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       for (int r = 0; r < 2; ++r)
 #pragma unroll
         for (int q = 0; q < 4; ++q) total[r][q] = kk != 255 ? fmaf(gate, acc[r][q], total[r][q]) : total[r][q];
+    };
+#pragma unroll 1
+    for (int un = 0; un < units / 2; ++un) {
+      unit(std::integral_constant<int, 0>(), std::false_type());
+      unit(std::integral_constant<int, 1>(), std::false_type());
     }
+    if (units & 1) unit(std::integral_constant<int, 0>(), std::true_type());
     lds_barrier();  // the sums' space is free
     s_red[0][wave][lane] = total[0];
     s_red[1][wave][lane] = total[1];
@@ -990,8 +1015,11 @@ extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
   r.counters = reinterpret_cast<uint32_t*>(ws);
   r.scores = reinterpret_cast<double*>(ws + L.scores);
   r.xn = reinterpret_cast<uint16_t*>(ws + L.xn);
-  if (norm) decode_rows_kernel<true><<<dim3(q->n_experts, (q->T + 3) / 4), kRowThreads, 0, stream>>>(r);
-  else decode_rows_kernel<false><<<dim3(q->n_experts, (q->T + 3) / 4), kRowThreads, 0, stream>>>(r);
+  const int token_groups = (q->T + 3) / 4;
+  r.experts = token_groups;  // as many workgroups as experts: all at once on the card
+  const dim3 rows_grid((q->n_experts + r.experts - 1) / r.experts, token_groups);
+  if (norm) decode_rows_kernel<true><<<rows_grid, kRowThreads, 0, stream>>>(r);
+  else decode_rows_kernel<false><<<rows_grid, kRowThreads, 0, stream>>>(r);
   ExpertArgs a;
   a.xn = norm ? r.xn : static_cast<const uint16_t*>(q->x);
   a.ldxn = norm ? q->d : q->ldx;
