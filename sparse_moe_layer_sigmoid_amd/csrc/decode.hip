@@ -44,6 +44,7 @@ constexpr int kMaxTopK = 32;
 constexpr int kMaxD = 8192;       // inputs a workgroup's waves hold in registers
 constexpr int kNW = 8;            // waves of a workgroup
 constexpr int kMaxActive = 257;
+constexpr int kJoiners = 2;       // waves that add the waves' sums: a token's 8 columns of a tile to 8 lanes
 constexpr int kRowThreads = 1024;
 constexpr uint64_t kWaitTicks = 500000000ull;  // 5 s of the 100 MHz clock: bound of the wait for h
 
@@ -268,20 +269,20 @@ __device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t v, ui
 
 __device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
 
-template <int FMT>
+template <int FMT, bool WIDE = false>
 struct Fmt {
   static constexpr bool kScaled = FMT != W_BF16;
   static constexpr int kBlock = FMT == W_BF16 ? 64 : FMT == W_FP4 ? 256 : 128;  // inputs in 128 bytes of a weight row
   static constexpr int kVec = kBlock / 64;              // operands of 8 inputs per lane in half a block
   static constexpr int kSteps = kMaxD / kBlock / kNW;   // blocks per wave of a gate/up tile at most
-  static constexpr int kUnit = 256 / kBlock;            // blocks per wave of a unit of the down projection
   static constexpr int kSlot = 2048 + (kScaled ? 128 : 0);  // a step's weights and scales
-  // Steps in flight per wave: as many as LDS holds, and in the down projection a whole number of units (of 2 * kUnit steps)
-  // whose loads, with the 16 loads of h that each unit adds, can still be counted (see wait_step)
-  static constexpr int kDepth = FMT == W_FP4 ? 6 : 8;
+  static constexpr int kDepth = FMT == W_FP4 ? 6 : 8;   // steps in flight per wave: as many as LDS holds, an even number
   static constexpr int kLoads = kScaled ? 3 : 2;        // loads of a step
   static constexpr int kWaitUp = kLoads * (kDepth - 1);
-  static constexpr int kWaitDown = kWaitUp + kDepth / (2 * kUnit) * 16;
+  // down: a unit is an expert's next 8 blocks of inner columns, one per wave, two steps; each brings kParts * 2 * kVec loads of h
+  static constexpr int kParts = WIDE ? 2 : 1;
+  static constexpr int kSets = FMT == W_BF16 ? 4 : 2;   // units that h is loaded ahead
+  static constexpr int kWaitDown = kWaitUp + kDepth / 2 * kParts * 2 * kVec;
 };
 
 // 8 weights of a step's half block: dword pairs (bf16: the 16 bytes), its operand `s`.
@@ -293,12 +294,13 @@ __device__ __forceinline__ bf16x8_t operand(const u32x4& q, int s, float scale) 
   else return decode_e4m3(q[2 * s], q[2 * s + 1]);
 }
 
-template <int FMT>
+// WIDE: more than 8 tokens.  h is in two bf16 parts; of up to 8 tokens the lower parts are columns of their own, t + 8, else
+// products of their own (the two sums meet at the end either way: the same bits).
+template <int FMT, bool WIDE>
 __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs p) {
-  using F = Fmt<FMT>;
-  constexpr int D = F::kDepth, SLOT = F::kSlot;
-  constexpr int U = 2 * F::kUnit;  // steps of a unit of the down projection: (expert, slice of the inner width)
-  static_assert(D % U == 0 && F::kSteps >= D / 2, "the ring holds whole units, and at most two tiles ahead");
+  using F = Fmt<FMT, WIDE>;
+  constexpr int D = F::kDepth, SLOT = F::kSlot, P = F::kParts;
+  static_assert(D % 2 == 0 && F::kSteps >= D / 2, "the ring holds whole units, and at most two tiles ahead");
   __shared__ __attribute__((aligned(1024))) uint8_t s_ring[kNW * D * SLOT];
   __shared__ __attribute__((aligned(16))) f32x4 s_red[2][kNW][64];
   __shared__ float s_gate[kMaxT * (kMaxTopK + 1)];  // gate of slot t (K + n_shared) + k
@@ -404,6 +406,9 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   double u[4];
 #pragma unroll
   for (int r = 0; r < 4; ++r) u[r] = wave < T && lane * 4 + r < p.N ? p.scores[wave * 256 + lane * 4 + r] : 0.0;
+  float bias[4];
+#pragma unroll
+  for (int r = 0; r < 4; ++r) bias[r] = lane * 4 + r < p.N ? p.bias[lane * 4 + r] : 0.f;
   bf16x8_t x[F::kSteps][2][F::kVec];  // this wave's blocks of all tokens (columns past T hold the last token again)
   {
     const uint16_t* xr = p.xn + (int64_t)min(lr, T - 1) * p.ldxn;
@@ -452,7 +457,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       for (int r = 0; r < 4; ++r) u[r] = lane * 4 + r < p.N ? p.scores[t * 256 + lane * 4 + r] : 0.0;
     }
     float* const gate = s_gate + t * (KS - K);  // select_token writes at t * K + k; rows here are KS apart
-    select_token<double, true>(u, p.bias, p.N, K, p.n_group, p.topk_group, t, true, s_idx, gate, nullptr);
+    select_token<double, true>(u, bias, p.N, K, p.n_group, p.topk_group, t, true, s_idx, gate, nullptr);
     if (lane == 0 && p.n_shared) s_gate[t * KS + K] = 1.0f;
   }
   lds_barrier();
@@ -499,7 +504,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   // every gridDim.x-th from there): no other workgroup needs them, so they may wait for one that starts late ----
   const int R = min(32, (((p.d + (int)gridDim.x - 1) / (int)gridDim.x) + 3) & ~3);
   const int blocks = (p.d + R - 1) / R;
-  const int slices = (nb2 + kNW * F::kUnit - 1) / (kNW * F::kUnit);
+  const int slices = (nb2 + kNW - 1) / kNW;                  // units of an expert
   const int units = A * slices;
   uint32_t dn_v[4], dn_vs[2];  // this lane's rows of a block, two times 16
   auto set_block = [&](int block) __attribute__((always_inline)) {
@@ -516,9 +521,9 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     q.sc = p.s2 + e * scale_bytes(p.d, nb2, p.inter);
     return q;
   };
-  auto down_step = [&](const Place& q, int e, int sl, int i) __attribute__((always_inline)) {  // step i of slice sl
-    Source r = {q, row2_b, block_of(sl * F::kUnit + (i >> 1), e, nb2), dn_v[0], dn_v[1], 0, dn_vs[0]};
-    if (i & 1) {
+  auto down_step = [&](const Place& q, int e, int sl, int i) __attribute__((always_inline)) {  // step i of unit sl of expert e
+    Source r = {q, row2_b, block_of(sl, e, nb2), dn_v[0], dn_v[1], 0, dn_vs[0]};
+    if (i) {
       r.v0 = dn_v[2];
       r.v1 = dn_v[3];
       r.vs = dn_vs[1];
@@ -526,11 +531,11 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     return r;
   };
   auto down_step_at = [&](int c) __attribute__((always_inline)) {  // step c of the block (past its end: step 0's, unused)
-    int un = c / U;
+    int un = c / 2;
     un = un < units ? un : 0;
     const int a = slices == 1 ? un : (int)((uint32_t)un / (uint32_t)slices);
     const int e = expert(a);
-    return down_step(down_place(e), e, un - a * slices, c % U);
+    return down_step(down_place(e), e, un - a * slices, c & 1);
   };
   set_block(number < blocks ? number : 0);
 
@@ -634,8 +639,11 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     if (id < tiles) {
       r = up_step(q, ahead - k * steps);
     } else {
+      // The waves that store h wait for their stores before these are counted, and so for whatever they loaded before: a step of
+      // the tile at work again instead (it is in L2), the down projection's later.
       const int have = (q0 < tiles) + (q1 < tiles) + (q2 < tiles);  // they are taken in order
-      r = down_step_at(ahead - have * steps);
+      if (wave < kJoiners) r = up_step(p0, 0);
+      else r = down_step_at(ahead - have * steps);
     }
     load_step(slot, r);
   };
@@ -706,7 +714,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     }
     s_red[buf][wave][lane] = acc;
     lds_barrier();
-    if (tid < 128) {  // the waves' sums in wave order, SwiGLU, h
+    if (wave < kJoiners) {  // the waves' sums in wave order, SwiGLU, h
       const int t = tid >> 3, c = tid & 7;
       const uint32_t at = red_at + buf * (kNW * 1024) + (t + 16 * (c >> 2)) * 16 + (c & 3) * 4;
       const float g = join8(at), up = join8(at + 512);
@@ -740,9 +748,14 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   if (mine > 0) {
     // This workgroup's h is in memory, past the XCD's L2, before it is counted: its stores went through and are waited for.
     // (A release fence would write the whole L2 back, one workgroup after the other: 13 us.)
-    wait_vm<0>();
-    __syncthreads();
+    if (wave < kJoiners) wait_vm<0>();
+    lds_barrier();
     if (tid == 0) __hip_atomic_fetch_add(done, (uint32_t)mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  }
+  if (wave < kJoiners) {
+    wait_vm<0>();
+#pragma unroll 1
+    for (int s = 0; s < D; ++s) load_step(slot + s < D ? slot + s : slot + s - D, down_step_at(s));
   }
 
   // ---- down ----
@@ -761,136 +774,134 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       }
       // one wave's acquire clears what L1 and L2 hold for the others too (by all waves of all workgroups: 13 us)
       if (wave == 0) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-      __syncthreads();
+      lds_barrier();
     } else {
       set_block(block);
       slot = 0;
 #pragma unroll 1
       for (int s = 0; s < D; ++s) load_step(s, down_step_at(s));
     }
-    f32x4 total[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
-    // this lane's h of a unit: token lr's, or for a token that did not choose the expert one that did (not used)
-    u32x4 raw[2][F::kUnit][2][F::kVec][2];  // of the next two units
+    f32x4 total[2][P];
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int q = 0; q < P; ++q) total[r][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // This lane's h of a unit: its column's token's, or for a token that did not choose the expert one that did (not used).
+    const int col = WIDE ? lr : lr & 7, lower = WIDE || lr < 8 ? 0 : p.inter;
+    u32x4 raw[F::kSets][2][F::kVec][P];  // of the next units
     auto load_h = [&](auto set_c, int a, int e, int sl) __attribute__((always_inline)) {
       constexpr int S = decltype(set_c)::value;
-      const int t = s_k[a][lr] != 255 ? lr : s_first[a];
-      const uint16_t* hr = p.h + (int64_t)(t * KS + s_k[a][t]) * 2 * p.inter;
+      const int t = s_k[a][col] != 255 ? col : s_first[a];
+      const uint16_t* hr = p.h + (int64_t)(t * KS + s_k[a][t]) * 2 * p.inter + lower;
+      const int k1 = block_of(sl, e, nb2) * F::kBlock;
 #pragma unroll
-      for (int u = 0; u < F::kUnit; ++u) {
-        const int k1 = block_of(sl * F::kUnit + u, e, nb2) * F::kBlock;
+      for (int hf = 0; hf < 2; ++hf) {
+        const int k0 = k1 + (FMT == W_FP4 && k1 + F::kBlock / 2 >= p.inter ? 0 : hf * (F::kBlock / 2)) + lg * (F::kBlock / 8);
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf) {
-          const int k0 = k1 + (FMT == W_FP4 && k1 + F::kBlock / 2 >= p.inter ? 0 : hf * (F::kBlock / 2)) + lg * (F::kBlock / 8);
+        for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
-          for (int v = 0; v < F::kVec; ++v)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) raw[S][u][hf][v][q] = *(const u32x4*)(hr + q * p.inter + k0 + v * 8);
-        }
+          for (int q = 0; q < P; ++q) raw[S][hf][v][q] = *(const u32x4*)(hr + q * p.inter + k0 + v * 8);
       }
     };
     int a = 0, e = expert(0), sl = 0;  // the unit at work; (na, ne, ns) the one whose h is loaded next; (la, ls) D steps ahead
     int na = 0, ne = e, ns = 0;
-    int la = (D / U) / slices, ls = (D / U) - la * slices;
-    auto next_h = [&]() __attribute__((always_inline)) {  // past the end the first units' again, not used
+    int la = (D / 2) / slices, ls = (D / 2) - la * slices;
+    auto load_next_h = [&](auto set_c) __attribute__((always_inline)) {  // past the end the first units' again, not used
+      load_h(set_c, na, ne, ns);
       if (++ns == slices) {
         ns = 0;
         na = na + 1 < A ? na + 1 : 0;
         ne = expert(na);
       }
     };
-    load_h(std::integral_constant<int, 0>(), na, ne, ns);
-    next_h();
-    load_h(std::integral_constant<int, 1>(), na, ne, ns);
-    next_h();
+    load_next_h(std::integral_constant<int, 0>());
+    load_next_h(std::integral_constant<int, 1>());
+    if constexpr (F::kSets == 4) {
+      load_next_h(std::integral_constant<int, 2>());
+      load_next_h(std::integral_constant<int, 3>());
+    }
     wait_vm<0>();  // the compiler then counts the next units' loads against the ring's instead of waiting for all
-    auto unit = [&](auto set_c, auto ends_c) __attribute__((always_inline)) {
+    // (Every unit loads, also those that only round their number up: the waits count on it.)
+    auto unit = [&](auto set_c, bool live) __attribute__((always_inline)) {
       constexpr int S = decltype(set_c)::value;
-      constexpr bool kEnds = decltype(ends_c)::value;  // the last unit: nothing loads h any more, and no wait may count on it
-      bf16x8_t h[F::kUnit][2][F::kVec][2];
+      bf16x8_t h[2][F::kVec][P];
 #pragma unroll
-      for (int u = 0; u < F::kUnit; ++u)
+      for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
-        for (int hf = 0; hf < 2; ++hf)
+        for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
-          for (int v = 0; v < F::kVec; ++v)
-#pragma unroll
-            for (int q = 0; q < 2; ++q) {
-              h[u][hf][v][q] = __builtin_bit_cast(bf16x8_t, raw[S][u][hf][v][q]);
-              asm volatile("" : "+v"(h[u][hf][v][q]));  // the wait for h is here, not among the loads below
-            }
-      const int kk = s_k[a][lr], i0 = sl * F::kUnit, e0 = e;
-      const float gate = kk != 255 ? s_gate[lr * KS + kk] : 0.f;
+          for (int q = 0; q < P; ++q) {
+            h[hf][v][q] = __builtin_bit_cast(bf16x8_t, raw[S][hf][v][q]);
+            asm volatile("" : "+v"(h[hf][v][q]));  // the wait for h is here, not among the loads below
+          }
+      const int kk = live ? s_k[a][col] : 255;
+      const float gate = kk != 255 ? s_gate[col * KS + kk] : 0.f;
+      const int b = own_block(sl, e);
       if (++sl == slices) {
         sl = 0;
         a = a + 1 < A ? a + 1 : 0;
         e = expert(a);
       }
-      if constexpr (!kEnds) {
-        load_h(set_c, na, ne, ns);
-        next_h();
-      }
+      load_next_h(set_c);
       const int le = expert(la < A ? la : 0);
       const Place lp = down_place(le);
-      f32x4 acc[2] = {f32x4{0.f, 0.f, 0.f, 0.f}, f32x4{0.f, 0.f, 0.f, 0.f}};
 #pragma unroll
-      for (int u = 0; u < F::kUnit; ++u)
+      for (int r = 0; r < 2; ++r) {
+        wait_vm<F::kWaitDown>();
+        const Step s = read_step(slot);
+        load_step(slot, down_step(lp, le, ls, r));
+        next_slot();
+        if (b < nb2) {
+          f32x4 part[P];
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
-          wait_vm<kEnds ? F::kWaitDown - 16 : F::kWaitDown>();
-          const Step s = read_step(slot);
-          load_step(slot, down_step(lp, le, ls, u * 2 + r));
-          next_slot();
-          const int b = own_block(i0 + u, e0);
-          if (b < nb2) {
-            f32x4 part = {0.f, 0.f, 0.f, 0.f};
-            if constexpr (FMT != W_E4M3 && FMT != W_E4M3_E8M0) part = acc[r];
-            const float s0 = __uint_as_float(s.sc[0] << 23), s1 = __uint_as_float(s.sc[1] << 23);
+          for (int q = 0; q < P; ++q) part[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+          const float s0 = __uint_as_float(s.sc[0] << 23), s1 = __uint_as_float(s.sc[1] << 23);
+#pragma unroll
+          for (int v = 0; v < F::kVec; ++v) {
+            const bf16x8_t w = operand<FMT>(s.lo, v, s0);
+#pragma unroll
+            for (int q = 0; q < P; ++q) part[q] = mfma_bf16(w, h[0][v][q], part[q]);
+          }
+          if (FMT != W_FP4 || b * F::kBlock + F::kBlock / 2 < p.inter) {
 #pragma unroll
             for (int v = 0; v < F::kVec; ++v) {
-              const bf16x8_t w = operand<FMT>(s.lo, v, s0);
-              part = mfma_bf16(w, h[u][0][v][0], part);
-              part = mfma_bf16(w, h[u][0][v][1], part);
-            }
-            if (FMT != W_FP4 || b * F::kBlock + F::kBlock / 2 < p.inter) {
+              const bf16x8_t w = operand<FMT>(s.hi, v, s1);
 #pragma unroll
-              for (int v = 0; v < F::kVec; ++v) {
-                const bf16x8_t w = operand<FMT>(s.hi, v, s1);
-                part = mfma_bf16(w, h[u][1][v][0], part);
-                part = mfma_bf16(w, h[u][1][v][1], part);
-              }
-            }
-            if constexpr (FMT == W_E4M3 || FMT == W_E4M3_E8M0) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) acc[r][q] = fmaf(part[q], row_scale(s, b, q), acc[r][q]);
-            } else {
-              acc[r] = part;
+              for (int q = 0; q < P; ++q) part[q] = mfma_bf16(w, h[1][v][q], part[q]);
             }
           }
-          if constexpr (FMT == W_I8) {
-            if (u == F::kUnit - 1) {
 #pragma unroll
-              for (int q = 0; q < 4; ++q) acc[r][q] *= __uint_as_float(s.sc[q]);
+          for (int q = 0; q < P; ++q)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              float v = part[q][i];
+              if constexpr (FMT == W_E4M3 || FMT == W_E4M3_E8M0 || FMT == W_I8) v *= row_scale(s, b, i);
+              total[r][q][i] = kk != 255 ? fmaf(gate, v, total[r][q][i]) : total[r][q][i];
             }
-          }
         }
+      }
       if (++ls == slices) {
         ls = 0;
         ++la;
       }
-#pragma unroll
-      for (int r = 0; r < 2; ++r)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) total[r][q] = kk != 255 ? fmaf(gate, acc[r][q], total[r][q]) : total[r][q];
     };
 #pragma unroll 1
-    for (int un = 0; un < units / 2; ++un) {
-      unit(std::integral_constant<int, 0>(), std::false_type());
-      unit(std::integral_constant<int, 1>(), std::false_type());
+    for (int un = 0; un < units; un += F::kSets) {
+      unit(std::integral_constant<int, 0>(), true);
+      unit(std::integral_constant<int, 1>(), un + 1 < units);
+      if constexpr (F::kSets == 4) {
+        unit(std::integral_constant<int, 2>(), un + 2 < units);
+        unit(std::integral_constant<int, 3>(), un + 3 < units);
+      }
     }
-    if (units & 1) unit(std::integral_constant<int, 0>(), std::true_type());
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)  // upper and lower parts: column t + 8 holds the latter, or the other sum
+        total[r][0][i] += WIDE ? total[r][P - 1][i] : __uint_as_float(row_ror<8>(__float_as_uint(total[r][0][i])));
     lds_barrier();  // the sums' space is free
-    s_red[0][wave][lane] = total[0];
-    s_red[1][wave][lane] = total[1];
+    s_red[0][wave][lane] = total[0][0];
+    s_red[1][wave][lane] = total[1][0];
     lds_barrier();
     const int t = tid >> 5, c = tid & 31;
     float v = join8(red_at + (c >> 4) * (kNW * 1024) + (t + 16 * ((c & 15) >> 2)) * 16 + (c & 3) * 4);
@@ -912,6 +923,12 @@ int compute_units() {
       v >= 1)
     return v;
   return 256;
+}
+
+template <int FMT>
+void launch_experts(const ExpertArgs& a, int grid, hipStream_t stream) {
+  if (a.T > 8) decode_experts_kernel<FMT, true><<<grid, kNW * 64, 0, stream>>>(a);
+  else decode_experts_kernel<FMT, false><<<grid, kNW * 64, 0, stream>>>(a);
 }
 
 bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
@@ -1048,13 +1065,13 @@ extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
   const int block = fmt == W_BF16 ? 64 : fmt == W_FP4 ? 256 : 128, depth = fmt == W_FP4 ? Fmt<W_FP4>::kDepth : Fmt<W_BF16>::kDepth;
   const int per_wave = ((q->d + block - 1) / block + kNW - 1) / kNW;
   a.ahead = per_wave < depth ? 3 : 2;
-  const int grid = compute_units(), threads = kNW * 64;
+  const int grid = compute_units();
   switch (fmt) {
-    case W_BF16: decode_experts_kernel<W_BF16><<<grid, threads, 0, stream>>>(a); break;
-    case W_E4M3: decode_experts_kernel<W_E4M3><<<grid, threads, 0, stream>>>(a); break;
-    case W_E4M3_E8M0: decode_experts_kernel<W_E4M3_E8M0><<<grid, threads, 0, stream>>>(a); break;
-    case W_I8: decode_experts_kernel<W_I8><<<grid, threads, 0, stream>>>(a); break;
-    default: decode_experts_kernel<W_FP4><<<grid, threads, 0, stream>>>(a); break;
+    case W_BF16: launch_experts<W_BF16>(a, grid, stream); break;
+    case W_E4M3: launch_experts<W_E4M3>(a, grid, stream); break;
+    case W_E4M3_E8M0: launch_experts<W_E4M3_E8M0>(a, grid, stream); break;
+    case W_I8: launch_experts<W_I8>(a, grid, stream); break;
+    default: launch_experts<W_FP4>(a, grid, stream); break;
   }
   return check_launch("moe_decode");
 }

@@ -43,6 +43,12 @@ constexpr int kRows = kTM + 256;     // LDS rows per stage: kTM tokens + 256 rou
 constexpr int kLogitsThreads = 512;  // 8 waves: 2 token halves x 4 expert quarters, 64 x 64 each
 constexpr int kChunks = kRows * 8 / kLogitsThreads;  // 16-byte chunks per thread per stage
 
+__device__ __forceinline__ void load_bias(const float* __restrict__ bias, int N, float b[4]) {
+  const int e = (threadIdx.x & 63) * 4;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) b[r] = e + r < N ? bias[e + r] : 0.f;
+}
+
 // ---- kernel 1: split-K logits ----
 __global__ __launch_bounds__(kLogitsThreads) void route_logits_kernel(const uint16_t* __restrict__ x,
                                                            const uint16_t* __restrict__ wr,
@@ -179,7 +185,9 @@ __global__ __launch_bounds__(256) void route_select_kernel(const float* __restri
 #pragma unroll
     for (int r = 0; r < 4; ++r) u[r] += v[r];
   }
-  const float margin = select_token<float>(u, bias, N, K, n_group, topk_group, t, true, topk_idx, topk_gate, scores);
+  float b[4];
+  load_bias(bias, N, b);
+  const float margin = select_token<float>(u, b, N, K, n_group, topk_group, t, true, topk_idx, topk_gate, scores);
   if (lane == 0 && margin < kRefineGap) flagged[atomicAdd(n_flagged, 1)] = (int32_t)t;
 }
 
@@ -266,7 +274,9 @@ __global__ __launch_bounds__(256) void route_refine_select_kernel(const float* _
     double u[4];
 #pragma unroll
     for (int r = 0; r < 4; ++r) u[r] = (lane * 4 + r < N) ? l64[(int64_t)i * 256 + lane * 4 + r] : 0.0;
-    select_token<double>(u, bias, N, K, n_group, topk_group, t, true, topk_idx, topk_gate, scores);
+    float b[4];
+    load_bias(bias, N, b);
+    select_token<double>(u, b, N, K, n_group, topk_group, t, true, topk_idx, topk_gate, scores);
   }
 }
 

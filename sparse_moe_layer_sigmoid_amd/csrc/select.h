@@ -72,13 +72,13 @@ __device__ __forceinline__ float sigmoid_v<float>(float u) { return 1.0f / (1.0f
 template <>
 __device__ __forceinline__ double sigmoid_v<double>(double u) { return 1.0 / (1.0 + exp(-u)); }
 
-// Selection for one token by one wave.  u[r] is the logit (AFFINITY: the affinity) of expert 4*lane + r.  Writes the
+// Selection for one token by one wave.  u[r] is the logit (AFFINITY: the affinity) of expert 4*lane + r, bias[r] its bias.  Writes the
 // outputs when `write`; returns the decision margin (min of the expert gap and half the
 // group gap), +inf when nothing competes.
 template <typename V, bool AFFINITY = false>
-__device__ __forceinline__ V select_token(const V u[4], const float* __restrict__ bias, int N, int K, int n_group,
-                          int topk_group, int64_t t, bool write, int32_t* __restrict__ topk_idx,
-                          float* __restrict__ topk_gate, float* __restrict__ scores) {
+__device__ __forceinline__ V select_token(const V u[4], const float bias[4], int N, int K, int n_group, int topk_group, int64_t t,
+                                          bool write, int32_t* __restrict__ topk_idx, float* __restrict__ topk_gate,
+                                          float* __restrict__ scores) {
   const int lane = threadIdx.x & 63;
   const V inf = (V)INFINITY;
   V s4[4], z4[4];
@@ -88,7 +88,7 @@ __device__ __forceinline__ V select_token(const V u[4], const float* __restrict_
     const int e = lane * 4 + r;
     if (e < N) {
       const V s = AFFINITY ? u[r] : sigmoid_v<V>(u[r]);
-      V z = s + (V)bias[e];
+      V z = s + (V)bias[r];
       if (z != z) z = -inf;  // NaN ranks below every number
       s4[r] = s;
       z4[r] = z;
