@@ -49,7 +49,9 @@ constexpr int kRowThreads = 1024;
 constexpr uint64_t kWaitTicks = 500000000ull;  // 5 s of the 100 MHz clock: bound of the wait for h
 
 // Workspace: counters, affinities, normalised rows, h.
-constexpr size_t kCounterBytes = 512;  // the next tile, finished tiles, started workgroups: 128 bytes apart
+constexpr int kFlags = 16;  // "h is complete", for a workgroup in 16 each
+constexpr int kCounters = 3 + kFlags;  // the next tile, finished tiles, started workgroups, flags: 128 bytes apart
+constexpr size_t kCounterBytes = (kCounters * 128 + 255) & ~255;
 constexpr size_t kScoreBytes = (size_t)kMaxT * 256 * sizeof(double);
 struct DecodeWs {
   size_t scores, xn, h, total;
@@ -116,7 +118,7 @@ __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(RowsArgs p) {
   const int e0 = blockIdx.x * p.experts, e1 = min(e0 + p.experts, p.N);
   const int t0 = blockIdx.y * G, nt = min(G, p.T - t0);
   const bool in = c < p.d;
-  if (e0 == 0 && t0 == 0 && tid < 3) p.counters[tid * 32] = 0;
+  if (e0 == 0 && t0 == 0 && tid < kCounters) p.counters[tid * 32] = 0;
   u32x4 wv = {0u, 0u, 0u, 0u};
   if (in) wv = *(const u32x4*)(p.wr + (int64_t)e0 * p.d + c);
   float f[G][8];
@@ -267,6 +269,17 @@ __device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t v, ui
 #endif
 }
 
+// 16 bytes at base + v; zeros, and no memory access, for a lane whose v is kNoLoad.
+constexpr uint32_t kNoLoad = 0xffffffffu;
+__device__ __forceinline__ u32x4 load16_if(const void* base, uint32_t v) {
+#ifdef __HIP_DEVICE_COMPILE__
+  const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0xffffff00u, 0x00020000);
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, v, 0, 0));
+#else
+  return u32x4{v, 0u, 0u, 0u};
+#endif
+}
+
 __device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
 
 template <int FMT, bool WIDE = false>
@@ -306,7 +319,6 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   __shared__ float s_gate[kMaxT * (kMaxTopK + 1)];  // gate of slot t (K + n_shared) + k
   __shared__ __attribute__((aligned(16))) uint8_t s_k[kMaxActive][kMaxT];  // k of a token's active expert, 255: not chosen
   __shared__ uint16_t s_exp[kMaxActive];            // active experts, the shared one first
-  __shared__ uint8_t s_first[kMaxActive];           // a token that chose it
   __shared__ int s_ctl[5];                          // tiles taken (two in turn), gave up waiting, first tile, number
   // of the selection, before the sums need the space
   uint32_t* const s_mask = reinterpret_cast<uint32_t*>(&s_red[0][0][0]);
@@ -473,14 +485,10 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     at += __popcll(any & ((1ull << lane) - 1));
     if (mask != 0) {
       s_exp[at] = (uint16_t)tid;
-      s_first[at] = (uint8_t)__builtin_ctz(mask);
       s_pos[tid] = at;
     }
     if (tid == 0) {
-      if (p.n_shared) {
-        s_exp[0] = (uint16_t)p.N;
-        s_first[0] = 0;
-      }
+      if (p.n_shared) s_exp[0] = (uint16_t)p.N;
       s_ctl[2] = 0;
       s_ctl[4] = number_taken;
     }
@@ -622,7 +630,8 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   int last = ticket + p.ahead - 1;                               // the latest ticket
   const int no_more = max(tiles, p.ahead * (int)gridDim.x);      // from here on tickets name no tile
   Place p0 = place_of(q0), p1 = place_of(q1), p2 = place_of(q2);
-  // the step `ahead` of tile q0's first one: in a taken tile, or past the last one of those in the down projection
+  // The step `ahead` of tile q0's first one.  Past the last taken tile a step of the one at work again (it is in L2; the number in
+  // flight stays): the down projection's weights would delay this workgroup's stores of h, which everyone waits for.
   auto load_ahead = [&](int slot, int ahead) __attribute__((always_inline)) {
     const int k = (ahead >= steps) + (ahead >= 2 * steps);
     int id = q2;
@@ -639,11 +648,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     if (id < tiles) {
       r = up_step(q, ahead - k * steps);
     } else {
-      // The waves that store h wait for their stores before these are counted, and so for whatever they loaded before: a step of
-      // the tile at work again instead (it is in L2), the down projection's later.
-      const int have = (q0 < tiles) + (q1 < tiles) + (q2 < tiles);  // they are taken in order
-      if (wave < kJoiners) r = up_step(p0, 0);
-      else r = down_step_at(ahead - have * steps);
+      r = up_step(p0, 0);
     }
     load_step(slot, r);
   };
@@ -652,7 +657,9 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
 #pragma unroll 1
   for (; loaded < D; ++loaded) load_ahead(loaded, loaded);
 
-  int buf = 0, mine = 0;
+  int buf = 0, mine = 0, taken = 0;
+  bool asked = (deep ? q2 : q1) < tiles && last < no_more;  // a ticket is on the way
+  if (asked && tid == 0) taken = take(next_tile);
   for (;;) {
     if (q0 >= tiles) {
       // Nothing left of what was taken.  Unless the latest ticket was past the end there may be tiles of workgroups that have
@@ -666,23 +673,18 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       if (q0 >= tiles) continue;
       p0 = place_of(q0);
       q1 = q2 = tiles;
+      asked = false;
       wait_vm<0>();  // start over with an empty ring
       slot = 0;
 #pragma unroll 1
       for (int s = 0; s < D; ++s) load_ahead(s, s);
     }
     const int a = (int)((uint32_t)q0 / (uint32_t)nt), tile = q0 - a * nt;
-    const bool ask = (deep ? q2 : q1) < tiles && last < no_more;
-    int taken = 0;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
     u32x4 sc = {0u, 0u, 0u, 0u};
 #pragma unroll
     for (int j = 0; j < F::kSteps; ++j) {
       if (j < D / 2 || j < steps) {
-        // The next tile's number is asked for at the start of this one and looked at D / 2 steps on (those are unconditional, so
-        // the compiler can count the loads behind it)
-        if (j == 0 && ask && tid == 0) taken = take(next_tile);
-        if (j == D / 2 - 1 && tid == 0) s_ctl[buf] = taken;
         wait_vm<F::kWaitUp>();
         const Step s = read_step(slot);
         load_ahead(slot, j + D);
@@ -713,7 +715,14 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       for (int r = 0; r < 4; ++r) acc[r] *= __uint_as_float(sc[r]);
     }
     s_red[buf][wave][lane] = acc;
+    if (asked && tid == 0) s_ctl[buf] = taken;
     lds_barrier();
+    if (asked) last = __builtin_amdgcn_readfirstlane(s_ctl[buf]);
+    const int next = asked && last < no_more ? tile_of(last) : tiles;
+    // The tile after the ones that are known by now is asked for here, where only the first wave will wait for the answer
+    // (at the end of the next tile), not the others' loads.
+    asked = next < tiles && last < no_more;
+    if (asked && tid == 0) taken = take(next_tile);
     if (wave < kJoiners) {  // the waves' sums in wave order, SwiGLU, h
       const int t = tid >> 3, c = tid & 7;
       const uint32_t at = red_at + buf * (kNW * 1024) + (t + 16 * (c >> 2)) * 16 + (c & 3) * 4;
@@ -732,8 +741,6 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
         __hip_atomic_store(reinterpret_cast<uint32_t*>(o), pair, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
       }
     }
-    if (ask) last = __builtin_amdgcn_readfirstlane(s_ctl[buf]);
-    const int next = ask && last < no_more ? tile_of(last) : tiles;
     q0 = q1;
     p0 = p1;
     q1 = deep ? q2 : next;
@@ -750,13 +757,20 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     // (A release fence would write the whole L2 back, one workgroup after the other: 13 us.)
     if (wave < kJoiners) wait_vm<0>();
     lds_barrier();
-    if (tid == 0) __hip_atomic_fetch_add(done, (uint32_t)mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    // The last one raises the flags, each for few enough that their reads do not hold it up (of one word, read by everyone,
+    // the news took 6 us).
+    if (wave == 0) {
+      uint32_t before = 0;
+      if (lane == 0) before = __hip_atomic_fetch_add(done, (uint32_t)mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if ((int)__builtin_amdgcn_readfirstlane(before) + mine == tiles && lane < kFlags)
+        __hip_atomic_store(p.counters + (3 + lane) * 32, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
   }
-  if (wave < kJoiners) {
-    wait_vm<0>();
+  // the down projection's first weights, while the others finish
+  wait_vm<0>();
+  slot = 0;
 #pragma unroll 1
-    for (int s = 0; s < D; ++s) load_step(slot + s < D ? slot + s : slot + s - D, down_step_at(s));
-  }
+  for (int s = 0; s < D; ++s) load_step(s, down_step_at(s));
 
   // ---- down ----
   for (int block = number; block < blocks; block += gridDim.x) {
@@ -764,8 +778,9 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     if (block == number) {
       if (tid == 0) {
         const uint64_t t0 = wall_clock64();
-        while (__hip_atomic_load(done, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) < (uint32_t)tiles) {
-          __builtin_amdgcn_s_sleep(8);
+        const uint32_t* const flag = p.counters + (3 + number % kFlags) * 32;
+        while (__hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) {
+          __builtin_amdgcn_s_sleep(4);
           if (wall_clock64() - t0 > kWaitTicks) {
             s_ctl[2] = 1;
             break;
@@ -786,13 +801,14 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int q = 0; q < P; ++q) total[r][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // This lane's h of a unit: its column's token's, or for a token that did not choose the expert one that did (not used).
-    const int col = WIDE ? lr : lr & 7, lower = WIDE || lr < 8 ? 0 : p.inter;
+    // This lane's h of a unit: its column's token's, zeros for a token that did not choose the expert.
+    const int col = WIDE ? lr : lr & 7;
+    const uint32_t lower = WIDE || lr < 8 ? 0 : p.inter * 2;
     u32x4 raw[F::kSets][2][F::kVec][P];  // of the next units
     auto load_h = [&](auto set_c, int a, int e, int sl) __attribute__((always_inline)) {
       constexpr int S = decltype(set_c)::value;
-      const int t = s_k[a][col] != 255 ? col : s_first[a];
-      const uint16_t* hr = p.h + (int64_t)(t * KS + s_k[a][t]) * 2 * p.inter + lower;
+      const int k = s_k[a][col];
+      const uint32_t hr = (uint32_t)(col * KS + k) * (uint32_t)p.inter * 4 + lower;
       const int k1 = block_of(sl, e, nb2) * F::kBlock;
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf) {
@@ -800,7 +816,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
 #pragma unroll
         for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
-          for (int q = 0; q < P; ++q) raw[S][hf][v][q] = *(const u32x4*)(hr + q * p.inter + k0 + v * 8);
+          for (int q = 0; q < P; ++q) raw[S][hf][v][q] = load16_if(p.h, k != 255 ? hr + (q * p.inter + k0 + v * 8) * 2 : kNoLoad);
       }
     };
     int a = 0, e = expert(0), sl = 0;  // the unit at work; (na, ne, ns) the one whose h is loaded next; (la, ls) D steps ahead
@@ -887,6 +903,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     };
 #pragma unroll 1
     for (int un = 0; un < units; un += F::kSets) {
+      __builtin_amdgcn_s_barrier();  // the waves keep together: the last ones alone would not load at the full rate
       unit(std::integral_constant<int, 0>(), true);
       unit(std::integral_constant<int, 1>(), un + 1 < units);
       if constexpr (F::kSets == 4) {
@@ -1012,6 +1029,9 @@ extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
     if (q->expert_counts) decode_zero_counts_kernel<<<1, 256, 0, stream>>>(q->expert_counts, q->n_experts);
     return check_launch("moe_decode");
   }
+  MOE_REQUIRE((int64_t)q->T * (q->top_k + q->n_shared) * q->inter * 4 < ((int64_t)1 << 32) - 256, MOE_ERR_SHAPE,
+              "moe_decode: T * (top_k + n_shared) * inter = %lld values of h exceed 4 GiB",
+              (long long)q->T * (q->top_k + q->n_shared) * q->inter);
   const DecodeWs L = decode_ws(q->T, q->d, q->inter, q->n_shared, q->top_k);
   MOE_REQUIRE(q->ws && q->ws_bytes >= L.total && aligned16(q->ws), MOE_ERR_WORKSPACE,
               "moe_decode: workspace %zu < %zu bytes (or NULL / unaligned)", q->ws_bytes, L.total);
