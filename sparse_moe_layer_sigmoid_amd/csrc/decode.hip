@@ -269,14 +269,14 @@ __device__ __forceinline__ void load4_to_lds(const uint8_t* base, uint32_t v, ui
 #endif
 }
 
-// 16 bytes at base + v; zeros, and no memory access, for a lane whose v is kNoLoad.
+// 16 bytes at base + v + off (off uniform); zeros, and no memory access, from `bytes` on, as for a lane whose v is kNoLoad.
 constexpr uint32_t kNoLoad = 0xffffffffu;
-__device__ __forceinline__ u32x4 load16_if(const void* base, uint32_t v) {
+__device__ __forceinline__ u32x4 load16_if(const void* base, uint32_t bytes, uint32_t v, uint32_t off) {
 #ifdef __HIP_DEVICE_COMPILE__
-  const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, 0xffffff00u, 0x00020000);
-  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, v, 0, 0));
+  const auto r = __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, bytes, 0x00020000);
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(r, v, off, 0));
 #else
-  return u32x4{v, 0u, 0u, 0u};
+  return u32x4{v, off, bytes, 0u};
 #endif
 }
 
@@ -294,8 +294,10 @@ struct Fmt {
   static constexpr int kWaitUp = kLoads * (kDepth - 1);
   // down: a unit is an expert's next 8 blocks of inner columns, one per wave, two steps; each brings kParts * 2 * kVec loads of h
   static constexpr int kParts = WIDE ? 2 : 1;
-  static constexpr int kSets = FMT == W_BF16 ? 4 : 2;   // units that h is loaded ahead
-  static constexpr int kWaitDown = kWaitUp + kDepth / 2 * kParts * 2 * kVec;
+  // Units that h is loaded ahead: as many as the ring holds, for loads end in order, and a wait for h of the unit before the
+  // last would be one for all weights but the last unit's (4 bits and two parts: one less, there are no more registers).
+  static constexpr int kSets = kDepth / 2 - (FMT == W_FP4 && WIDE ? 1 : 0);
+  static constexpr int kWaitDown = (kDepth / 2 - 1) * (2 * kLoads + kParts * 2 * kVec);
 };
 
 // 8 weights of a step's half block: dword pairs (bf16: the 16 bytes), its operand `s`.
@@ -581,6 +583,36 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     }
     return s;
   };
+  // The two steps of a unit, in an even slot and the next one.
+  auto read_pair = [&](int slot, Step& s, Step& t) __attribute__((always_inline)) {
+    const uint32_t at = ring_at + slot * SLOT + rd, at2 = at ^ 64, bt = at + SLOT, bt2 = at2 + SLOT;
+    if constexpr (FMT == W_FP4) {
+      static_assert(SLOT == 2176, "the offsets below");
+      const uint32_t sa = ring_at + slot * SLOT + lr * 8 + lg;
+      asm volatile(
+          "ds_read_b128 %0, %8\n\tds_read_b128 %1, %9\n\tds_read_u8 %2, %12 offset:2048\n\tds_read_u8 %3, %12 offset:2052\n\t"
+          "ds_read_b128 %4, %10\n\tds_read_b128 %5, %11\n\tds_read_u8 %6, %12 offset:4224\n\tds_read_u8 %7, %12 offset:4228\n\t"
+          "s_waitcnt lgkmcnt(0)"
+          : "=&v"(s.lo), "=&v"(s.hi), "=&v"(s.sc[0]), "=&v"(s.sc[1]), "=&v"(t.lo), "=&v"(t.hi), "=&v"(t.sc[0]), "=&v"(t.sc[1])
+          : "v"(at), "v"(at2), "v"(bt), "v"(bt2), "v"(sa)
+          : "memory");
+    } else if constexpr (F::kScaled) {
+      static_assert(SLOT == 2176, "the offsets below");
+      const uint32_t sa = ring_at + slot * SLOT + lg * 16;
+      asm volatile(
+          "ds_read_b128 %0, %6\n\tds_read_b128 %1, %7\n\tds_read_b128 %2, %10 offset:2048\n\t"
+          "ds_read_b128 %3, %8\n\tds_read_b128 %4, %9\n\tds_read_b128 %5, %10 offset:4224\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(s.lo), "=&v"(s.hi), "=&v"(s.sc), "=&v"(t.lo), "=&v"(t.hi), "=&v"(t.sc)
+          : "v"(at), "v"(at2), "v"(bt), "v"(bt2), "v"(sa)
+          : "memory");
+    } else {
+      asm volatile(
+          "ds_read_b128 %0, %4\n\tds_read_b128 %1, %5\n\tds_read_b128 %2, %6\n\tds_read_b128 %3, %7\n\ts_waitcnt lgkmcnt(0)"
+          : "=&v"(s.lo), "=&v"(s.hi), "=&v"(t.lo), "=&v"(t.hi)
+          : "v"(at), "v"(at2), "v"(bt), "v"(bt2)
+          : "memory");
+    }
+  };
   // scale of row lg * 4 + r of a step from block b (E4M3: of its block; int8: of the row)
   auto row_scale = [&](const Step& s, int b, int r) __attribute__((always_inline)) {
     if constexpr (FMT == W_E4M3_E8M0) {
@@ -801,104 +833,101 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     for (int r = 0; r < 2; ++r)
 #pragma unroll
       for (int q = 0; q < P; ++q) total[r][q] = f32x4{0.f, 0.f, 0.f, 0.f};
-    // This lane's h of a unit: its column's token's, zeros for a token that did not choose the expert.
+    // This lane's h of a unit: its column's token's, zeros for a token that did not choose the expert.  What a unit needs from
+    // tables in LDS is read an expert earlier: a chain of lookups would take longer than its products.
     const int col = WIDE ? lr : lr & 7;
-    const uint32_t lower = WIDE || lr < 8 ? 0 : p.inter * 2;
+    const uint32_t h_b = (uint32_t)(T * KS) * (uint32_t)p.inter * 4;
+    const uint32_t hl = (WIDE || lr < 8 ? 0 : p.inter * 2) + lg * (F::kBlock / 4);
+    auto after = [&](int a) __attribute__((always_inline)) { return a + 1 < A ? a + 1 : 0; };  // past the end the first units again
+    auto h_at = [&](int k) __attribute__((always_inline)) {
+      return k != 255 ? (uint32_t)(col * KS + k) * (uint32_t)p.inter * 4 + hl : kNoLoad;
+    };
     u32x4 raw[F::kSets][2][F::kVec][P];  // of the next units
-    auto load_h = [&](auto set_c, int a, int e, int sl) __attribute__((always_inline)) {
+    int raw_k[F::kSets], raw_b[F::kSets];
+    float raw_gate[F::kSets];
+    int na = 0, ns = 0, ne = expert(0), nk = s_k[0][col];  // the unit whose h is loaded next
+    uint32_t hv = h_at(nk);
+    int ne2 = s_exp[after(0)], nk2 = s_k[after(0)][col];   // of the expert behind it
+    auto load_next_h = [&](auto set_c) __attribute__((always_inline)) {
       constexpr int S = decltype(set_c)::value;
-      const int k = s_k[a][col];
-      const uint32_t hr = (uint32_t)(col * KS + k) * (uint32_t)p.inter * 4 + lower;
-      const int k1 = block_of(sl, e, nb2) * F::kBlock;
-#pragma unroll
-      for (int hf = 0; hf < 2; ++hf) {
-        const int k0 = k1 + (FMT == W_FP4 && k1 + F::kBlock / 2 >= p.inter ? 0 : hf * (F::kBlock / 2)) + lg * (F::kBlock / 8);
-#pragma unroll
-        for (int v = 0; v < F::kVec; ++v)
-#pragma unroll
-          for (int q = 0; q < P; ++q) raw[S][hf][v][q] = load16_if(p.h, k != 255 ? hr + (q * p.inter + k0 + v * 8) * 2 : kNoLoad);
-      }
-    };
-    int a = 0, e = expert(0), sl = 0;  // the unit at work; (na, ne, ns) the one whose h is loaded next; (la, ls) D steps ahead
-    int na = 0, ne = e, ns = 0;
-    int la = (D / 2) / slices, ls = (D / 2) - la * slices;
-    auto load_next_h = [&](auto set_c) __attribute__((always_inline)) {  // past the end the first units' again, not used
-      load_h(set_c, na, ne, ns);
-      if (++ns == slices) {
-        ns = 0;
-        na = na + 1 < A ? na + 1 : 0;
-        ne = expert(na);
-      }
-    };
-    load_next_h(std::integral_constant<int, 0>());
-    load_next_h(std::integral_constant<int, 1>());
-    if constexpr (F::kSets == 4) {
-      load_next_h(std::integral_constant<int, 2>());
-      load_next_h(std::integral_constant<int, 3>());
-    }
-    wait_vm<0>();  // the compiler then counts the next units' loads against the ring's instead of waiting for all
-    // (Every unit loads, also those that only round their number up: the waits count on it.)
-    auto unit = [&](auto set_c, bool live) __attribute__((always_inline)) {
-      constexpr int S = decltype(set_c)::value;
-      bf16x8_t h[2][F::kVec][P];
+      raw_k[S] = nk;
+      raw_gate[S] = s_gate[col * KS + min(nk, KS - 1)];
+      raw_b[S] = own_block(ns, ne);
+      const uint32_t off = block_of(ns, ne, nb2) * (F::kBlock * 2);
 #pragma unroll
       for (int hf = 0; hf < 2; ++hf)
 #pragma unroll
         for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
-          for (int q = 0; q < P; ++q) {
-            h[hf][v][q] = __builtin_bit_cast(bf16x8_t, raw[S][hf][v][q]);
-            asm volatile("" : "+v"(h[hf][v][q]));  // the wait for h is here, not among the loads below
-          }
-      const int kk = live ? s_k[a][col] : 255;
-      const float gate = kk != 255 ? s_gate[col * KS + kk] : 0.f;
-      const int b = own_block(sl, e);
-      if (++sl == slices) {
-        sl = 0;
-        a = a + 1 < A ? a + 1 : 0;
-        e = expert(a);
+          for (int q = 0; q < P; ++q) raw[S][hf][v][q] = load16_if(p.h, h_b, hv, off + q * p.inter * 2 + hf * F::kBlock + v * 16);
+      if (++ns == slices) {
+        ns = 0;
+        na = after(na);
+        ne = __builtin_amdgcn_readfirstlane(ne2);
+        nk = nk2;
+        hv = h_at(nk);
+        ne2 = s_exp[after(na)];
+        nk2 = s_k[after(na)][col];
       }
-      load_next_h(set_c);
-      const int le = expert(la < A ? la : 0);
-      const Place lp = down_place(le);
+    };
+    int la = D / 2 / slices, ls = D / 2 - la * slices;     // the unit whose weights are loaded next
+    la = la < A ? la : 0;
+    int le = expert(la), le2 = s_exp[after(la)];
+    Place lp = down_place(le);
+    load_next_h(std::integral_constant<int, 0>());
+    load_next_h(std::integral_constant<int, 1>());
+    if constexpr (F::kSets > 2) load_next_h(std::integral_constant<int, F::kSets == 2 ? 0 : 2>());
+    if constexpr (F::kSets > 3) load_next_h(std::integral_constant<int, F::kSets == 4 ? 3 : 0>());
+    wait_vm<0>();  // the compiler then counts the next units' loads against the ring's instead of waiting for all
+    // (Every unit loads, also those that only round their number up: the waits count on it.)
+    auto unit = [&](auto set_c, bool live) __attribute__((always_inline)) {
+      constexpr int S = decltype(set_c)::value;
+      const bool chosen = live && raw_k[S] != 255;
+      const float gate = raw_gate[S];
+      const int b = raw_b[S];
+      wait_vm<F::kWaitDown>();
+      Step st[2];
+      read_pair(slot, st[0], st[1]);
+      if (b < nb2) {
+        f32x4 part[2][P];
 #pragma unroll
-      for (int r = 0; r < 2; ++r) {
-        wait_vm<F::kWaitDown>();
-        const Step s = read_step(slot);
-        load_step(slot, down_step(lp, le, ls, r));
-        next_slot();
-        if (b < nb2) {
-          f32x4 part[P];
+        for (int r = 0; r < 2; ++r)
 #pragma unroll
-          for (int q = 0; q < P; ++q) part[q] = f32x4{0.f, 0.f, 0.f, 0.f};
-          const float s0 = __uint_as_float(s.sc[0] << 23), s1 = __uint_as_float(s.sc[1] << 23);
+          for (int q = 0; q < P; ++q) part[r][q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        auto products = [&](int hf) __attribute__((always_inline)) {
 #pragma unroll
-          for (int v = 0; v < F::kVec; ++v) {
-            const bf16x8_t w = operand<FMT>(s.lo, v, s0);
+          for (int v = 0; v < F::kVec; ++v)
 #pragma unroll
-            for (int q = 0; q < P; ++q) part[q] = mfma_bf16(w, h[0][v][q], part[q]);
-          }
-          if (FMT != W_FP4 || b * F::kBlock + F::kBlock / 2 < p.inter) {
+            for (int r = 0; r < 2; ++r) {
+              const bf16x8_t w = operand<FMT>(hf ? st[r].hi : st[r].lo, v, __uint_as_float(st[r].sc[hf] << 23));
 #pragma unroll
-            for (int v = 0; v < F::kVec; ++v) {
-              const bf16x8_t w = operand<FMT>(s.hi, v, s1);
-#pragma unroll
-              for (int q = 0; q < P; ++q) part[q] = mfma_bf16(w, h[1][v][q], part[q]);
+              for (int q = 0; q < P; ++q) part[r][q] = mfma_bf16(w, __builtin_bit_cast(bf16x8_t, raw[S][hf][v][q]), part[r][q]);
             }
-          }
+        };
+        products(0);
+        if (FMT != W_FP4 || b * F::kBlock + F::kBlock / 2 < p.inter) products(1);
+        if (chosen) {
 #pragma unroll
-          for (int q = 0; q < P; ++q)
+          for (int r = 0; r < 2; ++r)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-              float v = part[q][i];
-              if constexpr (FMT == W_E4M3 || FMT == W_E4M3_E8M0 || FMT == W_I8) v *= row_scale(s, b, i);
-              total[r][q][i] = kk != 255 ? fmaf(gate, v, total[r][q][i]) : total[r][q][i];
+              float g = gate;
+              if constexpr (FMT == W_E4M3 || FMT == W_E4M3_E8M0 || FMT == W_I8) g *= row_scale(st[r], b, i);
+#pragma unroll
+              for (int q = 0; q < P; ++q) total[r][q][i] = fmaf(g, part[r][q][i], total[r][q][i]);
             }
         }
       }
+      load_next_h(set_c);
+      load_step(slot, down_step(lp, le, ls, 0));
+      load_step(slot + 1, down_step(lp, le, ls, 1));
+      slot = slot + 2 == D ? 0 : slot + 2;
       if (++ls == slices) {
         ls = 0;
-        ++la;
+        la = after(la);
+        le = __builtin_amdgcn_readfirstlane(le2);
+        lp = down_place(le);
+        le2 = s_exp[after(la)];
       }
     };
 #pragma unroll 1
@@ -906,10 +935,8 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
       __builtin_amdgcn_s_barrier();  // the waves keep together: the last ones alone would not load at the full rate
       unit(std::integral_constant<int, 0>(), true);
       unit(std::integral_constant<int, 1>(), un + 1 < units);
-      if constexpr (F::kSets == 4) {
-        unit(std::integral_constant<int, 2>(), un + 2 < units);
-        unit(std::integral_constant<int, 3>(), un + 3 < units);
-      }
+      if constexpr (F::kSets > 2) unit(std::integral_constant<int, F::kSets == 2 ? 0 : 2>(), un + 2 < units);
+      if constexpr (F::kSets > 3) unit(std::integral_constant<int, F::kSets == 4 ? 3 : 0>(), un + 3 < units);
     }
 #pragma unroll
     for (int r = 0; r < 2; ++r)
