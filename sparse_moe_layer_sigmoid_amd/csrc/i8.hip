@@ -13,6 +13,7 @@
 #include "rows_common.h"
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x4_t __attribute__((ext_vector_type(4)));
 
 namespace moe {
 namespace {
@@ -342,8 +343,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
       }
     } else {
       uint16_t* o = reinterpret_cast<uint16_t*>(orow) + col;
-      const u32x2 b = {f32_to_bf16_rne(v[0]) | (f32_to_bf16_rne(v[1]) << 16),
-                       f32_to_bf16_rne(v[2]) | (f32_to_bf16_rne(v[3]) << 16)};
+      const u32x2 b = __builtin_bit_cast(u32x2, bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]});  // RNE
       if (left >= 4) {
         *reinterpret_cast<u32x2_u*>(o) = b;
       } else {
