@@ -155,33 +155,37 @@ struct Tile {
 // Both operands come by direct-to-LDS loads in steps of 128 bytes of K, a ring of STAGES steps that runs on over tile
 // boundaries; 16-byte chunks are XOR-swizzled by row so that operand reads meet distinct banks.  The tile's scales travel
 // the same way.  Tiles go by expert, column block, row block, a contiguous range to each XCD.
-template <int BM, int BN, int WGM, int WGN, int STAGES, bool SWIGLU>
+template <int BM, int BN, int WGM, int WGN, int KB, int STAGES, bool SWIGLU>
 __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN;
   constexpr int TM = WM / 16, TN = WN / 16;
-  constexpr int A_BYTES = BM * 128, STAGE = (BM + BN) * 128;
-  constexpr int A_PW = BM / 8 / NW, B_PW = BN / 8 / NW, L_STAGE = A_PW + B_PW;
+  constexpr int A_BYTES = BM * KB, STAGE = (BM + BN) * KB;
+  constexpr int RPL = 1024 / KB, CPR = KB / 16;  // rows of a load, 16-byte chunks of a row
+  constexpr int A_LD = BM / RPL, A_PW = (A_LD + NW - 1) / NW, B_PW = BN / RPL / NW, L_STAGE = A_PW + B_PW;
+  constexpr bool AHEAD = KB == 64;  // operands are read a step ahead
   constexpr int OC = SWIGLU ? BN / 2 : BN;
   constexpr int SC = BM + BN;  // scales of a tile
-  static_assert(A_PW * NW * 8 == BM && B_PW * NW * 8 == BN, "loads split evenly over the waves");
+  static_assert(A_LD * RPL == BM && B_PW * NW * RPL == BN, "loads split evenly over the waves");
   static_assert(SC / 64 <= NW, "one load of scales per wave at most");
+  static_assert(AHEAD ? STAGES == 4 : STAGES == 3, "the slots below");
+  // rows of a wave's i-th load of A; where they do not come out even, some loads are done by two waves
+  auto a_load = [](int wave, int i) { return A_PW * NW == A_LD ? wave * A_PW + i : (wave + i * NW) % A_LD; };
   static_assert(!SWIGLU || TN % 2 == 0, "a wave holds gate columns and their up columns");
   __shared__ __attribute__((aligned(1024))) uint8_t slot0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t slot1[STAGE];
-  __shared__ __attribute__((aligned(1024))) uint8_t slot2[STAGES > 2 ? STAGE : 16];
+  __shared__ __attribute__((aligned(1024))) uint8_t slot2[STAGE];
+  __shared__ __attribute__((aligned(1024))) uint8_t slot3[STAGES > 3 ? STAGE : 16];
   __shared__ float s_scale[STAGES][SC];  // row scales, then column scales; tiles of one step are STAGES - 1 ahead
-  __shared__ int s_tstart[kMaxRowGroups + 1];
+  __shared__ int s_tstart[kMaxRowGroups + 1], s_off[kMaxRowGroups + 1];
+  __shared__ int s_rows[2][NW][A_PW + 1][64];  // row numbers of a tile: of the wave's loads and of its scales (two in turn)
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WGN, wn = wave - wm * WGN;
   const int G = p.rows.n_groups;
   const int32_t* offs = p.rows.offs;
   const int limit = __builtin_amdgcn_readfirstlane(rows_end(p.rows));
-  auto offset = [&](int g) __attribute__((always_inline)) {
-    return min(__builtin_amdgcn_readfirstlane(offs[__builtin_amdgcn_readfirstlane(g)]), limit);
-  };
-
+  for (int g = tid; g <= G; g += NW * 64) s_off[g] = min(offs[g], limit);
   if (wave == 0) {  // tiles before each group
     const int per = (G + 63) >> 6, g0 = min(G, lane * per), g1 = min(G, g0 + per);
     auto tiles = [&](int g) { return (max(min(offs[g + 1], limit) - min(offs[g], limit), 0) + BM - 1) / BM * p.n_tiles; };
@@ -206,43 +210,60 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   const int xcd = blockIdx.x % n_xcd, seat = blockIdx.x / n_xcd, seats = gridDim.x / n_xcd;
   const int t_begin = (int)((int64_t)total * xcd / n_xcd), t_end = (int)((int64_t)total * (xcd + 1) / n_xcd);
   const int n_my = t_end - t_begin > seat ? (t_end - t_begin - seat + seats - 1) / seats : 0;
-  const int ksteps = (p.K + 127) / 128;
-  const int last_chunks = (p.K - (ksteps - 1) * 128) / 16;  // chunks of the last step
+  // AHEAD: steps come in fours, one per slot, so that a tile ends in the last slot; steps past K are zeros
+  const int ksteps = AHEAD ? (p.K + 4 * KB - 1) / (4 * KB) * 4 : (p.K + KB - 1) / KB;
+  const int k_chunks = p.K / 16;
   const int total_steps = n_my * ksteps;
   if (total_steps == 0) return;
 
-  auto tile_of = [&](int q) __attribute__((always_inline)) {
+  // Tile q of this workgroup, found from the group of an earlier one: tiles rise with q.  A lane each looks at the next 64 groups.
+  auto tile_of = [&](int q, int from) __attribute__((always_inline)) {
     const int L = t_begin + seat + q * seats;
-    int lo = 0, hi = G;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (s_tstart[mid] <= L) lo = mid;
-      else hi = mid;
-    }
     Tile t;
-    t.g = __builtin_amdgcn_readfirstlane(lo);
-    const int m0 = offset(t.g), m1 = offset(t.g + 1), local = L - s_tstart[t.g], blocks = (m1 - m0 + BM - 1) / BM;
-    t.nt = __builtin_amdgcn_readfirstlane(local / blocks);
-    t.row0 = m0 + __builtin_amdgcn_readfirstlane(local - t.nt * blocks) * BM;
+    t.g = from;
+    for (;;) {
+      const int n = __popcll(__ballot(s_tstart[min(t.g + 1 + lane, G)] <= L && t.g + 1 + lane <= G));
+      t.g += n;
+      if (n < 64) break;
+    }
+    t.g = __builtin_amdgcn_readfirstlane(t.g);
+    const int m0 = __builtin_amdgcn_readfirstlane(s_off[t.g]), m1 = __builtin_amdgcn_readfirstlane(s_off[t.g + 1]);
+    const int local = L - __builtin_amdgcn_readfirstlane(s_tstart[t.g]), blocks = (m1 - m0 + BM - 1) / BM;
+    t.nt = (int)((uint32_t)local / (uint32_t)blocks);
+    t.row0 = m0 + (local - t.nt * blocks) * BM;
     t.nrows = min(BM, m1 - t.row0);
     return t;
   };
 
   // ---- loads ----
-  const int cch = lane & 7, lrow = lane >> 3;
+  // A row's chunks are permuted by the row, so that neither 8 nor 16 lanes reading one chunk of rows that follow each other
+  // share a bank.
+  auto swizzle = [](int row) { return KB == 128 ? row & 7 : ((row >> 1) & 3) ^ ((row >> 3) & 1); };
+  const int lrow = lane / CPR;
   const uint8_t* a_ptr[A_PW];
   const uint8_t* b_ptr[B_PW];
   const float* sc_ptr = p.a_scale;  // this lane's scale of the tile
-  int a_nxt[A_PW], sc_nxt = 0;
-  const int chunk_of_row = cch ^ lrow;  // rows of a load are a multiple of 8 plus lrow
-  auto fetch_rows = [&](const Tile& t) __attribute__((always_inline)) {  // used one tile later
+  const int chunk_of_row = (lane % CPR) ^ swizzle(lrow);  // rows of a load are a multiple of 8 or 16 plus lrow
+  // Row numbers of a tile go to LDS a tile ahead, each lane's own: in registers they would have to be waited for with everything
+  // else in flight.  They are older than the loads of the step that they were asked in, so the next step's wait covers them.
+  auto tile_row = [&](const Tile& t, int i) __attribute__((always_inline)) {  // i = A_PW: of the scales
+    const int r = i < A_PW ? RPL * a_load(wave, i) + lrow : min(wave * 64, BM - 64) + lane;
+    return t.row0 + min(r, t.nrows - 1);
+  };
+  auto fetch_rows = [&](const Tile& t, int q) __attribute__((always_inline)) {
+    if (!p.a_rows) return;
 #pragma unroll
-    for (int i = 0; i < A_PW; ++i) {
-      const int r = t.row0 + min(8 * (wave * A_PW + i) + lrow, t.nrows - 1);
-      a_nxt[i] = p.a_rows ? p.a_rows[r] : r;
+    for (int i = 0; i <= A_PW; ++i)
+      __builtin_amdgcn_global_load_lds((glb_void*)(p.a_rows + tile_row(t, i)), (lds_void*)s_rows[q & 1][wave][i], 4, 0, 0);
+  };
+  const uint32_t rows_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int*)&s_rows[0][wave][0][lane];
+  auto row_number = [&](const Tile& t, int q, int i) __attribute__((always_inline)) {
+    int r = tile_row(t, i);
+    if (p.a_rows) {  // (the compiler would wait for all loads into LDS)
+      const uint32_t at = rows_at + (q & 1) * (uint32_t)sizeof(s_rows[0]) + i * 256;
+      asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(r) : "v"(at) : "memory");
     }
-    const int r = t.row0 + min(min(wave * 64, BM - 64) + lane, t.nrows - 1);
-    sc_nxt = p.a_rows ? p.a_rows[r] : r;
+    return r;
   };
   auto weight_row = [&](int nt, int rr) __attribute__((always_inline)) {
     if constexpr (SWIGLU) {
@@ -252,41 +273,46 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
       return min(nt * BN + rr, p.N - 1);
     }
   };
-  auto set_tile = [&](const Tile& t) __attribute__((always_inline)) {
+  auto set_tile = [&](const Tile& t, int q) __attribute__((always_inline)) {
     const int64_t first = (int64_t)(p.first_group + t.g) * p.N;
 #pragma unroll
-    for (int i = 0; i < A_PW; ++i) a_ptr[i] = p.a + (int64_t)a_nxt[i] * p.lda + chunk_of_row * 16;
+    for (int i = 0; i < A_PW; ++i) a_ptr[i] = p.a + (int64_t)row_number(t, q, i) * p.lda + chunk_of_row * 16;
 #pragma unroll
     for (int i = 0; i < B_PW; ++i)
-      b_ptr[i] = p.w + (first + weight_row(t.nt, 8 * (wave * B_PW + i) + lrow)) * p.K + chunk_of_row * 16;
-    sc_ptr = wave < BM / 64 ? p.a_scale + sc_nxt
+      b_ptr[i] = p.w + (first + weight_row(t.nt, RPL * (wave * B_PW + i) + lrow)) * p.K + chunk_of_row * 16;
+    sc_ptr = wave < BM / 64 ? p.a_scale + row_number(t, q, A_PW)
                             : p.w_scale + first + weight_row(t.nt, min((wave - BM / 64) * 64, BN - 64) + lane);
   };
+  Tile ct = tile_of(0, 0), lt = ct;  // the tile at work; the next one to load
   int lq = -1, dma_kt = 0, ld_kt = ksteps;  // tile and step of the batch being issued
   bool dma_ragged = false, dma_first = false;
-  auto issue_prep = [&](int js) __attribute__((always_inline)) {
+  auto issue_prep = [&](int js, bool may_switch = true) __attribute__((always_inline)) {
     dma_first = false;
     if (js < total_steps) {  // past the end the last step is loaded again: the number in flight stays
-      if (++ld_kt >= ksteps) {
+      ++ld_kt;
+      if (may_switch && ld_kt >= ksteps) {
         ld_kt = 0;
         ++lq;
-        set_tile(tile_of(lq));
-        if (lq + 1 < n_my) fetch_rows(tile_of(lq + 1));
+        set_tile(lt, lq);
+        if (lq + 1 < n_my) {
+          lt = tile_of(lq + 1, lt.g);
+          fetch_rows(lt, lq + 1);
+        }
         dma_first = true;
       }
     }
     dma_kt = ld_kt;
-    dma_ragged = ld_kt == ksteps - 1 && last_chunks < 8 && chunk_of_row >= last_chunks;
+    dma_ragged = ld_kt * CPR + chunk_of_row >= k_chunks;
   };
   auto issue_one = [&](auto slot_c, int k) __attribute__((always_inline)) {
     constexpr int SL = decltype(slot_c)::value;
-    uint8_t* st = SL == 0 ? slot0 : (SL == 1 ? slot1 : slot2);
+    uint8_t* st = SL == 0 ? slot0 : (SL == 1 ? slot1 : (SL == 2 ? slot2 : slot3));
     if (k < A_PW) {  // chunks past the row: zeros against whatever the weights hold there
-      const uint8_t* src = dma_ragged ? kZeros : a_ptr[k] + dma_kt * 128;
-      __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)(st + (wave * A_PW + k) * 1024), 16, 0, 0);
+      const uint8_t* src = dma_ragged ? kZeros : a_ptr[k] + dma_kt * KB;
+      __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)(st + a_load(wave, k) * 1024), 16, 0, 0);
     } else {
       const int i = k - A_PW;
-      const uint8_t* src = b_ptr[i] + (dma_ragged ? -chunk_of_row * 16 : dma_kt * 128);
+      const uint8_t* src = b_ptr[i] + (dma_ragged ? -chunk_of_row * 16 : dma_kt * KB);
       __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)(st + A_BYTES + (wave * B_PW + i) * 1024), 16, 0, 0);
     }
   };
@@ -310,9 +336,12 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
         __builtin_amdgcn_sched_barrier(0);
       }
   };
-  fetch_rows(tile_of(0));
+  fetch_rows(ct, 0);
+  I8_WAIT_VM(0);
   issue(std::integral_constant<int, 0>(), 0);
-  if constexpr (STAGES > 2) issue(std::integral_constant<int, 1>(), 1);
+  if (ksteps == 1) I8_WAIT_VM(0);  // the second tile's rows
+  issue(std::integral_constant<int, 1>(), 1);
+  if constexpr (AHEAD) issue(std::integral_constant<int, 2>(), 2);
 
   // ---- products: weights first, so a lane's four results are four columns of one token row ----
   const int lr = lane & 15, lg = lane >> 4;
@@ -321,105 +350,161 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-  const int sw_lo = (lg ^ (lr & 7)) << 4, sw_hi = sw_lo ^ 64;
-  const int fa = (wm * WM + lr) * 128;
-  const int fb = (SWIGLU ? wn * (WN / 2) + lr : wn * WN + lr) * 128;
-  const int base_row = offset(0), tail_row = offset(p.rows.tail_first);
+  // a wave's blocks of 16 rows are every WGM-th one, so that a short tile's rows are shared out too
+  const int sw_lo = (lg ^ swizzle(lr)) << 4, sw_hi = sw_lo ^ 64;
+  const int fa = (wm * 16 + lr) * KB;
+  const int fb = (SWIGLU ? wn * (WN / 2) + lr : wn * WN + lr) * KB;
+  const int base_row = __builtin_amdgcn_readfirstlane(s_off[0]);
+  const int tail_row = __builtin_amdgcn_readfirstlane(s_off[p.rows.tail_first]);
   int c_q = 0, c_kt = 0;
-  Tile ct = tile_of(0);
 
-  auto store4 = [&](const Tile& t, int m, int col, const float v[4]) __attribute__((always_inline)) {
-    const int left = p.out_cols - col;
-    if (m >= t.nrows || left <= 0) return;
-    const bool tail = t.g >= p.rows.tail_first;
-    const int64_t row = t.row0 + m;
-    uint8_t* orow = tail ? p.out_tail + (row - tail_row) * p.ldo_tail_b : p.out + (row - base_row) * p.ldo_b;
-    if (tail || p.out_dtype == ROW_F32) {
-      float* o = reinterpret_cast<float*>(orow) + col;
-      if (left >= 4) {
-        *reinterpret_cast<f32x4_u*>(o) = f32x4{v[0], v[1], v[2], v[3]};
-      } else {
-        for (int e = 0; e < left; ++e) o[e] = v[e];
-      }
-    } else {
-      uint16_t* o = reinterpret_cast<uint16_t*>(orow) + col;
-      const u32x2 b = __builtin_bit_cast(u32x2, bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]});  // RNE
-      if (left >= 4) {
-        *reinterpret_cast<u32x2_u*>(o) = b;
-      } else {
-        for (int e = 0; e < left; ++e) o[e] = (uint16_t)(b[e / 2] >> (16 * (e & 1)));
-      }
-    }
-  };
-  auto epilogue = [&](const Tile& t, const float* sc) __attribute__((always_inline)) {
+  // A tile's results, as F32 or bf16; FULL: none of its columns is past the last one.
+  auto store_tile = [&](const Tile& t, const float* sc, auto f32_c, auto full_c) __attribute__((always_inline)) {
+    constexpr bool F32 = decltype(f32_c)::value, FULL = decltype(full_c)::value;
     constexpr int TO = SWIGLU ? TN / 2 : TN;
+    const bool tail = t.g >= p.rows.tail_first;
+    uint8_t* base = tail ? p.out_tail + (int64_t)(t.row0 - tail_row) * p.ldo_tail_b : p.out + (int64_t)(t.row0 - base_row) * p.ldo_b;
+    const int64_t ldo_b = tail ? p.ldo_tail_b : p.ldo_b;
+    const int c0 = (SWIGLU ? wn * (WN / 2) : wn * WN) + lg * 4;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-      const int m = wm * WM + i * 16 + lr;
+      const int m = (i * WGM + wm) * 16 + lr;
+      if (m >= t.nrows) continue;
       const float as = sc[m];
+      uint8_t* o = base + m * ldo_b + (int64_t)(t.nt * OC + c0) * (F32 ? 4 : 2);
 #pragma unroll
       for (int j = 0; j < TO; ++j) {
-        const int c = (SWIGLU ? wn * (WN / 2) : wn * WN) + j * 16 + lg * 4;
-        const f32x4 ws = *(const f32x4*)(sc + BM + c);
-        float v[4];
+        const f32x4 ws = *(const f32x4*)(sc + BM + c0 + j * 16);
+        f32x4 v;
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][r] * (as * ws[r]);
         if constexpr (SWIGLU) {
-          const f32x4 us = *(const f32x4*)(sc + BM + BN / 2 + c);
+          const f32x4 us = *(const f32x4*)(sc + BM + BN / 2 + c0 + j * 16);
 #pragma unroll
           for (int r = 0; r < 4; ++r) v[r] = silu(v[r]) * ((float)acc[i][j + TO][r] * (as * us[r]));
         }
-        store4(t, m, t.nt * OC + c, v);
+        const u32x2 b = __builtin_bit_cast(u32x2, bf16x4_t{(__bf16)v[0], (__bf16)v[1], (__bf16)v[2], (__bf16)v[3]});  // RNE
+        const int left = FULL ? 4 : p.out_cols - (t.nt * OC + c0 + j * 16);
+        if (left >= 4) {
+          if constexpr (F32) *reinterpret_cast<f32x4_u*>(o + j * 64) = v;
+          else *reinterpret_cast<u32x2_u*>(o + j * 32) = b;
+        } else {
+#pragma unroll
+          for (int e = 0; e < 3; ++e) {
+            if (e >= left) break;
+            if constexpr (F32) reinterpret_cast<float*>(o + j * 64)[e] = v[e];
+            else reinterpret_cast<uint16_t*>(o + j * 32)[e] = (uint16_t)(b[e / 2] >> (16 * (e & 1)));
+          }
+        }
       }
+    }
+  };
+  auto epilogue = [&]() __attribute__((always_inline)) {
+    const float* sc = s_scale[c_q % STAGES];
+    const bool f32 = ct.g >= p.rows.tail_first || p.out_dtype == ROW_F32, full = (ct.nt + 1) * OC <= p.out_cols;
+    if (full) {
+      if (f32) store_tile(ct, sc, std::true_type(), std::true_type());
+      else store_tile(ct, sc, std::false_type(), std::true_type());
+    } else {
+      if (f32) store_tile(ct, sc, std::true_type(), std::false_type());
+      else store_tile(ct, sc, std::false_type(), std::false_type());
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
+    c_kt = 0;
+    if (++c_q < n_my) ct = tile_of(c_q, ct.g);
   };
 
-  auto step = [&](auto slot_c, int j) __attribute__((always_inline)) {
-    constexpr int SL = decltype(slot_c)::value;
-    constexpr auto next = std::integral_constant<int, (SL + STAGES - 1) % STAGES>();
-    const uint8_t* As = SL == 0 ? slot0 : (SL == 1 ? slot1 : slot2);
-    const uint8_t* Bs = As + A_BYTES;
-    I8_WAIT_VM(L_STAGE * (STAGES - 2));
-    I8_BARRIER();
-    issue_prep(j + STAGES - 1);
+  auto slot_of = [&](auto slot_c) __attribute__((always_inline)) {
+    constexpr int SL = decltype(slot_c)::value % STAGES;
+    return (const uint8_t*)(SL == 0 ? slot0 : (SL == 1 ? slot1 : (SL == 2 ? slot2 : slot3)));
+  };
+  auto b_row = [](int jj) { return SWIGLU && jj >= TN / 2 ? BN / 2 + (jj - TN / 2) * 16 : jj * 16; };
+  if constexpr (!AHEAD) {
+    auto step = [&](auto slot_c, int j) __attribute__((always_inline)) {
+      constexpr auto next = std::integral_constant<int, (decltype(slot_c)::value + STAGES - 1) % STAGES>();
+      const uint8_t *As = slot_of(slot_c), *Bs = As + A_BYTES;
+      I8_WAIT_VM(L_STAGE * (STAGES - 2));
+      I8_BARRIER();
+      issue_prep(j + STAGES - 1);
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-      i32x4 af[TM], bf[TN];
+      for (int h = 0; h < 2; ++h) {
+        i32x4 af[TM], bf[TN];
 #pragma unroll
-      for (int i = 0; i < TM; ++i) af[i] = *(const i32x4*)(As + fa + (h ? sw_hi : sw_lo) + i * 2048);
+        for (int i = 0; i < TM; ++i) af[i] = *(const i32x4*)(As + fa + (h ? sw_hi : sw_lo) + i * (WGM * 16 * KB));
 #pragma unroll
-      for (int jj = 0; jj < TN; ++jj) {
-        const int ro = (SWIGLU && jj >= TN / 2 ? BN / 2 + (jj - TN / 2) * 16 : jj * 16) * 128;
-        bf[jj] = *(const i32x4*)(Bs + fb + (h ? sw_hi : sw_lo) + ro);
+        for (int jj = 0; jj < TN; ++jj) bf[jj] = *(const i32x4*)(Bs + fb + (h ? sw_hi : sw_lo) + b_row(jj) * KB);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int jj = 0; jj < TN; ++jj) {
+            acc[i][jj] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[jj], af[i], acc[i][jj], 0, 0, 0);
+            dma_in(next, (h * TM + i) * TN + jj, 2 * TM * TN);
+          }
       }
+      issue_scales();
+      if (++c_kt == ksteps) epilogue();
+    };
+    int j = 0;
+    for (; j + 3 <= total_steps; j += 3) {
+      step(std::integral_constant<int, 0>(), j);
+      step(std::integral_constant<int, 1>(), j + 1);
+      step(std::integral_constant<int, 2>(), j + 2);
+    }
+    if (j < total_steps) step(std::integral_constant<int, 0>(), j);
+    if (j + 1 < total_steps) step(std::integral_constant<int, 1>(), j + 1);
+  } else {
+    // Step j's products run on operands in registers and read step j + 1's, each right behind the last product that needs its
+    // registers.  So slot j + 1 has to be complete at barrier j, and slot j - 1 may be loaded anew from there on: its last readers
+    // have used what they read.
+    constexpr int AW = TM / 2;  // rows' operands in registers
+    static_assert(TM % 2 == 0 && TM >= TN, "the window turns over twice a step, and the weights' operands fit between");
+    i32x4 af[AW], bf[2][TN];
+    auto read_a = [&](const uint8_t* As, int i) __attribute__((always_inline)) {
+      af[i % AW] = *(const i32x4*)(As + fa + sw_lo + i * (WGM * 16 * KB));
+    };
+    auto read_b = [&](const uint8_t* As, int set, int jj) __attribute__((always_inline)) {
+      bf[set][jj] = *(const i32x4*)(As + A_BYTES + fb + sw_lo + b_row(jj) * KB);
+    };
+    I8_WAIT_VM(2 * L_STAGE);
+    I8_BARRIER();
 #pragma unroll
-      for (int i = 0; i < TM; ++i)
+    for (int jj = 0; jj < TN; ++jj) read_b(slot0, 0, jj);
+#pragma unroll
+    for (int i = 0; i < AW; ++i) read_a(slot0, i);
+    auto step = [&](auto slot_c, int j) __attribute__((always_inline)) {
+      constexpr int SL = decltype(slot_c)::value, set = SL & 1;
+      constexpr auto next = std::integral_constant<int, (SL + 3) % 4>();
+      const uint8_t *Cs = slot_of(slot_c), *Ns = slot_of(std::integral_constant<int, SL + 1>());
+      I8_WAIT_VM(L_STAGE);
+      __builtin_amdgcn_s_barrier();
+      asm volatile("" ::: "memory");
+      issue_prep(j + 3, SL == 1);  // a tile begins in slot 0
+#pragma unroll
+      for (int i = 0; i < TM; ++i) {
 #pragma unroll
         for (int jj = 0; jj < TN; ++jj) {
-          acc[i][jj] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[jj], af[i], acc[i][jj], 0, 0, 0);
-          dma_in(next, (h * TM + i) * TN + jj, 2 * TM * TN);
+          acc[i][jj] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[set][jj], af[i % AW], acc[i][jj], 0, 0, 0);
+          dma_in(next, i * TN + jj, TM * TN);
         }
+        __builtin_amdgcn_sched_barrier(0);
+        if (i < TN) read_b(Ns, set ^ 1, i);
+        if (i + AW < TM) read_a(Cs, i + AW);
+        else read_a(Ns, i + AW - TM);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      issue_scales();
+    };
+    for (int j = 0; j < total_steps; j += 4) {
+      step(std::integral_constant<int, 0>(), j);
+      step(std::integral_constant<int, 1>(), j + 1);
+      step(std::integral_constant<int, 2>(), j + 2);
+      step(std::integral_constant<int, 3>(), j + 3);
+      if ((c_kt += 4) == ksteps) epilogue();
     }
-    issue_scales();
-    if (++c_kt == ksteps) {
-      epilogue(ct, s_scale[c_q % STAGES]);
-      c_kt = 0;
-      if (++c_q < n_my) ct = tile_of(c_q);
-    }
-  };
-  int j = 0;
-  for (; j + STAGES <= total_steps; j += STAGES) {
-    step(std::integral_constant<int, 0>(), j);
-    step(std::integral_constant<int, 1>(), j + 1);
-    if constexpr (STAGES > 2) step(std::integral_constant<int, 2 % STAGES>(), j + 2);
   }
-  if (j < total_steps) step(std::integral_constant<int, 0>(), j);
-  if constexpr (STAGES > 2)
-    if (j + 1 < total_steps) step(std::integral_constant<int, 1>(), j + 1);
   I8_WAIT_VM(0);  // the repeated loads land before the workgroup's LDS is given away
 }
 
@@ -431,7 +516,7 @@ int compute_units() {
   return 256;
 }
 
-template <int BM, int BN, int WGM, int WGN, int STAGES, bool SWIGLU>
+template <int BM, int BN, int WGM, int WGN, int KB, int STAGES, bool SWIGLU>
 void launch_gemm(I8Args a, int64_t m_total, hipStream_t stream) {
   constexpr int OC = SWIGLU ? BN / 2 : BN;
   a.n_tiles = (a.out_cols + OC - 1) / OC;
@@ -439,13 +524,14 @@ void launch_gemm(I8Args a, int64_t m_total, hipStream_t stream) {
   const int64_t tiles = (full < m_total ? full : m_total) * a.n_tiles;
   const int cus = compute_units();
   const int64_t grid = tiles < cus ? (tiles + 7) / 8 * 8 : cus;
-  i8_gemm_kernel<BM, BN, WGM, WGN, STAGES, SWIGLU><<<(unsigned)grid, WGM * WGN * 64, 0, stream>>>(a);
+  i8_gemm_kernel<BM, BN, WGM, WGN, KB, STAGES, SWIGLU><<<(unsigned)grid, WGM * WGN * 64, 0, stream>>>(a);
 }
 
+constexpr int BIGM = 192;
 template <bool SWIGLU>
 void dispatch_gemm(const I8Args& a, int64_t m_total, hipStream_t stream) {
-  if (m_total / a.rows.n_groups < 64) launch_gemm<64, 256, 1, 8, 3, SWIGLU>(a, m_total, stream);
-  else launch_gemm<128, 256, 2, 4, 3, SWIGLU>(a, m_total, stream);
+  if (m_total / a.rows.n_groups < 64) launch_gemm<64, 256, 1, 8, 128, 3, SWIGLU>(a, m_total, stream);
+  else launch_gemm<BIGM, 256, 2, 4, 64, 4, SWIGLU>(a, m_total, stream);
 }
 
 template <int DT, int L, int CH>
