@@ -155,30 +155,24 @@ struct Tile {
 // Both operands come by direct-to-LDS loads in steps of 128 bytes of K, a ring of STAGES steps that runs on over tile
 // boundaries; 16-byte chunks are XOR-swizzled by row so that operand reads meet distinct banks.  The tile's scales travel
 // the same way.  Tiles go by expert, column block, row block, a contiguous range to each XCD.
-template <int BM, int BN, int WGM, int WGN, int KB, int STAGES, bool SWIGLU>
+template <int BM, int BN, int WGM, int WGN, bool SWIGLU>
 __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   constexpr int NW = WGM * WGN;
   constexpr int WM = BM / WGM, WN = BN / WGN;
   constexpr int TM = WM / 16, TN = WN / 16;
-  constexpr int A_BYTES = BM * KB, STAGE = (BM + BN) * KB;
-  constexpr int RPL = 1024 / KB, CPR = KB / 16;  // rows of a load, 16-byte chunks of a row
-  constexpr int A_LD = BM / RPL, A_PW = (A_LD + NW - 1) / NW, B_PW = BN / RPL / NW, L_STAGE = A_PW + B_PW;
-  constexpr bool AHEAD = KB == 64;  // operands are read a step ahead
+  constexpr int STAGES = 3, A_BYTES = BM * 128, STAGE = (BM + BN) * 128;
+  constexpr int A_PW = BM / 8 / NW, B_PW = BN / 8 / NW, L_STAGE = A_PW + B_PW;
   constexpr int OC = SWIGLU ? BN / 2 : BN;
   constexpr int SC = BM + BN;  // scales of a tile
-  static_assert(A_LD * RPL == BM && B_PW * NW * RPL == BN, "loads split evenly over the waves");
+  static_assert(A_PW * NW * 8 == BM && B_PW * NW * 8 == BN, "loads split evenly over the waves");
   static_assert(SC / 64 <= NW, "one load of scales per wave at most");
-  static_assert(AHEAD ? STAGES == 4 : STAGES == 3, "the slots below");
-  // rows of a wave's i-th load of A; where they do not come out even, some loads are done by two waves
-  auto a_load = [](int wave, int i) { return A_PW * NW == A_LD ? wave * A_PW + i : (wave + i * NW) % A_LD; };
   static_assert(!SWIGLU || TN % 2 == 0, "a wave holds gate columns and their up columns");
   __shared__ __attribute__((aligned(1024))) uint8_t slot0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t slot1[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t slot2[STAGE];
-  __shared__ __attribute__((aligned(1024))) uint8_t slot3[STAGES > 3 ? STAGE : 16];
-  __shared__ float s_scale[STAGES][SC];  // row scales, then column scales; tiles of one step are STAGES - 1 ahead
+  __shared__ float s_scale[STAGES][SC];  // row scales, then column scales; loads are up to two tiles ahead
   __shared__ int s_tstart[kMaxRowGroups + 1], s_off[kMaxRowGroups + 1];
-  __shared__ int s_rows[2][NW][A_PW + 1][64];  // row numbers of a tile: of the wave's loads and of its scales (two in turn)
+  __shared__ int s_rows[NW][64], s_srows[BM / 64][64];  // row numbers of the next tile: of a wave's loads, and of scales
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WGN, wn = wave - wm * WGN;
@@ -210,8 +204,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   const int xcd = blockIdx.x % n_xcd, seat = blockIdx.x / n_xcd, seats = gridDim.x / n_xcd;
   const int t_begin = (int)((int64_t)total * xcd / n_xcd), t_end = (int)((int64_t)total * (xcd + 1) / n_xcd);
   const int n_my = t_end - t_begin > seat ? (t_end - t_begin - seat + seats - 1) / seats : 0;
-  // AHEAD: steps come in fours, one per slot, so that a tile ends in the last slot; steps past K are zeros
-  const int ksteps = AHEAD ? (p.K + 4 * KB - 1) / (4 * KB) * 4 : (p.K + KB - 1) / KB;
+  const int ksteps = max((p.K + 127) / 128, 2);  // steps past K are zeros
   const int k_chunks = p.K / 16;
   const int total_steps = n_my * ksteps;
   if (total_steps == 0) return;
@@ -236,83 +229,76 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   };
 
   // ---- loads ----
-  // A row's chunks are permuted by the row, so that neither 8 nor 16 lanes reading one chunk of rows that follow each other
-  // share a bank.
-  auto swizzle = [](int row) { return KB == 128 ? row & 7 : ((row >> 1) & 3) ^ ((row >> 3) & 1); };
-  const int lrow = lane / CPR;
+  const int cch = lane & 7, lrow = lane >> 3;
   const uint8_t* a_ptr[A_PW];
   const uint8_t* b_ptr[B_PW];
   const float* sc_ptr = p.a_scale;  // this lane's scale of the tile
-  const int chunk_of_row = (lane % CPR) ^ swizzle(lrow);  // rows of a load are a multiple of 8 or 16 plus lrow
-  // Row numbers of a tile go to LDS a tile ahead, each lane's own: in registers they would have to be waited for with everything
-  // else in flight.  They are older than the loads of the step that they were asked in, so the next step's wait covers them.
-  auto tile_row = [&](const Tile& t, int i) __attribute__((always_inline)) {  // i = A_PW: of the scales
-    const int r = i < A_PW ? RPL * a_load(wave, i) + lrow : min(wave * 64, BM - 64) + lane;
-    return t.row0 + min(r, t.nrows - 1);
-  };
-  auto fetch_rows = [&](const Tile& t, int q) __attribute__((always_inline)) {
+  const int chunk_of_row = cch ^ lrow;  // rows of a load are a multiple of 8 plus lrow
+  // Row numbers of a tile go to LDS a tile ahead: in registers they would have to be waited for with everything else in flight.
+  // They are older than the loads of the step that they were asked in, so the next step's wait covers them.
+  auto tile_row = [&](const Tile& t, int r) __attribute__((always_inline)) { return t.row0 + min(r, t.nrows - 1); };
+  auto fetch_rows = [&](const Tile& t) __attribute__((always_inline)) {
     if (!p.a_rows) return;
-#pragma unroll
-    for (int i = 0; i <= A_PW; ++i)
-      __builtin_amdgcn_global_load_lds((glb_void*)(p.a_rows + tile_row(t, i)), (lds_void*)s_rows[q & 1][wave][i], 4, 0, 0);
+    __builtin_amdgcn_global_load_lds((glb_void*)(p.a_rows + tile_row(t, wave * A_PW * 8 + min(lane, A_PW * 8 - 1))),
+                                     (lds_void*)s_rows[wave], 4, 0, 0);
+    if (wave < BM / 64)
+      __builtin_amdgcn_global_load_lds((glb_void*)(p.a_rows + tile_row(t, wave * 64 + lane)), (lds_void*)s_srows[wave], 4, 0, 0);
   };
-  const uint32_t rows_at = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) int*)&s_rows[0][wave][0][lane];
-  auto row_number = [&](const Tile& t, int q, int i) __attribute__((always_inline)) {
-    int r = tile_row(t, i);
-    if (p.a_rows) {  // (the compiler would wait for all loads into LDS)
-      const uint32_t at = rows_at + (q & 1) * (uint32_t)sizeof(s_rows[0]) + i * 256;
-      asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(r) : "v"(at) : "memory");
+  auto row_number = [&](const Tile& t, int r, const int* at) __attribute__((always_inline)) {
+    int v = tile_row(t, r);
+    if (p.a_rows) {  // (of a plain read the compiler would wait for all loads into LDS)
+      const uint32_t a = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) const int*)at;
+      asm volatile("ds_read_b32 %0, %1\n\ts_waitcnt lgkmcnt(0)" : "=v"(v) : "v"(a) : "memory");
     }
-    return r;
+    return v;
   };
   auto weight_row = [&](int nt, int rr) __attribute__((always_inline)) {
     if constexpr (SWIGLU) {
-      const int c = min(nt * (BN / 2) + (rr & (BN / 2 - 1)), p.N / 2 - 1);
+      const int c = min(nt * (BN / 2) + (rr < BN / 2 ? rr : rr - BN / 2), p.N / 2 - 1);
       return rr < BN / 2 ? c : p.N / 2 + c;
     } else {
       return min(nt * BN + rr, p.N - 1);
     }
   };
-  auto set_tile = [&](const Tile& t, int q) __attribute__((always_inline)) {
+  auto set_tile = [&](const Tile& t) __attribute__((always_inline)) {
     const int64_t first = (int64_t)(p.first_group + t.g) * p.N;
 #pragma unroll
-    for (int i = 0; i < A_PW; ++i) a_ptr[i] = p.a + (int64_t)row_number(t, q, i) * p.lda + chunk_of_row * 16;
+    for (int i = 0; i < A_PW; ++i) a_ptr[i] = p.a + (int64_t)row_number(t, 8 * (wave * A_PW + i) + lrow, &s_rows[wave][i * 8 + lrow]) * p.lda + chunk_of_row * 16;
 #pragma unroll
     for (int i = 0; i < B_PW; ++i)
-      b_ptr[i] = p.w + (first + weight_row(t.nt, RPL * (wave * B_PW + i) + lrow)) * p.K + chunk_of_row * 16;
-    sc_ptr = wave < BM / 64 ? p.a_scale + row_number(t, q, A_PW)
-                            : p.w_scale + first + weight_row(t.nt, min((wave - BM / 64) * 64, BN - 64) + lane);
+      b_ptr[i] = p.w + (first + weight_row(t.nt, 8 * (wave * B_PW + i) + lrow)) * p.K + chunk_of_row * 16;
+    if (wave < BM / 64) sc_ptr = p.a_scale + row_number(t, wave * 64 + lane, &s_srows[min(wave, BM / 64 - 1)][lane]);
+    else sc_ptr = p.w_scale + first + weight_row(t.nt, min((wave - BM / 64) * 64, BN - 64) + lane);
   };
   Tile ct = tile_of(0, 0), lt = ct;  // the tile at work; the next one to load
   int lq = -1, dma_kt = 0, ld_kt = ksteps;  // tile and step of the batch being issued
   bool dma_ragged = false, dma_first = false;
-  auto issue_prep = [&](int js, bool may_switch = true) __attribute__((always_inline)) {
+  auto issue_prep = [&](int js) __attribute__((always_inline)) {
     dma_first = false;
     if (js < total_steps) {  // past the end the last step is loaded again: the number in flight stays
-      ++ld_kt;
-      if (may_switch && ld_kt >= ksteps) {
+      if (++ld_kt >= ksteps) {
         ld_kt = 0;
         ++lq;
-        set_tile(lt, lq);
+        set_tile(lt);
         if (lq + 1 < n_my) {
           lt = tile_of(lq + 1, lt.g);
-          fetch_rows(lt, lq + 1);
+          fetch_rows(lt);
         }
         dma_first = true;
       }
     }
     dma_kt = ld_kt;
-    dma_ragged = ld_kt * CPR + chunk_of_row >= k_chunks;
+    dma_ragged = ld_kt * 8 + chunk_of_row >= k_chunks;
   };
   auto issue_one = [&](auto slot_c, int k) __attribute__((always_inline)) {
     constexpr int SL = decltype(slot_c)::value;
-    uint8_t* st = SL == 0 ? slot0 : (SL == 1 ? slot1 : (SL == 2 ? slot2 : slot3));
+    uint8_t* st = SL == 0 ? slot0 : (SL == 1 ? slot1 : slot2);
     if (k < A_PW) {  // chunks past the row: zeros against whatever the weights hold there
-      const uint8_t* src = dma_ragged ? kZeros : a_ptr[k] + dma_kt * KB;
-      __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)(st + a_load(wave, k) * 1024), 16, 0, 0);
+      const uint8_t* src = dma_ragged ? kZeros : a_ptr[k] + dma_kt * 128;
+      __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)(st + (wave * A_PW + k) * 1024), 16, 0, 0);
     } else {
       const int i = k - A_PW;
-      const uint8_t* src = b_ptr[i] + (dma_ragged ? -chunk_of_row * 16 : dma_kt * KB);
+      const uint8_t* src = b_ptr[i] + (dma_ragged ? -chunk_of_row * 16 : dma_kt * 128);
       __builtin_amdgcn_global_load_lds((glb_void*)src, (lds_void*)(st + A_BYTES + (wave * B_PW + i) * 1024), 16, 0, 0);
     }
   };
@@ -326,22 +312,12 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
     for (int k = 0; k < L_STAGE; ++k) issue_one(slot_c, k);
     issue_scales();
   };
-  // a step's loads are spread over its products
-  auto dma_in = [&](auto slot_c, int t, int n) __attribute__((always_inline)) {
-#pragma unroll
-    for (int k = 0; k < L_STAGE; ++k)
-      if (t == (k + 1) * n / (L_STAGE + 1)) {
-        __builtin_amdgcn_sched_barrier(0);
-        issue_one(slot_c, k);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-  };
-  fetch_rows(ct, 0);
+  fetch_rows(ct);
   I8_WAIT_VM(0);
   issue(std::integral_constant<int, 0>(), 0);
-  if (ksteps == 1) I8_WAIT_VM(0);  // the second tile's rows
   issue(std::integral_constant<int, 1>(), 1);
-  if constexpr (AHEAD) issue(std::integral_constant<int, 2>(), 2);
+  if (ksteps == 2) I8_WAIT_VM(0);  // the second tile's rows
+  issue(std::integral_constant<int, 2>(), 2);
 
   // ---- products: weights first, so a lane's four results are four columns of one token row ----
   const int lr = lane & 15, lg = lane >> 4;
@@ -351,9 +327,9 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
   // a wave's blocks of 16 rows are every WGM-th one, so that a short tile's rows are shared out too
-  const int sw_lo = (lg ^ swizzle(lr)) << 4, sw_hi = sw_lo ^ 64;
-  const int fa = (wm * 16 + lr) * KB;
-  const int fb = (SWIGLU ? wn * (WN / 2) + lr : wn * WN + lr) * KB;
+  const int sw_lo = (lg ^ (lr & 7)) << 4, sw_hi = sw_lo ^ 64;
+  const int fa = (wm * 16 + lr) * 128;
+  const int fb = (SWIGLU ? wn * (WN / 2) + lr : wn * WN + lr) * 128;
   const int base_row = __builtin_amdgcn_readfirstlane(s_off[0]);
   const int tail_row = __builtin_amdgcn_readfirstlane(s_off[p.rows.tail_first]);
   int c_q = 0, c_kt = 0;
@@ -417,94 +393,63 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
     if (++c_q < n_my) ct = tile_of(c_q, ct.g);
   };
 
-  auto slot_of = [&](auto slot_c) __attribute__((always_inline)) {
-    constexpr int SL = decltype(slot_c)::value % STAGES;
-    return (const uint8_t*)(SL == 0 ? slot0 : (SL == 1 ? slot1 : (SL == 2 ? slot2 : slot3)));
-  };
-  auto b_row = [](int jj) { return SWIGLU && jj >= TN / 2 ? BN / 2 + (jj - TN / 2) * 16 : jj * 16; };
-  if constexpr (!AHEAD) {
-    auto step = [&](auto slot_c, int j) __attribute__((always_inline)) {
-      constexpr auto next = std::integral_constant<int, (decltype(slot_c)::value + STAGES - 1) % STAGES>();
-      const uint8_t *As = slot_of(slot_c), *Bs = As + A_BYTES;
-      I8_WAIT_VM(L_STAGE * (STAGES - 2));
-      I8_BARRIER();
-      issue_prep(j + STAGES - 1);
-#pragma unroll
-      for (int h = 0; h < 2; ++h) {
-        i32x4 af[TM], bf[TN];
-#pragma unroll
-        for (int i = 0; i < TM; ++i) af[i] = *(const i32x4*)(As + fa + (h ? sw_hi : sw_lo) + i * (WGM * 16 * KB));
-#pragma unroll
-        for (int jj = 0; jj < TN; ++jj) bf[jj] = *(const i32x4*)(Bs + fb + (h ? sw_hi : sw_lo) + b_row(jj) * KB);
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-#pragma unroll
-          for (int jj = 0; jj < TN; ++jj) {
-            acc[i][jj] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[jj], af[i], acc[i][jj], 0, 0, 0);
-            dma_in(next, (h * TM + i) * TN + jj, 2 * TM * TN);
-          }
-      }
-      issue_scales();
-      if (++c_kt == ksteps) epilogue();
-    };
-    int j = 0;
-    for (; j + 3 <= total_steps; j += 3) {
-      step(std::integral_constant<int, 0>(), j);
-      step(std::integral_constant<int, 1>(), j + 1);
-      step(std::integral_constant<int, 2>(), j + 2);
+  // A step is two halves of 64 bytes of K.  A half's products run on operands in registers, and read the next half's between
+  // them.  So at the barrier between step j's halves every wave has read all of slot j, and step j + 3 may be loaded into it; step
+  // j + 1 has to be complete there.
+  i32x4 af[2][TM], bf[2][TN];
+  auto read_one = [&](auto slot_c, int half, int k) __attribute__((always_inline)) {
+    constexpr int SL = decltype(slot_c)::value;
+    const uint8_t* st = SL == 0 ? slot0 : (SL == 1 ? slot1 : slot2);
+    const int sw = half ? sw_hi : sw_lo;
+    if (k < TN) {
+      const int row = SWIGLU && k >= TN / 2 ? BN / 2 + (k - TN / 2) * 16 : k * 16;
+      bf[half][k] = *(const i32x4*)(st + A_BYTES + fb + sw + row * 128);
+    } else {
+      af[half][k - TN] = *(const i32x4*)(st + fa + sw + (k - TN) * (WGM * 16 * 128));
     }
-    if (j < total_steps) step(std::integral_constant<int, 0>(), j);
-    if (j + 1 < total_steps) step(std::integral_constant<int, 1>(), j + 1);
-  } else {
-    // Step j's products run on operands in registers and read step j + 1's, each right behind the last product that needs its
-    // registers.  So slot j + 1 has to be complete at barrier j, and slot j - 1 may be loaded anew from there on: its last readers
-    // have used what they read.
-    constexpr int AW = TM / 2;  // rows' operands in registers
-    static_assert(TM % 2 == 0 && TM >= TN, "the window turns over twice a step, and the weights' operands fit between");
-    i32x4 af[AW], bf[2][TN];
-    auto read_a = [&](const uint8_t* As, int i) __attribute__((always_inline)) {
-      af[i % AW] = *(const i32x4*)(As + fa + sw_lo + i * (WGM * 16 * KB));
-    };
-    auto read_b = [&](const uint8_t* As, int set, int jj) __attribute__((always_inline)) {
-      bf[set][jj] = *(const i32x4*)(As + A_BYTES + fb + sw_lo + b_row(jj) * KB);
-    };
-    I8_WAIT_VM(2 * L_STAGE);
-    I8_BARRIER();
+  };
+  auto half_step = [&](int half, auto read_c, auto load_c, bool load) __attribute__((always_inline)) {
+    constexpr int n = TM * TN, reads = TM + TN;
 #pragma unroll
-    for (int jj = 0; jj < TN; ++jj) read_b(slot0, 0, jj);
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-    for (int i = 0; i < AW; ++i) read_a(slot0, i);
-    auto step = [&](auto slot_c, int j) __attribute__((always_inline)) {
-      constexpr int SL = decltype(slot_c)::value, set = SL & 1;
-      constexpr auto next = std::integral_constant<int, (SL + 3) % 4>();
-      const uint8_t *Cs = slot_of(slot_c), *Ns = slot_of(std::integral_constant<int, SL + 1>());
-      I8_WAIT_VM(L_STAGE);
-      __builtin_amdgcn_s_barrier();
-      asm volatile("" ::: "memory");
-      issue_prep(j + 3, SL == 1);  // a tile begins in slot 0
+      for (int jj = 0; jj < TN; ++jj) {
+        const int t = i * TN + jj;
+        acc[i][jj] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[half][jj], af[half][i], acc[i][jj], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int i = 0; i < TM; ++i) {
+        for (int k = 0; k < reads; ++k)
+          if (t == k * n / reads) read_one(read_c, half ^ 1, k);
+        if (load) {
 #pragma unroll
-        for (int jj = 0; jj < TN; ++jj) {
-          acc[i][jj] = __builtin_amdgcn_mfma_i32_16x16x64_i8(bf[set][jj], af[i % AW], acc[i][jj], 0, 0, 0);
-          dma_in(next, i * TN + jj, TM * TN);
+          for (int k = 0; k < L_STAGE; ++k)
+            if (t == k * n / L_STAGE) issue_one(load_c, k);
         }
         __builtin_amdgcn_sched_barrier(0);
-        if (i < TN) read_b(Ns, set ^ 1, i);
-        if (i + AW < TM) read_a(Cs, i + AW);
-        else read_a(Ns, i + AW - TM);
-        __builtin_amdgcn_sched_barrier(0);
       }
-      issue_scales();
-    };
-    for (int j = 0; j < total_steps; j += 4) {
-      step(std::integral_constant<int, 0>(), j);
-      step(std::integral_constant<int, 1>(), j + 1);
-      step(std::integral_constant<int, 2>(), j + 2);
-      step(std::integral_constant<int, 3>(), j + 3);
-      if ((c_kt += 4) == ksteps) epilogue();
-    }
+  };
+  I8_WAIT_VM(2 * L_STAGE);
+  I8_BARRIER();
+#pragma unroll
+  for (int k = 0; k < TM + TN; ++k) read_one(std::integral_constant<int, 0>(), 0, k);
+  auto step = [&](auto slot_c, int j) __attribute__((always_inline)) {
+    constexpr auto next = std::integral_constant<int, (decltype(slot_c)::value + 1) % 3>();
+    half_step(0, slot_c, slot_c, false);
+    I8_WAIT_VM(L_STAGE);
+    I8_BARRIER();
+    issue_prep(j + 3);
+    half_step(1, next, slot_c, true);
+    issue_scales();
+    if (++c_kt == ksteps) epilogue();
+  };
+  int j = 0;
+  for (; j + 3 <= total_steps; j += 3) {
+    step(std::integral_constant<int, 0>(), j);
+    step(std::integral_constant<int, 1>(), j + 1);
+    step(std::integral_constant<int, 2>(), j + 2);
   }
+  if (j < total_steps) step(std::integral_constant<int, 0>(), j);
+  if (j + 1 < total_steps) step(std::integral_constant<int, 1>(), j + 1);
   I8_WAIT_VM(0);  // the repeated loads land before the workgroup's LDS is given away
 }
 
@@ -516,7 +461,7 @@ int compute_units() {
   return 256;
 }
 
-template <int BM, int BN, int WGM, int WGN, int KB, int STAGES, bool SWIGLU>
+template <int BM, int BN, int WGM, int WGN, bool SWIGLU>
 void launch_gemm(I8Args a, int64_t m_total, hipStream_t stream) {
   constexpr int OC = SWIGLU ? BN / 2 : BN;
   a.n_tiles = (a.out_cols + OC - 1) / OC;
@@ -524,14 +469,13 @@ void launch_gemm(I8Args a, int64_t m_total, hipStream_t stream) {
   const int64_t tiles = (full < m_total ? full : m_total) * a.n_tiles;
   const int cus = compute_units();
   const int64_t grid = tiles < cus ? (tiles + 7) / 8 * 8 : cus;
-  i8_gemm_kernel<BM, BN, WGM, WGN, KB, STAGES, SWIGLU><<<(unsigned)grid, WGM * WGN * 64, 0, stream>>>(a);
+  i8_gemm_kernel<BM, BN, WGM, WGN, SWIGLU><<<(unsigned)grid, WGM * WGN * 64, 0, stream>>>(a);
 }
 
-constexpr int BIGM = 192;
 template <bool SWIGLU>
 void dispatch_gemm(const I8Args& a, int64_t m_total, hipStream_t stream) {
-  if (m_total / a.rows.n_groups < 64) launch_gemm<64, 256, 1, 8, 128, 3, SWIGLU>(a, m_total, stream);
-  else launch_gemm<BIGM, 256, 2, 4, 64, 4, SWIGLU>(a, m_total, stream);
+  if (m_total / a.rows.n_groups < 64) launch_gemm<64, 256, 1, 8, SWIGLU>(a, m_total, stream);
+  else launch_gemm<192, 192, 4, 2, SWIGLU>(a, m_total, stream);
 }
 
 template <int DT, int L, int CH>
