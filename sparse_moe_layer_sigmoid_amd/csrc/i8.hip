@@ -151,10 +151,17 @@ struct Tile {
   int g, nt, row0, nrows;
 };
 
-// Persistent workgroups of WGM x WGN waves walk tiles of BM rows x BN weight rows (SwiGLU: BN/2 gate rows and their up rows).
-// Both operands come by direct-to-LDS loads in steps of 128 bytes of K, a ring of STAGES steps that runs on over tile
-// boundaries; 16-byte chunks are XOR-swizzled by row so that operand reads meet distinct banks.  The tile's scales travel
-// the same way.  Tiles go by expert, column block, row block, a contiguous range to each XCD.
+// Persistent workgroups of WGM x WGN waves, one to a CU, walk tiles of BM rows x BN weight rows (SwiGLU: BN/2 gate rows and
+// their up rows).  Both operands come by direct-to-LDS loads in steps of 128 bytes of K (a cache line: steps of 64 ask L2 for
+// twice as many), three steps in flight in a ring that runs on over tile boundaries; 16-byte chunks are XOR-swizzled by row so
+// that operand reads meet distinct banks.  A tile's scales travel the same way, its row numbers a tile ahead.  Tiles go by
+// expert, column block, row block, a contiguous range to each XCD.
+//
+// Few rows to an expert: the weights' bytes bound it (256 tokens' down projection: 3.4 GB at 5.9 TB/s, a copy has 5.1).  Many:
+// 192 x 192 is the most products per loaded byte of which LDS holds three steps.  16384 tokens' down projection (147456 rows,
+// 7168 x 2048) takes 2.62 ms, 1.65 Pop/s; the library's largest 8-bit product on this card has 2.14.  The clock is down to
+// 1.8 GHz, and what is left is rows of short tiles (an eighth) and, at a tile's end, its stores, which the next step's wait for
+// loads includes.
 template <int BM, int BN, int WGM, int WGN, bool SWIGLU>
 __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   constexpr int NW = WGM * WGN;
@@ -474,7 +481,10 @@ void launch_gemm(I8Args a, int64_t m_total, hipStream_t stream) {
 
 template <bool SWIGLU>
 void dispatch_gemm(const I8Args& a, int64_t m_total, hipStream_t stream) {
-  if (m_total / a.rows.n_groups < 64) launch_gemm<64, 256, 1, 8, SWIGLU>(a, m_total, stream);
+  // By rows per expert: the low tile wastes fewer products where the weights' bytes are the time, the high one reads them fewer
+  // times.  257 experts, 2000 tokens of 8 (70 rows): gate/up 1.62 against 1.69 ms, down 0.90 against 0.93; 3000 (105 rows):
+  // 1.93 against 1.76 ms and 1.01 against 0.98.
+  if (m_total / a.rows.n_groups < 80) launch_gemm<64, 256, 1, 8, SWIGLU>(a, m_total, stream);
   else launch_gemm<192, 192, 4, 2, SWIGLU>(a, m_total, stream);
 }
 
