@@ -677,8 +677,10 @@ typedef struct {
 } moe_decode_desc;
 /* Limits: those of moe_route on T, d, n_experts and the groups; d <= 8192; d and inter multiples of 64 (bf16)
  * or 128 (E4M3, int8, 4 bits; E4M3 with power-of-two scales: d and inter multiples of 512); w13, w2,
- * w_router 16-byte aligned, the rest aligned to its elements (4-bit scale codes to 4 bytes); ldx >= d, and without a norm a multiple of 8 with x
- * 16-byte aligned; ldo >= d; one expert's w13 or w2 < 2 GiB.  T = 0 writes zero counts only.  Rows of out past T are not touched.
+ * w_router 16-byte aligned, the rest aligned to its elements (4-bit scale codes to 4 bytes); ldx >= d, and
+ * without a norm a multiple of 8 with x 16-byte aligned; ldo >= d; one expert's w13 or w2 < 2 GiB, h
+ * (T * (top_k + n_shared) * inter * 4 bytes) < 4 GiB.  T = 0 writes zero counts only.  Rows of out past T are
+ * not touched.
  * The second launch's workgroups wait for each other's parts of h; none waits for a workgroup that has not
  * started, and the wait ends by itself after seconds (NaN rows) should the workspace be overwritten meanwhile. */
 size_t moe_decode_workspace_size(int T, int d, int inter, int n_experts, int n_shared, int top_k);

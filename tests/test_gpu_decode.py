@@ -135,6 +135,16 @@ def test_decode(fmt, case):
     check(Case(fmt, T, d, inter, E, K, groups, norm, shared))
 
 
+@pytest.mark.parametrize("fmt", ["bf16", "i8", "w4"])
+def test_decode_every_expert(fmt):
+    """16 tokens that choose all 256 experts among them: more units than any token has."""
+    c = Case(fmt, 16, 256, 256, 256, 32)
+    out = check(c)
+    assert len(torch.unique(c.run()[1])) > 200
+    Case(fmt, 2, 512, 384, 8, 2).run()                      # another shape between, on the same stream
+    assert torch.equal(c.run()[0], out)
+
+
 @pytest.mark.parametrize("T,d,inter", [(1, 64, 64), (5, 256, 64), (3, 192, 320), (2, 8128, 64), (16, 64, 2112)])
 def test_decode_bf16_blocks_of_64(T, d, inter):
     check(Case("bf16", T, d, inter, 8, 2))

@@ -167,6 +167,25 @@ def test_i8_gemm(lens, N, K, swiglu):
     assert torch.equal(out2, out[:rows])
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("K", [16, 256, 288, 400])
+def test_i8_gemm_tall_groups(K, swiglu):
+    """Hundreds of rows to an expert and more tiles than workgroups: tiles that follow each other after two steps and more, in
+    other experts and column blocks, and a last short one."""
+    say(f"i8_gemm tall groups K={K} swiglu={swiglu}")
+    lens, N = [6000, 90, 0, 3000, 193], 1606
+    offs = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    rows = int(offs[-1])
+    a, as_, w, ws = _operands(760 + K, len(lens), N, K, 700)
+    gather = np.random.default_rng(761).integers(0, 700, rows).astype(np.int32)
+    want, tol = _reference(a, as_, w, ws, offs, gather, swiglu)
+    out = torch.full((rows + 1, want.shape[1]), 9.0, dtype=torch.float32, device=DEV)
+    M().moe_i8_gemm(a, as_, w, ws, torch.from_numpy(offs).to(DEV), 0, len(lens), rows, out,
+                    a_rows=torch.from_numpy(gather).to(DEV), swiglu=swiglu)
+    got = np64(out)
+    assert np.all(np.abs(got[:rows] - want) <= tol) and np.all(got[rows:] == 9.0)
+
+
 def test_i8_gemm_group_range_and_tail():
     """A sub-range of the groups (rows relative to its first), and the last groups' f32 rows in their own output."""
     lens, N, K = [4, 0, 21, 3, 140, 6], 80, 192

@@ -93,6 +93,7 @@ def _decode(**kw):
     (dict(d=96, ldx=96), 2), (dict(d=0), 2), (dict(d=8256, ldx=8256, ldo=8256), 2), (dict(inter=32), 2), (dict(inter=0), 2),
     (dict(w_dtype=3, d=320, ldx=320, ldo=320, w13_scale=16, w2_scale=16), 2), (dict(w_dtype=4, inter=192, w13_scale=16, w2_scale=16), 2),
     (dict(w_dtype=2, scale_fmt=1, w13_scale=16, w2_scale=16), 2), (dict(inter=1 << 17, d=8192, ldx=8192, ldo=8192), 2),
+    (dict(T=16, n_experts=64, top_k=32, d=64, ldx=64, ldo=64, inter=1 << 21), 2),    # h of 4.1 GiB
     (dict(ldx=255), 4), (dict(ldx=260), 4), (dict(x=8), 4), (dict(ldo=255), 4), (dict(out=17), 4), (dict(out=18, out_dtype=1), 4),
     (dict(w_router=8), 4), (dict(w13=8), 4), (dict(w2=8), 4), (dict(bias=18), 4), (dict(w_dtype=4, w13_scale=18, w2_scale=16), 4),
     (dict(norm=0, x=17), 4), (dict(norm=0, norm_weight=18), 4), (dict(topk_idx=18), 4), (dict(ws=None), 5), (dict(ws_bytes=100), 5),
