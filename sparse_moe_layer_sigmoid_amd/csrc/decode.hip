@@ -23,7 +23,7 @@
 // step, XOR-swizzled so that operand reads meet distinct banks.  The ring runs on across tiles and experts: with 8 steps to a
 // wave the chip has 32 MB on the way, what 6.5 TB/s need at 5 us.
 //
-// The hand-over: gate/up tiles are taken by ticket, the first two (three) of a workgroup at once, and every ticket is in the
+// The hand-over: gate/up tiles are taken from counters, the first two (three) of a workgroup at once, and every tile is in the
 // hands of a running workgroup before any workgroup waits for h.  None waits for one that has not started: calls may overlap on
 // the device.  h goes through to memory by its stores; the workgroup that finishes the last tile raises flags.
 //
@@ -54,8 +54,9 @@ constexpr int kRowThreads = 1024;
 constexpr uint64_t kWaitTicks = 500000000ull;  // 5 s of the 100 MHz clock: bound of the wait for h
 
 // Workspace: counters, affinities, normalised rows, h.
-constexpr int kFlags = 16;  // "h is complete", for a workgroup in 16 each
-constexpr int kCounters = 3 + kFlags;  // the next tile, finished tiles, started workgroups, flags: 128 bytes apart
+constexpr int kFlags = 16;    // "h is complete", for a workgroup in 16 each
+constexpr int kClasses = 16;  // counters of the workgroups that have started, for a workgroup in 16 each
+constexpr int kCounters = 2 + kFlags + kClasses;  // the next tile, finished tiles, flags, classes: 128 bytes apart
 constexpr size_t kCounterBytes = (kCounters * 128 + 255) & ~255;
 constexpr size_t kScoreBytes = (size_t)kMaxT * 256 * sizeof(double);
 struct DecodeWs {
@@ -326,7 +327,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   __shared__ float s_gate[kMaxT * (kMaxTopK + 1)];  // gate of slot t (K + n_shared) + k
   __shared__ __attribute__((aligned(16))) uint8_t s_k[kMaxActive][kMaxT];  // k of a token's active expert, 255: not chosen
   __shared__ uint16_t s_exp[kMaxActive];            // active experts, the shared one first
-  __shared__ int s_ctl[5];                          // tiles taken (two in turn), gave up waiting, first tile, number
+  __shared__ int s_ctl[4];                          // tiles taken (two in turn), gave up waiting, batch or tile taken
   // of the selection, before the sums need the space
   uint32_t* const s_mask = reinterpret_cast<uint32_t*>(&s_red[0][0][0]);
   int32_t* const s_idx = reinterpret_cast<int32_t*>(&s_red[0][4][0]);
@@ -339,13 +340,19 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   const int T = p.T, K = p.K, KS = p.K + p.n_shared;
   uint32_t* const next_tile = p.counters;
   uint32_t* const done = p.counters + 32;
+  uint32_t* const flags = p.counters + 2 * 32;
+  uint32_t* const classes = flags + kFlags * 32;
+  const int grid = (int)gridDim.x;
   uint32_t in_vgpr = 0;  // of a uniform address the compiler combines the wave's additions, and waits for the sum at once
   asm volatile("" : "+v"(in_vgpr));
   auto take = [&](uint32_t* counter) __attribute__((always_inline)) {
     return (int)__hip_atomic_fetch_add(counter + in_vgpr, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
   };
-  if (tid == 0)
-    s_ctl[3] = (int)__hip_atomic_fetch_add(next_tile + in_vgpr, (uint32_t)p.ahead, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  // The first p.ahead * grid tiles come in batches of p.ahead, a grid apart, so that everyone starts with the shared expert's.
+  // The n-th workgroup of a class to start takes the class's n-th batch: one counter for all would keep the last ones waiting
+  // for 5 us.
+  auto claim = [&](int c) __attribute__((always_inline)) { return take(classes + c * 32) * kClasses + c; };
+  if (tid == 0) s_ctl[3] = claim((int)blockIdx.x % kClasses);
 
   // ---- what is needed of the weights' layout ----
   const int nt = p.inter / 8;                                // tiles of an expert
@@ -447,17 +454,8 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   for (int i = tid; i < 256; i += kNW * 64) s_mask[i] = 0;
   for (int i = tid; i < kMaxActive * kMaxT / 4; i += kNW * 64) reinterpret_cast<uint32_t*>(&s_k[0][0])[i] = 0xffffffffu;
   __syncthreads();
-  // Tickets name tiles: the first p.ahead * gridDim.x tickets are taken p.ahead at a time (one workgroup's tiles at work and ahead)
-  // and name tiles a gridDim.x apart, so that everyone starts with the shared expert's.
-  auto tile_of = [&](int ticket) __attribute__((always_inline)) {
-    if (ticket >= p.ahead * (int)gridDim.x) return ticket;
-    const int v = (int)((uint32_t)ticket / (uint32_t)p.ahead);
-    return (ticket - v * p.ahead) * (int)gridDim.x + v;
-  };
-  const int ticket = __builtin_amdgcn_readfirstlane(s_ctl[3]);
-  const int first = tile_of(ticket);
-  int number_taken = 0;  // looked at after the selection
-  if (tid == 0) number_taken = take(p.counters + 64);
+  const int batch = __builtin_amdgcn_readfirstlane(s_ctl[3]);
+  const int first = batch < grid ? batch : INT32_MAX;  // the class's batches may be in others' hands by now
 
   // the shared expert's tiles come first: their weights are on the way while the routed ones are being chosen
   int loaded = 0;
@@ -497,9 +495,8 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     if (tid == 0) {
       if (p.n_shared) s_exp[0] = (uint16_t)p.N;
       s_ctl[2] = 0;
-      s_ctl[4] = number_taken;
     }
-    if (ticket == 0) {  // the first workgroup reports the routing
+    if (blockIdx.x == 0) {  // one workgroup reports the routing
       if (p.counts && tid < p.N) p.counts[tid] = __popc(mask);
       for (int i = tid; i < T * K; i += kNW * 64) {
         if (p.topk_idx) p.topk_idx[i] = s_idx[i];
@@ -513,11 +510,10 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   for (int i = tid; i < T * K; i += kNW * 64) s_k[s_pos[s_idx[i]]][i / K] = (uint8_t)(i % K);
   if (p.n_shared && tid < T) s_k[0][tid] = (uint8_t)K;
 
-  const int number = __builtin_amdgcn_readfirstlane(s_ctl[4]);  // of this workgroup, in the order they started
-
   // ---- down: blocks of R output columns, block `number` for this workgroup (and, were there more blocks than workgroups,
-  // every gridDim.x-th from there): no other workgroup needs them, so they may wait for one that starts late ----
-  const int R = min(32, (((p.d + (int)gridDim.x - 1) / (int)gridDim.x) + 3) & ~3);
+  // every grid-th from there): no other workgroup needs them, so they may wait for one that starts late ----
+  const int number = (int)blockIdx.x;
+  const int R = min(32, (((p.d + grid - 1) / grid) + 3) & ~3);
   const int blocks = (p.d + R - 1) / R;
   const int slices = (nb2 + kNW - 1) / kNW;                  // units of an expert
   const int units = A * slices;
@@ -654,18 +650,15 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     return up_place(expert(a), id - a * nt);
   };
   const bool deep = p.ahead > 2;  // the ring reaches into the tile after next
-  int q0 = first, q1 = tile_of(ticket + 1), q2 = deep ? tile_of(ticket + 2) : tiles;
-  if (q1 >= tiles) {  // those that exist come first
-    q1 = q2;
-    q2 = tiles;
-  }
-  if (q0 >= tiles) {
-    q0 = q1;
-    q1 = q2;
-    q2 = tiles;
-  }
-  int last = ticket + p.ahead - 1;                               // the latest ticket
-  const int no_more = max(tiles, p.ahead * (int)gridDim.x);      // from here on tickets name no tile
+  const int base = p.ahead * grid;  // from here on tiles are taken one at a time
+  int q0, q1, q2;
+  auto set_batch = [&](int v) __attribute__((always_inline)) {
+    q0 = v < grid ? v : tiles;
+    q1 = v < grid ? grid + v : tiles;
+    q2 = v < grid && deep ? 2 * grid + v : tiles;
+  };
+  set_batch(batch);
+  bool drained = tiles <= base;  // no tile is left but in others' batches
   Place p0 = place_of(q0), p1 = place_of(q1), p2 = place_of(q2);
   // The step `ahead` of tile q0's first one.  Past the last taken tile a step of the one at work again (it is in L2; the number in
   // flight stays): the down projection's weights would delay this workgroup's stores of h, which everyone waits for.
@@ -695,22 +688,52 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   for (; loaded < D; ++loaded) load_ahead(loaded, loaded);
 
   int buf = 0, mine = 0, taken = 0;
-  bool asked = (deep ? q2 : q1) < tiles && last < no_more;  // a ticket is on the way
-  if (asked && tid == 0) taken = take(next_tile);
+  bool asked = (deep ? q2 : q1) < tiles && !drained;  // a tile's number is on the way
+  if (asked && tid == 0) taken = base + take(next_tile);
   for (;;) {
     if (q0 >= tiles) {
-      // Nothing left of what was taken.  Unless the latest ticket was past the end there may be tiles of workgroups that have
-      // not started, which may not start before this one ends: take them, one at a time.
-      if (last >= no_more) break;
-      if (tid == 0) s_ctl[3] = take(next_tile);
+      // Nothing left of what was taken.  Tiles may be left that workgroups would take which have not started, and may not start
+      // before this one ends: take those.  (Counts only rise: a class that has given out its batches by now has none later.)
+      uint32_t given = 0;
+      const int ours = min(grid, tiles) - lane + kClasses - 1;  // batches of class `lane`, times kClasses
+      if (wave == 0 && lane < kClasses) given = __hip_atomic_load(classes + lane * 32, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      // This workgroup's h is in memory, past the XCD's L2, before it is counted: its stores went through and are waited for.
+      // (A release fence would write the whole L2 back, one workgroup after the other: 13 us.)
+      if (wave < kJoiners) wait_vm<0>();
+      if (wave == 0) {
+        const uint64_t left = __ballot(lane < kClasses && (int)given < ours / kClasses);
+        if (lane == 0) {  // nothing; or a batch; or, from `grid` on, a tile taken alone
+          int v = -1;
+          if (!drained) v = grid + base + take(next_tile);
+          else if (left != 0) v = claim(__builtin_ctzll(left));
+          s_ctl[3] = v;
+        }
+      }
       lds_barrier();
-      last = __builtin_amdgcn_readfirstlane(s_ctl[3]);
-      lds_barrier();
-      q0 = last < no_more ? tile_of(last) : tiles;
+      const int v = __builtin_amdgcn_readfirstlane(s_ctl[3]);
+      // The last workgroup raises the flags, each for few enough that their reads do not hold it up (of one word, read by
+      // everyone, the news took 6 us).
+      if (wave == 0 && mine > 0) {
+        uint32_t before = 0;
+        if (lane == 0) before = __hip_atomic_fetch_add(done, (uint32_t)mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+        if ((int)__builtin_amdgcn_readfirstlane(before) + mine == tiles && lane < kFlags)
+          __hip_atomic_store(flags + lane * 32, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      }
+      mine = 0;
+      if (v < 0) break;
+      lds_barrier();  // everyone has read what was taken
+      if (drained) {
+        set_batch(v);
+      } else {
+        q0 = v - grid;
+        q1 = q2 = tiles;
+        drained = q0 >= tiles;
+      }
+      asked = false;
       if (q0 >= tiles) continue;
       p0 = place_of(q0);
-      q1 = q2 = tiles;
-      asked = false;
+      p1 = place_of(q1);
+      p2 = place_of(q2);
       wait_vm<0>();  // start over with an empty ring
       slot = 0;
 #pragma unroll 1
@@ -754,12 +777,12 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     s_red[buf][wave][lane] = acc;
     if (asked && tid == 0) s_ctl[buf] = taken;
     lds_barrier();
-    if (asked) last = __builtin_amdgcn_readfirstlane(s_ctl[buf]);
-    const int next = asked && last < no_more ? tile_of(last) : tiles;
+    const int next = asked ? __builtin_amdgcn_readfirstlane(s_ctl[buf]) : tiles;
+    drained = drained || (asked && next >= tiles);
     // The tile after the ones that are known by now is asked for here, where only the first wave will wait for the answer
     // (at the end of the next tile), not the others' loads.
-    asked = next < tiles && last < no_more;
-    if (asked && tid == 0) taken = take(next_tile);
+    asked = next < tiles;
+    if (asked && tid == 0) taken = base + take(next_tile);
     if (wave < kJoiners) {  // the waves' sums in wave order, SwiGLU, h
       const int t = tid >> 3, c = tid & 7;
       const uint32_t at = red_at + buf * (kNW * 1024) + (t + 16 * (c >> 2)) * 16 + (c & 3) * 4;
@@ -789,20 +812,6 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     buf ^= 1;
     ++mine;
   }
-  if (mine > 0) {
-    // This workgroup's h is in memory, past the XCD's L2, before it is counted: its stores went through and are waited for.
-    // (A release fence would write the whole L2 back, one workgroup after the other: 13 us.)
-    if (wave < kJoiners) wait_vm<0>();
-    lds_barrier();
-    // The last one raises the flags, each for few enough that their reads do not hold it up (of one word, read by everyone,
-    // the news took 6 us).
-    if (wave == 0) {
-      uint32_t before = 0;
-      if (lane == 0) before = __hip_atomic_fetch_add(done, (uint32_t)mine, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if ((int)__builtin_amdgcn_readfirstlane(before) + mine == tiles && lane < kFlags)
-        __hip_atomic_store(p.counters + (3 + lane) * 32, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-  }
   // the down projection's first weights, while the others finish
   wait_vm<0>();
   slot = 0;
@@ -815,7 +824,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     if (block == number) {
       if (tid == 0) {
         const uint64_t t0 = wall_clock64();
-        const uint32_t* const flag = p.counters + (3 + number % kFlags) * 32;
+        const uint32_t* const flag = flags + number % kFlags * 32;
         while (__hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) {
           __builtin_amdgcn_s_sleep(4);
           if (wall_clock64() - t0 > kWaitTicks) {
