@@ -7,8 +7,7 @@
 // (one token: 9 experts of 257) and everything else is latency: launches, the first loads, the hand-over of h.
 //
 //  1. decode_rows_kernel: a workgroup for up to four tokens and as many routed experts normalises its tokens (they are a few KB
-//     in L2, so that is done once per expert), writes its share of them as bf16 and sums its experts' logits in fp64 (bf16
-//     products are exact in fp32).
+//     in L2, so that is done once per expert), writes its share of them as bf16 and sums its experts' logits in fp64.
 //  2. decode_experts_kernel: one workgroup of 8 waves per CU.  Each selects the tokens' experts from the affinities by itself
 //     (4 us for one token, while its first weights are on the way), then takes tiles of 8 gate rows and their 8 up rows of the
 //     active experts, and then a block of output columns, which it sums over all experts: no atomics on values, no partial
@@ -120,7 +119,8 @@ __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(RowsArgs p) {
   __shared__ double s_sums[NORM ? W : 1][2 * G];
   __shared__ double s_stat[NORM ? G : 1][2];
   __shared__ double s_part[2][W][G];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, c = tid * 8;
+  const int tid = threadIdx.x, lane = tid & 63, wave = __builtin_amdgcn_readfirstlane(tid >> 6), c = tid * 8;
+  const bool busy = wave * 512 < p.d;  // a wave without inputs leaves the arithmetic to the others
   const int e0 = blockIdx.x * p.experts, e1 = min(e0 + p.experts, p.N);
   const int t0 = blockIdx.y * G, nt = min(G, p.T - t0);
   const bool in = c < p.d;
@@ -153,14 +153,16 @@ __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(RowsArgs p) {
                            : p.x_dtype == ROW_F32   ? (double)*(const float*)row
                                                     : (double)bf16_to_f32(*(const uint16_t*)row);
       double s1 = 0.0, s2 = 0.0;
+      if (busy) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        const double v = in ? (double)f[i][q] - pivot : 0.0;
-        s1 += v;
-        s2 = fma(v, v, s2);
+        for (int q = 0; q < 8; ++q) {
+          const double v = in ? (double)f[i][q] - pivot : 0.0;
+          s1 += v;
+          s2 = fma(v, v, s2);
+        }
+        if (p.norm == MOE_NORM_LAYER) s1 = wave_sum64(s1);
+        s2 = wave_sum64(s2);
       }
-      if (p.norm == MOE_NORM_LAYER) s1 = wave_sum64(s1);
-      s2 = wave_sum64(s2);
       if (lane == 0) {
         s_sums[wave][2 * i] = s1;
         s_sums[wave][2 * i + 1] = s2;
@@ -187,7 +189,7 @@ __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(RowsArgs p) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < G; ++i) {
-      if (i >= nt) break;
+      if (i >= nt || !busy) break;
       const double mean = s_stat[i][0], rstd = s_stat[i][1];
       float y[8];
 #pragma unroll
@@ -197,18 +199,28 @@ __global__ __launch_bounds__(kRowThreads) void decode_rows_kernel(RowsArgs p) {
       unpack_bf16x8(o, f[i]);
     }
   }
+  double x[G][8];
+#pragma unroll
+  for (int i = 0; i < G; ++i)
+#pragma unroll
+    for (int q = 0; q < 8; ++q) x[i][q] = in ? (double)f[i][q] : 0.0;
   for (int e = e0; e < e1; ++e) {
     float w[8];
     unpack_bf16x8(wv, w);
+    double wd[8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) wd[q] = in ? (double)w[q] : 0.0;
     if (in && e + 1 < e1) wv = *(const u32x4*)(p.wr + (int64_t)(e + 1) * p.d + c);
     double(*const part)[G] = s_part[e & 1];  // two in turn: a barrier lies between a sum's last reader and its next writer
 #pragma unroll
     for (int i = 0; i < G; ++i) {
       if (i >= nt) break;
       double acc = 0.0;
+      if (busy) {
 #pragma unroll
-      for (int q = 0; q < 8; ++q) acc += in ? (double)(f[i][q] * w[q]) : 0.0;  // bf16 products are exact in fp32
-      acc = wave_sum64(acc);
+        for (int q = 0; q < 8; ++q) acc = fma(x[i][q], wd[q], acc);
+        acc = wave_sum64(acc);
+      }
       if (lane == 0) part[wave][i] = acc;
     }
     __syncthreads();
