@@ -246,6 +246,7 @@ struct ExpertArgs {
   uint32_t* counters;
   uint16_t* h;  // [T][K + n_shared][inter], upper and lower parts one after the other
   int ahead;    // tiles a workgroup holds: the one at work and those that its ring reaches into
+  int lists;    // batches of `ahead` tiles that are dealt out: one to a workgroup, and more where some never start
   const uint8_t* w13;
   const uint8_t* s13;
   const uint8_t* w2;
@@ -354,7 +355,7 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   uint32_t* const done = p.counters + 32;
   uint32_t* const flags = p.counters + 2 * 32;
   uint32_t* const classes = flags + kFlags * 32;
-  const int grid = (int)gridDim.x;
+  const int grid = p.lists;
   uint32_t in_vgpr = 0;  // of a uniform address the compiler combines the wave's additions, and waits for the sum at once
   asm volatile("" : "+v"(in_vgpr));
   auto take = [&](uint32_t* counter) __attribute__((always_inline)) {
@@ -525,7 +526,8 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
   // ---- down: blocks of R output columns, block `number` for this workgroup (and, were there more blocks than workgroups,
   // every grid-th from there): no other workgroup needs them, so they may wait for one that starts late ----
   const int number = (int)blockIdx.x;
-  const int R = min(32, (((p.d + grid - 1) / grid) + 3) & ~3);
+  const int columns = (p.d + (int)gridDim.x - 1) / (int)gridDim.x;
+  const int R = min(32, (columns + 3) & ~3);
   const int blocks = (p.d + R - 1) / R;
   const int slices = (nb2 + kNW - 1) / kNW;                  // units of an expert
   const int units = A * slices;
@@ -1013,8 +1015,10 @@ extern "C" size_t moe_decode_workspace_size(int T, int d, int inter, int n_exper
   return moe::decode_ws(T, d, inter, n_shared, top_k).total;
 }
 
-extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
-  using namespace moe;
+namespace moe {
+namespace {
+
+moe_status decode(const moe_decode_desc* q, int workgroups, int lists, hipStream_t stream) {
   clear_error();
   MOE_REQUIRE(q != nullptr, MOE_ERR_NULL, "moe_decode: desc is NULL");
   MOE_REQUIRE(q->T >= 0 && q->T <= kMaxT, MOE_ERR_SHAPE, "moe_decode: T=%d must be in [0, %d]", q->T, kMaxT);
@@ -1138,13 +1142,32 @@ extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
   const int block = fmt == W_BF16 ? 64 : fmt == W_FP4 ? 256 : 128, depth = fmt == W_FP4 ? Fmt<W_FP4>::kDepth : Fmt<W_BF16>::kDepth;
   const int per_wave = ((q->d + block - 1) / block + kNW - 1) / kNW;
   a.ahead = per_wave < depth ? 3 : 2;
-  const int grid = compute_units();
+  a.lists = lists;
   switch (fmt) {
-    case W_BF16: launch_experts<W_BF16>(a, grid, stream); break;
-    case W_E4M3: launch_experts<W_E4M3>(a, grid, stream); break;
-    case W_E4M3_E8M0: launch_experts<W_E4M3_E8M0>(a, grid, stream); break;
-    case W_I8: launch_experts<W_I8>(a, grid, stream); break;
-    default: launch_experts<W_FP4>(a, grid, stream); break;
+    case W_BF16: launch_experts<W_BF16>(a, workgroups, stream); break;
+    case W_E4M3: launch_experts<W_E4M3>(a, workgroups, stream); break;
+    case W_E4M3_E8M0: launch_experts<W_E4M3_E8M0>(a, workgroups, stream); break;
+    case W_I8: launch_experts<W_I8>(a, workgroups, stream); break;
+    default: launch_experts<W_FP4>(a, workgroups, stream); break;
   }
   return check_launch("moe_decode");
+}
+
+}  // namespace
+}  // namespace moe
+
+extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
+  const int cus = moe::compute_units();
+  return moe::decode(q, cus, cus, stream);
+}
+
+// For the tests, not in moe.h: moe_decode as a smaller or a busy device runs it.  `workgroups` of the second launch start, and tiles
+// are dealt out as for `lists` of them, so that those which start take over the rest; they also walk more than one block of columns
+// each, where moe_decode's workgroups have one at most on 256 CUs.
+extern "C" moe_status moe_decode_shaped(const moe_decode_desc* q, int workgroups, int lists, hipStream_t stream) {
+  using namespace moe;
+  clear_error();
+  MOE_REQUIRE(workgroups >= 1 && workgroups <= lists && lists <= 1024, MOE_ERR_SHAPE,
+              "moe_decode_shaped: workgroups=%d must be in [1, lists=%d], lists at most 1024", workgroups, lists);
+  return decode(q, workgroups, lists, stream);
 }
