@@ -682,7 +682,10 @@ typedef struct {
  * (T * (top_k + n_shared) * inter * 4 bytes) < 4 GiB.  T = 0 writes zero counts only.  Rows of out past T are
  * not touched.
  * The second launch's workgroups wait for each other's parts of h; none waits for a workgroup that has not
- * started, and the wait ends by itself after seconds (NaN rows) should the workspace be overwritten meanwhile. */
+ * started.  The wait ends by itself after 2^22 looks (seconds of running; time that the queue is switched out does
+ * not count), which only a workspace that is overwritten meanwhile should bring about.  The status is MOE_OK by
+ * then: a workgroup that gave up writes NaN to its own columns (4 to 32 neighbouring ones of every token), and the
+ * others' may be right. */
 size_t moe_decode_workspace_size(int T, int d, int inter, int n_experts, int n_shared, int top_k);
 moe_status moe_decode(const moe_decode_desc* desc, hipStream_t stream);
 

@@ -50,7 +50,9 @@ constexpr int kNW = 8;            // waves of a workgroup
 constexpr int kMaxActive = 257;
 constexpr int kJoiners = 2;       // waves that add the waves' sums: a token's 8 columns of a tile to 8 lanes
 constexpr int kRowThreads = 1024;
-constexpr uint64_t kWaitTicks = 500000000ull;  // 5 s of the 100 MHz clock: bound of the wait for h
+// Bound of the wait for h, in looks at its flag (each a sleep of 256 clocks and a load past the caches: seconds).  Looks and not time,
+// which goes on while a queue that was switched out cannot look.
+constexpr int kWaitLooks = 1 << 22;
 
 // Workspace: counters, affinities, normalised rows, h.
 constexpr int kFlags = 16;    // "h is complete", for a workgroup in 16 each
@@ -247,6 +249,7 @@ struct ExpertArgs {
   uint16_t* h;  // [T][K + n_shared][inter], upper and lower parts one after the other
   int ahead;    // tiles a workgroup holds: the one at work and those that its ring reaches into
   int lists;    // batches of `ahead` tiles that are dealt out: one to a workgroup, and more where some never start
+  int looks;    // bound of the wait for h
   const uint8_t* w13;
   const uint8_t* s13;
   const uint8_t* w2;
@@ -837,15 +840,13 @@ __global__ __launch_bounds__(kNW * 64, 2) void decode_experts_kernel(ExpertArgs 
     const int c0 = block * R, cols = min(R, p.d - c0);
     if (block == number) {
       if (tid == 0) {
-        const uint64_t t0 = wall_clock64();
         const uint32_t* const flag = flags + number % kFlags * 32;
-        while (__hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) {
+        int left = p.looks;
+        while (left > 0 && __hip_atomic_load(flag, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == 0) {
           __builtin_amdgcn_s_sleep(4);
-          if (wall_clock64() - t0 > kWaitTicks) {
-            s_ctl[2] = 1;
-            break;
-          }
+          --left;
         }
+        if (left <= 0) s_ctl[2] = 1;
       }
       // one wave's acquire clears what L1 and L2 hold for the others too (by all waves of all workgroups: 13 us)
       if (wave == 0) __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
@@ -1018,7 +1019,7 @@ extern "C" size_t moe_decode_workspace_size(int T, int d, int inter, int n_exper
 namespace moe {
 namespace {
 
-moe_status decode(const moe_decode_desc* q, int workgroups, int lists, hipStream_t stream) {
+moe_status decode(const moe_decode_desc* q, int workgroups, int lists, int looks, hipStream_t stream) {
   clear_error();
   MOE_REQUIRE(q != nullptr, MOE_ERR_NULL, "moe_decode: desc is NULL");
   MOE_REQUIRE(q->T >= 0 && q->T <= kMaxT, MOE_ERR_SHAPE, "moe_decode: T=%d must be in [0, %d]", q->T, kMaxT);
@@ -1143,6 +1144,7 @@ moe_status decode(const moe_decode_desc* q, int workgroups, int lists, hipStream
   const int per_wave = ((q->d + block - 1) / block + kNW - 1) / kNW;
   a.ahead = per_wave < depth ? 3 : 2;
   a.lists = lists;
+  a.looks = looks;
   switch (fmt) {
     case W_BF16: launch_experts<W_BF16>(a, workgroups, stream); break;
     case W_E4M3: launch_experts<W_E4M3>(a, workgroups, stream); break;
@@ -1158,16 +1160,17 @@ moe_status decode(const moe_decode_desc* q, int workgroups, int lists, hipStream
 
 extern "C" moe_status moe_decode(const moe_decode_desc* q, hipStream_t stream) {
   const int cus = moe::compute_units();
-  return moe::decode(q, cus, cus, stream);
+  return moe::decode(q, cus, cus, moe::kWaitLooks, stream);
 }
 
 // For the tests, not in moe.h: moe_decode as a smaller or a busy device runs it.  `workgroups` of the second launch start, and tiles
 // are dealt out as for `lists` of them, so that those which start take over the rest; they also walk more than one block of columns
-// each, where moe_decode's workgroups have one at most on 256 CUs.
-extern "C" moe_status moe_decode_shaped(const moe_decode_desc* q, int workgroups, int lists, hipStream_t stream) {
+// each, where moe_decode's workgroups have one at most on 256 CUs.  Each gives up waiting for h after `looks` at its flag (0: none).
+extern "C" moe_status moe_decode_shaped(const moe_decode_desc* q, int workgroups, int lists, int looks, hipStream_t stream) {
   using namespace moe;
   clear_error();
   MOE_REQUIRE(workgroups >= 1 && workgroups <= lists && lists <= 1024, MOE_ERR_SHAPE,
               "moe_decode_shaped: workgroups=%d must be in [1, lists=%d], lists at most 1024", workgroups, lists);
-  return decode(q, workgroups, lists, stream);
+  MOE_REQUIRE(looks >= 0 && looks <= kWaitLooks, MOE_ERR_SHAPE, "moe_decode_shaped: looks=%d must be in [0, %d]", looks, kWaitLooks);
+  return decode(q, workgroups, lists, looks, stream);
 }
