@@ -573,8 +573,8 @@ moe_status moe_w4_gemm_bounded(const moe_w4_desc* desc, int64_t sorted_rows, int
  * channel for weights.
  *
  * Format: codes int8 [rows, cols] in [-127, 127] and scale f32 [rows]; value = code * scale.  For a row
- * of x with A = max(max |x|, 127 * 2^-126): scale = fl32(A / 127), code = RNE(127 x / A).  A row that
- * holds an infinity or NaN has the scale NaN and codes 0.
+ * of x with A = max(max |x|, 127 * 2^-126): scale = fl32(A / 127), code = RNE(127 x / A) of the exact
+ * quotient, for bf16 and f32 alike.  A row that holds an infinity or NaN has the scale NaN and codes 0.
  * ==================================================================================== */
 
 /* i8_quant -- x (device bf16 or f32 [rows, cols], leading dimension ldx) -> codes (contiguous) and

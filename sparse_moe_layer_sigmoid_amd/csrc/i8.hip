@@ -23,16 +23,31 @@ constexpr float kLeast = 127.0f * 1.17549435e-38f;  // 127 * 2^-126: below it a 
 // ---- rows to codes ----
 
 // 8 values -> codes RNE(127 v / A).  Values and A go times 2^-e, e the exponent of A, so that 127 v stays in range (exact but
-// for values that round to code 0 anyway); the quotient of bf16 values by their maximum is at a midpoint or at least 1/510
-// away from one, so the corrected reciprocal gives the codes of an exact division.
+// for values that round to code 0 anyway).  Of bf16 values 127 v is exact, and a quotient that is not at a midpoint is further from
+// it than the quotient's own rounding (254 v and (2 c + 1) A have 16 bits each): the corrected reciprocal gives the codes of an exact
+// division.  Of f32 values 127 v and the quotient are each off by 2^-24 of themselves, together by less than 2^-16: where a
+// midpoint is that near (a value in 32 thousand), the remainder decides, exact in 64 bits, for v and A are multiples of 2^-33 there.
+template <int DT>
 __device__ __forceinline__ u32x2 i8_encode8(const float f[8], int e, float a, float ra) {
   u32x2 q = {0u, 0u};
+  float v[8], c[8], off = 0.f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
-    const float v = 127.0f * ldexpf(f[i], -e);
-    const int c = (int)__builtin_rintf(quotient(v, a, ra));
-    q[i / 4] |= ((uint32_t)c & 255u) << (8 * (i & 3));
+    v[i] = ldexpf(f[i], -e);
+    const float t = quotient(127.0f * v[i], a, ra);
+    c[i] = __builtin_rintf(t);
+    if constexpr (DT == ROW_F32) off = fmaxf(off, fabsf(t - c[i]));
   }
+  if (DT == ROW_F32 && off >= 0.5f - 0x1p-16f) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const double rest = fma((double)-c[i], (double)a, 127.0 * (double)v[i]), half = 0.5 * (double)a;
+      const bool odd = ((int)c[i] & 1) != 0;
+      if (fabs(rest) > half || (fabs(rest) == half && odd)) c[i] += rest > 0.0 ? 1.0f : -1.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i / 4] |= ((uint32_t)(int)c[i] & 255u) << (8 * (i & 3));
   return q;
 }
 
@@ -82,7 +97,7 @@ __global__ __launch_bounds__(L < 256 ? 256 : L) void i8_quant_kernel(const void*
   auto put = [&](const Raw8<DT>& w, int c) __attribute__((always_inline)) {
     float f[8];
     values8(w, f);
-    const u32x2 code = i8_encode8(f, e, a, ra);
+    const u32x2 code = i8_encode8<DT>(f, e, a, ra);
     if (c < cols) store_codes8<false>(out, c, cols, bad ? u32x2{0u, 0u} : code);
   };
   if constexpr (CH > 0) {
