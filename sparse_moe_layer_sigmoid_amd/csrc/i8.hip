@@ -187,12 +187,13 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   constexpr int OC = SWIGLU ? BN / 2 : BN;
   constexpr int SC = BM + BN;  // scales of a tile
   static_assert(A_PW * NW * 8 == BM && B_PW * NW * 8 == BN, "loads split evenly over the waves");
+  static_assert(SC % 4 == 0 && BM % 4 == 0, "a tile's scales and its column scales begin at 16 bytes");
   static_assert(SC / 64 <= NW, "one load of scales per wave at most");
   static_assert(!SWIGLU || TN % 2 == 0, "a wave holds gate columns and their up columns");
   __shared__ __attribute__((aligned(1024))) uint8_t slot0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t slot1[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t slot2[STAGE];
-  __shared__ float s_scale[STAGES][SC];  // row scales, then column scales; loads are up to two tiles ahead
+  __shared__ __attribute__((aligned(16))) float s_scale[STAGES][SC];  // read four at a time: row scales, then column scales; loads are up to two tiles ahead
   __shared__ int s_tstart[kMaxRowGroups + 1], s_off[kMaxRowGroups + 1];
   __shared__ int s_rows[NW][64], s_srows[BM / 64][64];  // row numbers of the next tile: of a wave's loads, and of scales
   const int tid = threadIdx.x, lane = tid & 63;
