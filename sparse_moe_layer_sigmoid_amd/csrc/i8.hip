@@ -53,7 +53,7 @@ __device__ __forceinline__ u32x2 i8_encode8(const float f[8], int e, float a, fl
 
 // A row by L lanes (64: a wave of a workgroup of four; else the whole workgroup), CH chunks of 8 elements in each lane's
 // registers: one read of the row.  CH = 0: any width, the row read twice.
-template <int DT, int L, int CH, bool FULL>
+template <int DT, int L, int CH>
 __global__ __launch_bounds__(L < 256 ? 256 : L) void i8_quant_kernel(const void* __restrict__ x, int64_t ldx_b, int64_t rows,
                                                                      int cols, int8_t* __restrict__ q,
                                                                      float* __restrict__ scale) {
@@ -507,8 +507,7 @@ void dispatch_gemm(const I8Args& a, int64_t m_total, hipStream_t stream) {
 template <int DT, int L, int CH>
 void launch_quant(const void* x, int64_t ldx_b, int64_t rows, int cols, int8_t* q, float* scale, hipStream_t stream) {
   constexpr int PER = L < 256 ? 256 / L : 1;
-  i8_quant_kernel<DT, L, CH, false><<<(unsigned)((rows + PER - 1) / PER), L < 256 ? 256 : L, 0, stream>>>(x, ldx_b, rows, cols, q,
-                                                                                                     scale);
+  i8_quant_kernel<DT, L, CH><<<(unsigned)((rows + PER - 1) / PER), L < 256 ? 256 : L, 0, stream>>>(x, ldx_b, rows, cols, q, scale);
 }
 
 template <int DT>
