@@ -14,6 +14,8 @@ void set_error(const char* fmt, ...) __attribute__((format(printf, 1, 2)));
 void clear_error();
 
 inline bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+// n a power of two
+inline bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
 
 // Report a launch error (if any) of the kernels just enqueued.
 moe_status check_launch(const char* what);

@@ -264,18 +264,6 @@ struct ExpertArgs {
 
 typedef __attribute__((address_space(3))) void lds_void;
 
-template <int N>
-__device__ __forceinline__ void wait_vm() {  // at most N of the newest vector-memory operations in flight
-  static_assert(N >= 0 && N <= 63, "six bits");
-  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
-}
-// Workgroup barrier that waits for this wave's LDS operations but not for its loads in flight.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // 16 or 4 bytes per lane from base + v + off (v per lane, base and off uniform) to LDS at dst, lane after lane.  (The host
 // pass does not know the builtin.)
 __device__ __forceinline__ void load16_to_lds(const uint8_t* base, uint32_t v, uint32_t off, uint8_t* dst) {
@@ -301,8 +289,6 @@ __device__ __forceinline__ u32x4 load16_if(const void* base, uint32_t bytes, uin
   return u32x4{v, off, bytes, 0u};
 #endif
 }
-
-__device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
 
 template <int FMT, bool WIDE = false>
 struct Fmt {
@@ -1003,8 +989,6 @@ void launch_experts(const ExpertArgs& a, int grid, hipStream_t stream) {
   if (a.T > 8) decode_experts_kernel<FMT, true><<<grid, kNW * 64, 0, stream>>>(a);
   else decode_experts_kernel<FMT, false><<<grid, kNW * 64, 0, stream>>>(a);
 }
-
-bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
 
 }  // namespace
 }  // namespace moe

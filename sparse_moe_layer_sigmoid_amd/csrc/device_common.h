@@ -83,6 +83,20 @@ __device__ __forceinline__ int e8m0_exponent(float amax) {
 // 2^k as a float for k in [-126, 127] (exact).
 __device__ __forceinline__ float pow2f(int k) { return __uint_as_float((uint32_t)(k + 127) << 23); }
 
+__device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+
+template <int N>
+__device__ __forceinline__ void wait_vm() {  // at most N of the newest vector-memory operations in flight
+  static_assert(N >= 0 && N <= 63, "six bits");
+  __builtin_amdgcn_s_waitcnt((N & 15) | (7 << 4) | (15 << 8) | ((N >> 4) << 14));
+}
+// Workgroup barrier that waits for this wave's LDS operations but not for its loads in flight.
+__device__ __forceinline__ void lds_barrier() {
+  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
 // Matrix-core wrappers (gfx950).
 __device__ __forceinline__ f32x4 mfma_bf16(const bf16x8_t& a, const bf16x8_t& b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);

@@ -108,8 +108,6 @@ struct GemmArgs {
   int64_t ldo_pre_b;      // bytes per out_pre row
 };
 
-__device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
-
 struct TileInfo {
   int g;      // group index relative to first_group
   int nt;     // column block

@@ -127,7 +127,6 @@ __global__ __launch_bounds__(256) void i8_dequant_kernel(const int8_t* __restric
 
 // ---- products ----
 
-#define I8_WAIT_VM(n) __builtin_amdgcn_s_waitcnt(((n) & 15) | (7 << 4) | (15 << 8) | (((n) >> 4) << 14))
 #define I8_BARRIER()                                                          \
   do {                                                                        \
     __builtin_amdgcn_s_waitcnt((15) | (7 << 4) | (0 << 8) | (3 << 14));       \
@@ -160,8 +159,6 @@ struct I8Args {
   int64_t ldo_tail_b;
 };
 
-__device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
-
 struct Tile {
   int g, nt, row0, nrows;
 };
@@ -193,7 +190,8 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   __shared__ __attribute__((aligned(1024))) uint8_t slot0[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t slot1[STAGE];
   __shared__ __attribute__((aligned(1024))) uint8_t slot2[STAGE];
-  __shared__ __attribute__((aligned(16))) float s_scale[STAGES][SC];  // read four at a time: row scales, then column scales; loads are up to two tiles ahead
+  // row scales, then column scales, read four at a time; loads are up to two tiles ahead
+  __shared__ __attribute__((aligned(16))) float s_scale[STAGES][SC];
   __shared__ int s_tstart[kMaxRowGroups + 1], s_off[kMaxRowGroups + 1];
   __shared__ int s_rows[NW][64], s_srows[BM / 64][64];  // row numbers of the next tile: of a wave's loads, and of scales
   const int tid = threadIdx.x, lane = tid & 63;
@@ -336,10 +334,10 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
     issue_scales();
   };
   fetch_rows(ct);
-  I8_WAIT_VM(0);
+  wait_vm<0>();
   issue(std::integral_constant<int, 0>(), 0);
   issue(std::integral_constant<int, 1>(), 1);
-  if (ksteps == 2) I8_WAIT_VM(0);  // the second tile's rows
+  if (ksteps == 2) wait_vm<0>();  // the second tile's rows
   issue(std::integral_constant<int, 2>(), 2);
 
   // ---- products: weights first, so a lane's four results are four columns of one token row ----
@@ -451,14 +449,14 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
         __builtin_amdgcn_sched_barrier(0);
       }
   };
-  I8_WAIT_VM(2 * L_STAGE);
+  wait_vm<2 * L_STAGE>();
   I8_BARRIER();
 #pragma unroll
   for (int k = 0; k < TM + TN; ++k) read_one(std::integral_constant<int, 0>(), 0, k);
   auto step = [&](auto slot_c, int j) __attribute__((always_inline)) {
     constexpr auto next = std::integral_constant<int, (decltype(slot_c)::value + 1) % 3>();
     half_step(0, slot_c, slot_c, false);
-    I8_WAIT_VM(L_STAGE);
+    wait_vm<L_STAGE>();
     I8_BARRIER();
     issue_prep(j + 3);
     half_step(1, next, slot_c, true);
@@ -473,7 +471,7 @@ __global__ __launch_bounds__(WGM * WGN * 64) void i8_gemm_kernel(I8Args p) {
   }
   if (j < total_steps) step(std::integral_constant<int, 0>(), j);
   if (j + 1 < total_steps) step(std::integral_constant<int, 1>(), j + 1);
-  I8_WAIT_VM(0);  // the repeated loads land before the workgroup's LDS is given away
+  wait_vm<0>();  // the repeated loads land before the workgroup's LDS is given away
 }
 
 int compute_units() {
@@ -522,8 +520,6 @@ void dispatch_quant(const void* x, int64_t ldx, int64_t rows, int cols, int8_t* 
 }
 
 constexpr int kMaxQuantCols = 1 << 24;
-bool aligned_to(const void* p, int n) { return (reinterpret_cast<uintptr_t>(p) & (uintptr_t)(n - 1)) == 0; }
-
 }  // namespace
 }  // namespace moe
 

@@ -27,13 +27,13 @@
 
 #include "abi_common.h"
 #include "device_common.h"
+#include "group_rows.h"
 #include "rows_common.h"
 #include "weights.h"
 
 namespace moe {
 namespace {
 
-constexpr int kMaxGroups = 1024;
 constexpr int kGroup = 32;      // inputs per scale
 constexpr int kRowBlock = 32;   // token rows of a work item
 constexpr int kWaves = 4;
@@ -76,14 +76,8 @@ struct W4Args {
   int64_t lda_b;
   const uint8_t* q;
   const uint8_t* s;
-  const int32_t* offs;  // group_offsets + first_group
+  GroupRows rows;
   int first_group;
-  int n_groups;
-  // row counts, below 2^31 (an offset and a count add up in 32 bits): see row_limit
-  uint32_t m_total;
-  uint32_t sorted_rows;
-  uint32_t out_rows;
-  uint32_t tail_rows;
   int N;  // weight rows per group
   int K;
   int n_tiles;
@@ -91,33 +85,24 @@ struct W4Args {
   uint8_t* out;
   int out_dtype;
   int64_t ldo_b;
-  int tail_first;  // first group (relative) of the f32 tail output; n_groups if none
   uint8_t* out_tail;
   int64_t ldo_tail_b;
 };
 
-__device__ __forceinline__ float silu(float a) { return a * __builtin_amdgcn_rcpf(1.0f + __expf(-a)); }
+// Group offset i, held to the rows that the caller vouches for (limit: rows_end).
+__device__ __forceinline__ int group_offset(const W4Args& p, int limit, int i) { return min(p.rows.offs[i], limit); }
 
-// The sorted row from which nothing is read or written: the first one that the caller did not vouch for.  Where the
-// groups before the tail hold more rows than out does, that is the first row past out, and the tail is empty.
-__device__ __forceinline__ int row_limit(const W4Args& p) {
-  const uint32_t first = p.offs[0], tail = p.offs[p.tail_first];
-  const uint32_t room = tail - first > p.out_rows ? first + p.out_rows : tail + p.tail_rows;
-  return (int)min(min(first + p.m_total, p.sorted_rows), room);  // sorted_rows < 2^31
-}
-// Group offset i, held to that.
-__device__ __forceinline__ int group_offset(const W4Args& p, int limit, int i) { return min(p.offs[i], limit); }
-
-// Row blocks before each group (s_pre[g], of kMaxGroups + 1 entries) for row blocks of RB rows, built by a workgroup of THREADS lanes.
+// Row blocks before each group (s_pre[g], of kMaxRowGroups + 1 entries) for row blocks of RB rows, built by a workgroup of
+// THREADS lanes.
 template <int RB, int THREADS>
 __device__ __forceinline__ void row_block_prefix(const W4Args& p, int limit, int* s_pre, int* s_wsum) {
-  constexpr int PER = kMaxGroups / THREADS;
+  constexpr int PER = kMaxRowGroups / THREADS;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int c[PER], sum = 0;
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int g = tid * PER + j;
-    const int len = g < p.n_groups ? group_offset(p, limit, g + 1) - group_offset(p, limit, g) : 0;
+    const int len = g < p.rows.n_groups ? group_offset(p, limit, g + 1) - group_offset(p, limit, g) : 0;
     c[j] = (max(len, 0) + RB - 1) / RB;
     sum += c[j];
   }
@@ -136,7 +121,7 @@ __device__ __forceinline__ void row_block_prefix(const W4Args& p, int limit, int
     s_pre[tid * PER + j] = base;
     base += c[j];
   }
-  if (tid == THREADS - 1) s_pre[kMaxGroups] = base;
+  if (tid == THREADS - 1) s_pre[kMaxRowGroups] = base;
   __syncthreads();
 }
 
@@ -155,8 +140,8 @@ __device__ __forceinline__ int find_group(const int* s_pre, int n_groups, int64_
 __device__ __forceinline__ void store_columns(const W4Args& p, int limit, int g, int row, int base_row, int col, const f32x4& v) {
   const int left = p.out_cols - col;
   if (left <= 0) return;
-  const bool tail = g >= p.tail_first;
-  uint8_t* orow = tail ? p.out_tail + (int64_t)(row - group_offset(p, limit, p.tail_first)) * p.ldo_tail_b
+  const bool tail = g >= p.rows.tail_first;
+  uint8_t* orow = tail ? p.out_tail + (int64_t)(row - group_offset(p, limit, p.rows.tail_first)) * p.ldo_tail_b
                        : p.out + (int64_t)(row - base_row) * p.ldo_b;
   if (tail || p.out_dtype == ROW_F32) {
     float* o = reinterpret_cast<float*>(orow) + col;
@@ -177,13 +162,6 @@ __device__ __forceinline__ void store_columns(const W4Args& p, int limit, int g,
   }
 }
 
-// Workgroup barrier that waits for this wave's LDS operations but not for its loads in flight.
-__device__ __forceinline__ void lds_barrier() {
-  asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-}
-
 // The streaming kernel: K at most 128 * NW * KPW, N a multiple of 16.  A
 // workgroup walks weight tiles (16 rows; SwiGLU: 8 gate rows and their 8 up rows) against a block of
 // up to 16 token rows, whose values it holds in registers as matrix operands for as long as its
@@ -198,8 +176,8 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   constexpr int STRIDE = KPW * 64 + 16;      // bytes of a tile row in LDS, spread over the banks
   constexpr int SSTRIDE = SR * 4 + 1;        // dwords of a tile row's scales in LDS
   constexpr int THREADS = NW * 64;
-  __shared__ int s_off[kMaxGroups + 1];      // the groups' offsets
-  __shared__ int s_pre[kMaxGroups + 1];      // row blocks before each group
+  __shared__ int s_off[kMaxRowGroups + 1];      // the groups' offsets
+  __shared__ int s_pre[kMaxRowGroups + 1];      // row blocks before each group
   __shared__ int s_wsum[NW];
   __shared__ int s_first;
   __shared__ __attribute__((aligned(16))) uint8_t s_w[NW][16 * STRIDE];
@@ -208,7 +186,7 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int lr = lane & 15, lg = lane >> 4;
-  const int G = p.n_groups, n_tiles = p.n_tiles, limit = row_limit(p);
+  const int G = p.rows.n_groups, n_tiles = p.n_tiles, limit = rows_end(p.rows);
 
   // prefix of the groups' row blocks, `per` consecutive groups to a lane; the lane whose groups hold
   // the workgroup's first unit says which one
@@ -443,8 +421,8 @@ __global__ __launch_bounds__(NW * 64, 2) void w4_stream_kernel(W4Args p) {
       col = c.tile() * 8 + lg * 4;
     }
     if (!live) return;
-    const bool tail = c.g >= p.tail_first;
-    uint8_t* orow = tail ? p.out_tail + (int64_t)(row - s_off[p.tail_first]) * p.ldo_tail_b
+    const bool tail = c.g >= p.rows.tail_first;
+    uint8_t* orow = tail ? p.out_tail + (int64_t)(row - s_off[p.rows.tail_first]) * p.ldo_tail_b
                          : p.out + (int64_t)(row - base_row) * p.ldo_b;
     if (tail || p.out_dtype == ROW_F32) {
       *reinterpret_cast<f32x4_u*>(orow + col * 4) = v;
@@ -517,21 +495,21 @@ template <bool SWIGLU, int NT>
 __global__ __launch_bounds__(256, 4) void w4_gemm_kernel(W4Args p) {
   constexpr int BN = NT * 16;                   // weight rows per item
   constexpr int OC = SWIGLU ? BN / 2 : BN;      // output columns per item
-  __shared__ int s_pre[kMaxGroups + 1];         // row blocks before each group
+  __shared__ int s_pre[kMaxRowGroups + 1];         // row blocks before each group
   __shared__ int s_wsum[kWaves];
   __shared__ __attribute__((aligned(16))) float s_red[kWaves][16][BN + 4];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int lr = lane & 15, lg = lane >> 4;
 
-  const int limit = row_limit(p);
+  const int limit = rows_end(p.rows);
   row_block_prefix<kRowBlock, 256>(p, limit, s_pre, s_wsum);
-  const int64_t total = (int64_t)s_pre[kMaxGroups] * p.n_tiles;
-  const int base_row = p.offs[0];
+  const int64_t total = (int64_t)s_pre[kMaxRowGroups] * p.n_tiles;
+  const int base_row = p.rows.offs[0];
   const int kblocks = (p.K + 127) / 128;
   const uint32_t w_row_b = p.K / 2, s_row_b = p.K / kGroup;
 
   for (int64_t L = blockIdx.x; L < total; L += gridDim.x) {
-    const int g = find_group(s_pre, p.n_groups, p.n_tiles, L);
+    const int g = find_group(s_pre, p.rows.n_groups, p.n_tiles, L);
     const int blocks = s_pre[g + 1] - s_pre[g];
     const int local = (int)(L - (int64_t)s_pre[g] * p.n_tiles);
     const int nt = local / blocks, rb = local - nt * blocks;
@@ -705,8 +683,8 @@ extern "C" moe_status moe_w4_gemm_bounded(const moe_w4_desc* d, int64_t sorted_r
   MOE_REQUIRE(d->out_dtype == MOE_BF16 || d->out_dtype == MOE_F32, MOE_ERR_DTYPE,
               "moe_w4_gemm: out_dtype must be MOE_BF16 or MOE_F32 (%d)", d->out_dtype);
   const bool swiglu = d->epilogue == MOE_EPI_SWIGLU;
-  MOE_REQUIRE(d->n_groups >= 1 && d->n_groups <= kMaxGroups && d->first_group >= 0, MOE_ERR_SHAPE,
-              "moe_w4_gemm: n_groups=%d (1..%d) first_group=%d", d->n_groups, kMaxGroups, d->first_group);
+  MOE_REQUIRE(d->n_groups >= 1 && d->n_groups <= kMaxRowGroups && d->first_group >= 0, MOE_ERR_SHAPE,
+              "moe_w4_gemm: n_groups=%d (1..%d) first_group=%d", d->n_groups, kMaxRowGroups, d->first_group);
   MOE_REQUIRE(d->m_total >= 0 && d->m_total < ((int64_t)1 << 31), MOE_ERR_SHAPE, "moe_w4_gemm: m_total=%lld",
               (long long)d->m_total);
   MOE_REQUIRE(sorted_rows >= 0 && out_rows >= 0 && tail_rows >= 0, MOE_ERR_SHAPE,
@@ -722,11 +700,11 @@ extern "C" moe_status moe_w4_gemm_bounded(const moe_w4_desc* d, int64_t sorted_r
   MOE_REQUIRE(d->lda >= d->K && d->lda % 8 == 0 && aligned16(d->a), MOE_ERR_ALIGN,
               "moe_w4_gemm: lda=%lld must be >= K, a multiple of 8, and a 16-byte aligned", (long long)d->lda);
   MOE_REQUIRE(aligned16(d->w_q), MOE_ERR_ALIGN, "moe_w4_gemm: w_q must be 16-byte aligned");
-  MOE_REQUIRE((d->ldo >= out_cols || d->tail_groups == d->n_groups) && (reinterpret_cast<uintptr_t>(d->out) & (uintptr_t)(osz - 1)) == 0, MOE_ERR_ALIGN,
+  MOE_REQUIRE((d->ldo >= out_cols || d->tail_groups == d->n_groups) && aligned_to(d->out, osz), MOE_ERR_ALIGN,
               "moe_w4_gemm: ldo=%lld must be >= %d and out aligned to its elements", (long long)d->ldo, out_cols);
   if (d->tail_groups > 0) {
     MOE_REQUIRE(d->m_total == 0 || sorted_rows == 0 || tail_rows == 0 || d->out_tail, MOE_ERR_NULL, "moe_w4_gemm: out_tail is NULL");
-    MOE_REQUIRE(d->ldo_tail >= out_cols && (reinterpret_cast<uintptr_t>(d->out_tail) & 3u) == 0, MOE_ERR_ALIGN,
+    MOE_REQUIRE(d->ldo_tail >= out_cols && aligned_to(d->out_tail, 4), MOE_ERR_ALIGN,
                 "moe_w4_gemm: ldo_tail=%lld must be >= %d and out_tail 4-byte aligned", (long long)d->ldo_tail, out_cols);
   }
   MOE_REQUIRE((int64_t)d->N * (d->K / 2) < ((int64_t)1 << 31), MOE_ERR_SHAPE, "moe_w4_gemm: one W[g] exceeds 2 GiB");
@@ -737,21 +715,20 @@ extern "C" moe_status moe_w4_gemm_bounded(const moe_w4_desc* d, int64_t sorted_r
   a.lda_b = d->lda * 2;
   a.q = d->w_q;
   a.s = d->w_scale;
-  a.offs = d->group_offsets + d->first_group;
+  a.rows.offs = d->group_offsets + d->first_group;
   a.first_group = d->first_group;
-  a.n_groups = d->n_groups;
-  const auto count = [](int64_t n) { return (uint32_t)(n < INT32_MAX ? n : INT32_MAX); };  // no offset is larger
-  a.m_total = count(d->m_total);
-  a.sorted_rows = count(sorted_rows);
-  a.out_rows = count(out_rows);
-  a.tail_rows = d->tail_groups > 0 ? count(tail_rows) : INT32_MAX;
+  a.rows.n_groups = d->n_groups;
+  a.rows.m_total = row_count(d->m_total);
+  a.rows.sorted_rows = row_count(sorted_rows);
+  a.rows.out_rows = row_count(out_rows);
+  a.rows.tail_rows = d->tail_groups > 0 ? row_count(tail_rows) : INT32_MAX;
   a.N = d->N;
   a.K = d->K;
   a.out_cols = out_cols;
   a.out = static_cast<uint8_t*>(d->out);
   a.out_dtype = d->out_dtype == MOE_F32 ? ROW_F32 : ROW_BF16;
   a.ldo_b = d->ldo * osz;
-  a.tail_first = d->n_groups - d->tail_groups;
+  a.rows.tail_first = d->n_groups - d->tail_groups;
   a.out_tail = static_cast<uint8_t*>(d->out_tail);
   a.ldo_tail_b = d->ldo_tail * 4;
   if (d->K <= 128 * kMaxStreamBlocks && d->N % 16 == 0 && aligned4(d->w_scale)) {
