@@ -496,8 +496,15 @@ void launch_gemm(I8Args a, int64_t m_total, hipStream_t stream) {
 template <bool SWIGLU>
 void dispatch_gemm(const I8Args& a, int64_t m_total, hipStream_t stream) {
   // By rows per expert: the low tile wastes fewer products where the weights' bytes are the time, the high one reads them fewer
-  // times.  257 experts, 2000 tokens of 8 (70 rows): gate/up 1.62 against 1.69 ms, down 0.90 against 0.93; 3000 (105 rows):
-  // 1.93 against 1.76 ms and 1.01 against 0.98.
+  // times.  257 experts of 7168 x 2048, 8 to a token, 64 against 192 rows, ms (gate/up, down):
+  //   even routing, 256 tokens (9 rows)     1.26 / 1.53, 0.66 / 0.78    2000 (70)  1.51 / 1.62, 0.85 / 0.88
+  //                                         3000 (105)  1.85 / 1.70, 0.98 / 0.93
+  //   popularity rank^-1.1, 256 tokens      1.15 / 1.41, 0.61 / 0.73    2000       1.61 / 1.81, 0.87 / 0.96
+  //                                         3000        1.88 / 1.99, 0.99 / 1.08
+  //   all tokens on the same 8, 256 tokens  0.13 / 0.11, 0.06 / 0.06    2000       0.74 / 0.51, 0.43 / 0.32
+  //                                         3000        0.96 / 0.75, 0.56 / 0.46
+  // The offsets are on the device, so the rule cannot see who is popular: skewed batches above 80 rows pay 6 to 10%, and a
+  // collapse onto few experts below 80 pays up to 45%.
   if (m_total / a.rows.n_groups < 80) launch_gemm<64, 256, 1, 8, SWIGLU>(a, m_total, stream);
   else launch_gemm<192, 192, 4, 2, SWIGLU>(a, m_total, stream);
 }

@@ -162,7 +162,13 @@ class MoELayer:
     def decode(self, x, out_dtype=torch.bfloat16, update_bias: bool = False, gamma: float = 0.001):
         """The forward for up to 16 tokens in two launches (moe_decode): x [T, d] bf16 (or f32 with a norm) -> out
         [T, d].  The same layer as forward on the same weights; its inner rows are not rounded on the way (forward
-        rounds h to bf16, and quantises x and h on the E4M3 and 8-bit integer paths)."""
+        rounds h to bf16, and quantises x and h on the E4M3 and 8-bit integer paths).  d may be at most 8192, and d
+        and I are multiples of 64 (bf16), 128 (4 bits, int8, E4M3) or 512 (E4M3 with E8M0 scales).
+
+        One token is faster than in forward (7168 x 2048: 147 us in bf16 against 207, 67 in 4 bits against 98), four
+        are in bf16, and in 8 bits from about 4096 inputs on (249 in E4M3 against 307; 4 bits: 189 against 187); sixteen
+        are in bf16 on wide layers alone (1442 against 1544; E4M3 805 against 799, 4 bits 617 against 448) and
+        slower on narrow ones (1024 x 512, 128 experts: 151 in bf16 against 103, 225 in 4 bits against 63)."""
         out, _, _, counts = L.moe_decode(x, self.w_router, self.bias, self.W13, self.W2, self.top_k, self.n_group,
                                          self.topk_group, self.W13_s, self.W2_s, self.norm, self.norm_weight, self.norm_bias,
                                          self.norm_eps, out_dtype)
